@@ -318,6 +318,139 @@ ocq_status ocq_set_fused_requant(int mode);
  * mode, which has no requantization), -1 before the first call. */
 int ocq_last_requant_in_gateup(void);
 
+/* ------------------------------------------------------------------------
+ * The operators around the block in a speculative-verify layer: the norm in
+ * front of it, rotary positions with the append to a paged cache, and the
+ * attention of each request's new tokens over that cache ("Generate more
+ * tokens per target pass" in the post: one verify pass over 1 + drafts tokens
+ * per request; full-attention layers with a KV cache, "Why decoding dominates
+ * latency").
+ *
+ * All are asynchronous on `stream`; tensors are bf16 with their last axis
+ * contiguous, pointers 16-byte aligned and strides (in elements) multiples of
+ * 8.  Sizes are checked on the host before any launch.  The contents of
+ * device index arrays are not read by the host: the kernels bound every index
+ * they form, so that wrong contents give wrong results, never an access
+ * outside the tensors described by the call. */
+
+/* Residual addition, RMSNorm and per-token E4M3 quantization in one pass:
+ *   h = x + residual (fp32; residual_dev NULL: h = x)
+ *   residual_out = bf16(h)
+ *   y = h / sqrt(mean(h^2) + eps) * weight (fp32, of the unrounded h)
+ *   scales = fl32(max|y| / 448), codes = E4M3(fl32(y / scale)); a zero row has
+ *   scale 0 and codes 0, a row whose squares do not sum to a finite fp32
+ *   number has scale NaN and codes 0.
+ * x_bf16_dev, residual_bf16_dev: [rows, hidden] with row strides x_stride and
+ * residual_stride; weight_bf16_dev [hidden]; residual_out_bf16_dev and
+ * y_bf16_dev: [rows, hidden] contiguous, each nullable; codes_dev (uint8
+ * [rows, hidden]) and scales_dev (float [rows]) both or neither; y or codes
+ * must be given.  residual_out may be x or residual itself where that is
+ * contiguous; any other overlap of an output with an input is not allowed.
+ * 0 <= rows <= 2^24 (0: nothing is done), hidden a multiple of 8 in
+ * [8, 65536], eps >= 0 and finite. */
+ocq_status ocq_add_rmsnorm(const void* x_bf16_dev, int64_t x_stride, const void* residual_bf16_dev,
+                           int64_t residual_stride, const void* weight_bf16_dev, float eps, int rows, int hidden,
+                           void* residual_out_bf16_dev, void* y_bf16_dev, void* codes_dev, void* scales_dev,
+                           void* stream);
+
+typedef enum {
+  OCQ_CACHE_BF16 = 0,   /* k, v bf16                                                   */
+  OCQ_CACHE_E4M3 = 1    /* k, v E4M3 codes, one fp32 scale (max / 448) per token and head */
+} ocq_cache_format;
+
+/* A paged cache of one layer.  k_dev, v_dev: [num_pages, kv_heads, page_size,
+ * head_dim] elements (bf16 or E4M3 codes) with the strides below, the same
+ * for k and v: any order of the first three axes.  Strides in elements; in
+ * bytes they are multiples of 16.  k_scale_dev, v_scale_dev: float
+ * [num_pages, kv_heads, page_size] with strides of their own (E4M3 only).
+ * page_size: a power of two up to 1024; head_dim 64, 128 or 256. */
+typedef struct {
+  void* k_dev;
+  void* v_dev;
+  void* k_scale_dev;
+  void* v_scale_dev;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+  int num_pages, page_size, kv_heads, head_dim;
+  int format;
+} ocq_kv_cache;
+
+/* The tokens of one step.  The new tokens of request r are rows q_start[r] ..
+ * q_start[r + 1] of the token axis (q_start[0] = 0, not falling, q_start
+ * [requests] = tokens; a request may have none), kv_lens[r] tokens of it are
+ * in the cache when these are in it, and place p of the request is row p %
+ * page_size of page page_table[r][p / page_size].  New token i of n stands at
+ * place kv_lens[r] - n + i.
+ * q_start_dev int32 [requests + 1], kv_lens_dev int32 [requests],
+ * page_table_dev int32 [requests, max_pages] with row stride table_stride.
+ * max_new, max_kv: host bounds of the new tokens and of kv_lens of any
+ * request.  Tokens past max_new of a request are not attended; max_kv only
+ * shapes the split of the work.  tokens * heads and max_pages * page_size
+ * stay below 2^31. */
+typedef struct {
+  const void* q_start_dev;
+  const void* kv_lens_dev;
+  const void* page_table_dev;
+  int64_t table_stride;
+  int requests, tokens, max_pages, max_new, max_kv;
+} ocq_token_batch;
+
+/* Rotary frequencies of rot dimensions (float64 [rot / 2] to inv_freq_out,
+ * and to multiplier_out the factor of cos and sin), by a published rule:
+ *   OCQ_ROPE_PLAIN   base^(-2 j / rot)
+ *   OCQ_ROPE_LINEAR  the same / factor (positions divided by the factor)
+ *   OCQ_ROPE_NTK     of the base base * factor^(rot / (rot - 2))
+ *   OCQ_ROPE_YARN    (YaRN) those that turn at least beta_fast times in
+ *                    context tokens as in PLAIN, at most beta_slow times as in
+ *                    LINEAR, a ramp over j between; multiplier 0.1 ln(factor) + 1
+ * factor >= 1, base > 1; context > 0 and beta_fast > beta_slow > 0 for YARN.
+ * rot: a multiple of 16 in [16, 256].  Host only. */
+typedef enum { OCQ_ROPE_PLAIN = 0, OCQ_ROPE_LINEAR = 1, OCQ_ROPE_NTK = 2, OCQ_ROPE_YARN = 3 } ocq_rope_scaling;
+ocq_status ocq_rope_frequencies(int rot, double base, int scaling, double factor, double context, double beta_fast,
+                                double beta_slow, double* inv_freq_out, float* multiplier_out);
+
+/* Rotate q and k and append k and v to the cache.
+ * q_dev [tokens, heads, head_dim], k_dev and v_dev [tokens, kv_heads,
+ * head_dim]: token and head strides as given (slices of one projection's
+ * output are fine).  inv_freq_dev: float64 [rot / 2]; rot a multiple of 16 up
+ * to head_dim, elements past rot are not turned.  interleaved 0: pairs (j, j +
+ * rot / 2); 1: pairs (2 j, 2 j + 1).  multiplier scales cos and sin.
+ * positions_dev: int32 [tokens] rotary positions, or NULL for each token's
+ * place in its request.  q_out_dev: [tokens, heads, head_dim] contiguous, or q
+ * itself where that is contiguous.
+ * bf16 caches receive bf16(k'), bf16(v); E4M3 caches the codes of the fp32 k'
+ * and of v and their scales.  A token whose place is outside [0, max_pages *
+ * page_size) or whose page is outside [0, num_pages) is not appended (its q is
+ * rotated all the same).  Two new tokens must not share a cache slot. */
+ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, const void* k_dev,
+                           int64_t k_token_stride, int64_t k_head_stride, const void* v_dev, int64_t v_token_stride,
+                           int64_t v_head_stride, int heads, const void* inv_freq_dev, int rot, int interleaved,
+                           float multiplier, const void* positions_dev, const ocq_kv_cache* cache,
+                           const ocq_token_batch* batch, void* q_out_dev, void* stream);
+
+/* Attention of the batch's new tokens over the cache.  The token at place p
+ * sees the keys j <= p, j < kv_len of its request for which window = 0, or
+ * j > p - window, or j < sinks (the first tokens, which stay visible):
+ *   out = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j e^(scale q.k_j).
+ * A token that sees no key has out 0 and lse -inf.  heads is a multiple of the
+ * cache's kv_heads; query head h reads kv head h / (heads / kv_heads).
+ * q_dev [tokens, heads, head_dim] with token and head strides; out_dev bf16
+ * [tokens, heads, head_dim] contiguous; lse_dev float [tokens, heads] or NULL.
+ * scale > 0 and finite, window >= 0 (0: none), sinks >= 0 (0 without a
+ * window).  Scores, softmax statistics and sums are fp32; probabilities are
+ * rounded to bf16 for the second product.
+ * Keys and values past kv_len are not read into the result, whatever the
+ * pages hold there.  A page outside [0, num_pages) reads as zeros.  A value
+ * row that one token of the batch sees and another does not must be finite.
+ * workspace_dev: ocq_attention_workspace_bytes(...) bytes (may be 0), contents
+ * need not be initialized; calls that share it must be ordered on one stream. */
+size_t ocq_attention_workspace_bytes(int heads, const ocq_kv_cache* cache, const ocq_token_batch* batch, int window,
+                                     int sinks);
+ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, int heads,
+                               const ocq_kv_cache* cache, const ocq_token_batch* batch, float scale, int window,
+                               int sinks, void* out_dev, void* lse_dev, void* workspace_dev, size_t workspace_bytes,
+                               void* stream);
+
 /* Message for the last failure on this thread ("" if none). */
 const char* ocq_last_error(void);
 

@@ -1,0 +1,84 @@
+// Internal declarations of the operators around the MLP block: residual +
+// RMSNorm with an E4M3 output (norm.hip), rotary positions with the append to
+// a paged cache (rope.hip), attention over that cache (attention.hip).
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/ocq.h"
+
+namespace ocq {
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* res;       // nullable
+  const uint16_t* w;
+  uint16_t* res_out;         // nullable
+  uint16_t* y;               // nullable
+  uint8_t* codes;            // nullable
+  float* scales;             // with codes
+  int64_t x_stride, res_stride;   // elements between rows
+  float eps;
+  int rows, hidden;
+};
+
+// A token batch and a cache as the kernels take them (sizes checked by the
+// entry points; contents of device arrays are bounded by the kernels).
+struct BatchArgs {
+  const int32_t* q_start;    // [requests + 1]
+  const int32_t* kv_lens;    // [requests]
+  const int32_t* table;      // [requests][table_stride]
+  int64_t table_stride;
+  int requests, tokens, max_pages;
+};
+
+struct CacheArgs {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;            // E4M3 only
+  float* v_scale;
+  int64_t page, head, token;       // strides in bytes
+  int64_t s_page, s_head, s_token; // scale strides in elements
+  int num_pages, page_shift, kv_heads;
+};
+
+struct RopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;   // strides in elements
+  const double* inv_freq;    // [rot / 2]
+  const int32_t* positions;  // nullable: place in the request
+  uint16_t* q_out;           // [tokens][heads][dim]
+  float multiplier;
+  int heads, dim, rot, interleaved, e4m3;
+  BatchArgs b;
+  CacheArgs c;
+};
+
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t q_token, q_head;   // strides in elements
+  uint16_t* out;             // [tokens][heads][dim]
+  float* lse;                // nullable, [tokens][heads]
+  float scale;
+  int heads, group, dim, window, sinks, e4m3;
+  int max_new;
+  BatchArgs b;
+  CacheArgs c;
+  // split over the keys: partial outputs and their log2-sum-exps
+  int splits;
+  float* part_o;             // [splits][tokens][heads][dim]
+  float* part_lse;           // [splits][tokens][heads]
+};
+
+// each enqueues on `stream` and returns 0 or a hipError_t value
+int launch_norm(const NormArgs& a, void* stream);
+int launch_rope(const RopeArgs& a, void* stream);
+int launch_attn(const AttnArgs& a, void* stream);
+// ways the keys of one (request, kv head, row tile) are split, for a call of
+// this shape (1 = not split)
+int attn_splits(int tokens, int requests, int max_new, int max_kv, int heads, int kv_heads, int dim, int e4m3,
+                int window, int sinks);
+
+}  // namespace ocq

@@ -1,0 +1,29 @@
+// Device-side pieces shared by the operators around the MLP block.
+#pragma once
+#include "kcommon.h"
+#include "layer.h"
+
+namespace ocq {
+
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {   // nearest even, NaN kept
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2bf));
+}
+
+__device__ __forceinline__ v4i pack8_bf16(const float* f) {
+  return v4i{(int)pack_bf16(f[0], f[1]), (int)pack_bf16(f[2], f[3]), (int)pack_bf16(f[4], f[5]),
+             (int)pack_bf16(f[6], f[7])};
+}
+
+__device__ __forceinline__ void unpack8_bf16(const v4i& u, float* f) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = __uint_as_float((uint32_t)u[j] << 16);
+    f[2 * j + 1] = __uint_as_float((uint32_t)u[j] & 0xFFFF0000u);
+  }
+}
+
+}  // namespace ocq

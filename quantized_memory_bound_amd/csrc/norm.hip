@@ -1,0 +1,125 @@
+// Residual addition, RMSNorm and per-token E4M3 quantization in one pass.
+//
+//   h = x + residual (fp32), residual_out = bf16(h)
+//   y = h / sqrt(mean(h^2) + eps) * weight (fp32)
+//   codes = E4M3(fl32(y / s)), s = fl32(max|y| / 448), and / or bf16(y)
+//
+// The norm is taken of the fp32 sum, not of its bf16 rounding: each output is
+// rounded once.  WPR waves hold one row in registers (8 values per lane and
+// unit), so x and the residual are read once; two reductions (sum of squares,
+// then max|y|) meet in LDS.  Bound by HBM, or by latency for few rows.
+#include "layer_dev.h"
+
+namespace ocq {
+namespace {
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+template <int WPR, int PER>
+__global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_norm(NormArgs a) {
+  constexpr int RPB = WPR < 4 ? 4 / WPR : 1;   // rows per workgroup
+  __shared__ float s_sum[RPB][WPR], s_max[RPB][WPR];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int slot = wave / WPR, wr = wave % WPR;
+  const int row = blockIdx.x * RPB + slot;
+  const bool live = row < a.rows;
+  const int units = a.hidden / 8;
+  constexpr bool kHoldW = PER <= 2;            // longer rows read the weight again rather than spill
+  float h[PER][8];
+  v4i w[kHoldW ? PER : 1];
+  float ss = 0.0f;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int u = (p * WPR + wr) * 64 + lane;
+    const bool in = live && u < units;
+    const v4i xv = in ? *(const v4i*)(a.x + row * a.x_stride + u * 8) : v4i{0, 0, 0, 0};
+    const v4i rv = in && a.res ? *(const v4i*)(a.res + row * a.res_stride + u * 8) : v4i{0, 0, 0, 0};
+    if constexpr (kHoldW) w[p] = in ? *(const v4i*)(a.w + u * 8) : v4i{0, 0, 0, 0};
+    float r[8];
+    unpack8_bf16(xv, h[p]);
+    unpack8_bf16(rv, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[p][j] += r[j];
+      ss = __builtin_fmaf(h[p][j], h[p][j], ss);
+    }
+    if (in && a.res_out)
+      *(v4i*)(a.res_out + (size_t)row * a.hidden + u * 8) =
+          pack8_bf16(h[p]);
+  }
+  ss = wave_sum(ss);
+  if constexpr (WPR > 1) {
+    if (lane == 0) s_sum[slot][wr] = ss;
+    lds_barrier();
+    ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) ss += s_sum[slot][k];
+  }
+  const float inv = 1.0f / __builtin_sqrtf(ss / (float)a.hidden + a.eps);
+  float amax = 0.0f;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int u = (p * WPR + wr) * 64 + lane;
+    if constexpr (!kHoldW) w[0] = u < units ? *(const v4i*)(a.w + u * 8) : v4i{0, 0, 0, 0};
+    float wf[8];
+    unpack8_bf16(w[kHoldW ? p : 0], wf);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[p][j] = h[p][j] * inv * wf[j];
+      amax = fmaxf(amax, fabsf(h[p][j]));
+    }
+    if (live && u < units && a.y)
+      *(v4i*)(a.y + (size_t)row * a.hidden + u * 8) =
+          pack8_bf16(h[p]);
+  }
+  if (!a.codes) return;
+  amax = wave_max(amax);
+  if constexpr (WPR > 1) {
+    if (lane == 0) s_max[slot][wr] = amax;
+    lds_barrier();
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) amax = fmaxf(amax, s_max[slot][k]);
+  }
+  // a row whose squares do not sum to a finite number has no norm: its scale
+  // says so (the maximum skips NaN)
+  const float s = ss < __builtin_inff() ? amax / 448.0f : __builtin_nanf("");
+  const float rcp = s > 0.0f ? 1.0f / s : 0.0f;
+  if (!live) return;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int u = (p * WPR + wr) * 64 + lane;
+    if (u < units) {
+      const v2u c = s > 0.0f ? e4m3x8_quot(h[p], s, rcp) : v2u{0u, 0u};
+      *(v2u*)(a.codes + (size_t)row * a.hidden + u * 8) = c;
+    }
+  }
+  if (wr == 0 && lane == 0) a.scales[row] = s;
+}
+
+template <int WPR, int PER>
+int run(const NormArgs& a, hipStream_t st) {
+  constexpr int RPB = WPR < 4 ? 4 / WPR : 1;
+  constexpr int threads = WPR < 4 ? 256 : 64 * WPR;
+  hipLaunchKernelGGL((k_norm<WPR, PER>), dim3((a.rows + RPB - 1) / RPB), dim3(threads), 0, st, a);
+  return (int)hipGetLastError();
+}
+
+}  // namespace
+
+int launch_norm(const NormArgs& a, void* stream) {
+  hipStream_t st = (hipStream_t)stream;
+  const int waves = (a.hidden / 8 + 63) / 64;   // 64-lane units of a row
+  if (waves <= 1) return run<1, 1>(a, st);
+  if (waves <= 4) return run<4, 1>(a, st);
+  if (waves <= 8) return run<4, 2>(a, st);
+  if (waves <= 16) return run<16, 1>(a, st);
+  if (waves <= 32) return run<16, 2>(a, st);
+  if (waves <= 64) return run<16, 4>(a, st);
+  return run<16, 8>(a, st);
+}
+
+}  // namespace ocq

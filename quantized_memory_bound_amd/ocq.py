@@ -32,7 +32,9 @@ EXPORTS = ("ocq_version", "ocq_packed_bytes", "ocq_pack_weights_host", "ocq_pack
            "ocq_set_stage_events", "ocq_last_error", "ocq_stack_workspace_bytes", "ocq_mlp_stack_forward",
            "ocq_calibrate_smoothing_host", "ocq_pack_weights_smoothed_host", "ocq_pack_weights_smoothed",
            "ocq_diag_stream_read", "ocq_diag_window_read", "ocq_diag_mfma_rate", "ocq_diag_empty", "ocq_diag_mfma_dot", "ocq_diag_phase_stamps", "ocq_noalloc_scratch_bytes",
-           "ocq_mlp_forward_noalloc", "ocq_set_fused_requant", "ocq_last_requant_in_gateup")
+           "ocq_mlp_forward_noalloc", "ocq_set_fused_requant", "ocq_last_requant_in_gateup",
+           "ocq_add_rmsnorm", "ocq_rope_frequencies", "ocq_rope_append", "ocq_attention_workspace_bytes",
+           "ocq_paged_attention")
 
 
 class OcqError(RuntimeError):
@@ -44,6 +46,19 @@ class OcqError(RuntimeError):
 class Taps(ctypes.Structure):
     _fields_ = [("x_codes", ctypes.c_void_p), ("x_scales", ctypes.c_void_p),
                 ("h_out", ctypes.c_void_p), ("h_scales", ctypes.c_void_p)]
+
+
+class KVCacheStruct(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_dev", "v_dev", "k_scale_dev", "v_scale_dev")] +
+                [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride", "scale_page_stride",
+                                               "scale_head_stride", "scale_token_stride")] +
+                [(n, ctypes.c_int) for n in ("num_pages", "page_size", "kv_heads", "head_dim", "format")])
+
+
+class TokenBatchStruct(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q_start_dev", "kv_lens_dev", "page_table_dev")] +
+                [("table_stride", ctypes.c_int64)] +
+                [(n, ctypes.c_int) for n in ("requests", "tokens", "max_pages", "max_new", "max_kv")])
 
 
 _lib = None
@@ -93,6 +108,17 @@ def lib():
     L.ocq_diag_empty.argtypes, L.ocq_diag_empty.restype = [vp], i
     L.ocq_diag_mfma_dot.argtypes, L.ocq_diag_mfma_dot.restype = [i, vp, vp, i, i, i, vp, vp], i
     L.ocq_diag_phase_stamps.argtypes, L.ocq_diag_phase_stamps.restype = [i, vp, sz], i
+    i64, d = ctypes.c_int64, ctypes.c_double
+    cp, bp = ctypes.POINTER(KVCacheStruct), ctypes.POINTER(TokenBatchStruct)
+    L.ocq_add_rmsnorm.argtypes = [vp, i64, vp, i64, vp, f, i, i, vp, vp, vp, vp, vp]
+    L.ocq_add_rmsnorm.restype = i
+    L.ocq_rope_frequencies.argtypes = [i, d, i, d, d, d, d, vp, ctypes.POINTER(f)]
+    L.ocq_rope_frequencies.restype = i
+    L.ocq_rope_append.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i, vp, i, i, f, vp, cp, bp, vp, vp]
+    L.ocq_rope_append.restype = i
+    L.ocq_attention_workspace_bytes.argtypes, L.ocq_attention_workspace_bytes.restype = [i, cp, bp, i, i], sz
+    L.ocq_paged_attention.argtypes = [vp, i64, i64, i, cp, bp, f, i, i, vp, vp, vp, sz, vp]
+    L.ocq_paged_attention.restype = i
     _lib = L
     return L
 
@@ -370,6 +396,281 @@ class QuantizedMLP:
     def __call__(self, x, y=None, taps=None, stream=None):
         return mlp_forward(self.blob, x, self.hidden, self.inter, self.prec_mode, y=y,
                            workspace=self.workspace(x.shape[0]), taps=taps, stream=stream)
+
+
+# ---------------------------------------------------------------- the operators around the block
+
+ROPE_SCALINGS = ("none", "linear", "ntk", "yarn")
+
+
+def _rows_view(t, name, device, dims):
+    """Raise unless t is a bf16 tensor of `dims` axes on `device` with its last axis contiguous."""
+    import torch
+    if t is None or not hasattr(t, "data_ptr"):
+        raise OcqError(ERR_INVALID_ARG, "%s must be a tensor" % name)
+    if t.dtype != torch.bfloat16 or t.device != device:
+        raise OcqError(ERR_INVALID_ARG, "%s must be bfloat16 on %s, got %s on %s" % (name, device, t.dtype, t.device))
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise OcqError(ERR_INVALID_ARG, "%s must have %d axes, the last one contiguous" % (name, dims))
+
+
+def _device_of(t, name):
+    import torch
+    if t is None or not hasattr(t, "data_ptr") or not t.is_cuda:
+        raise OcqError(ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
+    if t.device.index != torch.cuda.current_device():
+        raise OcqError(ERR_INVALID_ARG, "%s is on %s, not on the current device" % (name, t.device))
+    return t.device
+
+
+def add_rmsnorm(x, weight, eps=1e-6, residual=None, want_y=False, want_codes=True, residual_out=None, y=None,
+                codes=None, scales=None, stream=None):
+    """RMSNorm of h = x + residual (x, residual: bf16 [rows, hidden] CUDA tensors, rows strided at will; weight: bf16
+    [hidden]); returns (residual_out, y, codes, scales).
+
+    residual_out: bf16(h), None without a residual; y: bf16 of the norm if wanted or given; codes (float8_e4m3fn
+    [rows, hidden]) and scales (float32 [rows]): its E4M3 quantization if wanted or given.  Outputs that are not
+    given are allocated; given codes may be uint8.
+    """
+    import torch
+    dev = _device_of(x, "x")
+    _rows_view(x, "x", dev, 2)
+    rows, hidden = x.shape
+    _need(weight, "weight", torch.bfloat16, dev, shape=(hidden,))
+    if residual is not None:
+        _rows_view(residual, "residual", dev, 2)
+        if residual.shape != x.shape:
+            raise OcqError(ERR_INVALID_ARG, "residual has shape %s, x %s" % (tuple(residual.shape), tuple(x.shape)))
+        if residual_out is None:
+            residual_out = _empty((rows, hidden), torch.bfloat16, dev, stream)
+    if residual_out is not None:
+        _need(residual_out, "residual_out", torch.bfloat16, dev, shape=(rows, hidden))
+    if y is not None:
+        _need(y, "y", torch.bfloat16, dev, shape=(rows, hidden))
+    elif want_y:
+        y = _empty((rows, hidden), torch.bfloat16, dev, stream)
+    if codes is not None or scales is not None or want_codes:
+        if codes is None:
+            codes = _empty((rows, hidden), torch.float8_e4m3fn, dev, stream)
+        else:
+            _need(codes, "codes", (torch.float8_e4m3fn, torch.uint8), dev, shape=(rows, hidden))
+        if scales is None:
+            scales = _empty(rows, torch.float32, dev, stream)
+        else:
+            _need(scales, "scales", torch.float32, dev, shape=(rows,))
+    _check(lib().ocq_add_rmsnorm(x.data_ptr(), x.stride(0), None if residual is None else residual.data_ptr(),
+                                 0 if residual is None else residual.stride(0), weight.data_ptr(), eps, rows, hidden,
+                                 None if residual_out is None else residual_out.data_ptr(),
+                                 None if y is None else y.data_ptr(), None if codes is None else codes.data_ptr(),
+                                 None if scales is None else scales.data_ptr(), _stream_handle(stream)))
+    return residual_out, y, codes, scales
+
+
+class PagedKVCache:
+    """The paged cache of one layer.
+
+    k, v: [num_pages, kv_heads, page_size, head_dim] CUDA tensors, bf16, or float8_e4m3fn (or uint8) codes with
+    k_scale, v_scale float32 [num_pages, kv_heads, page_size].  Any order of the first three axes in memory (a
+    permuted view of a pool of another layout is fine), the same for k and v.
+    """
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        dev = _device_of(k, "k")
+        if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
+            raise OcqError(ERR_INVALID_ARG, "k must be [pages, kv_heads, page_size, head_dim], bf16 or E4M3 codes")
+        if v is None or not hasattr(v, "data_ptr") or v.device != dev or v.dtype != k.dtype or v.shape != k.shape or \
+                v.stride() != k.stride():
+            raise OcqError(ERR_INVALID_ARG, "v must have k's device, dtype, shape and strides")
+        if k.stride(3) != 1:
+            raise OcqError(ERR_INVALID_ARG, "the last axis of k and v must be contiguous")
+        e4m3 = k.dtype != torch.bfloat16
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            raise OcqError(ERR_INVALID_ARG, "E4M3 caches have scales, bf16 caches none")
+        if e4m3:
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if t.device != dev or t.dtype != torch.float32 or t.shape != k.shape[:3] or \
+                        t.stride() != k_scale.stride():
+                    raise OcqError(ERR_INVALID_ARG, "%s must be float32 %s, k_scale and v_scale of one layout" %
+                                   (name, tuple(k.shape[:3])))
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, dev
+        pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        s = k_scale.stride() if e4m3 else (0, 0, 0)
+        self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
+                                    v_scale.data_ptr() if e4m3 else None, k.stride(0), k.stride(1), k.stride(2), s[0],
+                                    s[1], s[2], pages, self.page_size, self.kv_heads, self.head_dim, int(e4m3))
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def allocate(cls, num_pages, page_size, kv_heads, head_dim, e4m3=False, device="cuda"):
+        """A zeroed cache whose pages hold each head's rows side by side."""
+        import torch
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        if not e4m3:
+            return cls(*(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        kv = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+        return cls(*kv, *(torch.zeros(shape[:3], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+class TokenBatch:
+    """The new tokens of one step: request r has rows q_start[r] .. q_start[r + 1] of the token axis, kv_lens[r]
+    tokens in the cache with the new ones, and pages page_table[r].
+
+    q_start int32 [requests + 1], kv_lens int32 [requests], page_table int32 [requests, max_pages] (rows strided at
+    will): CUDA tensors whose contents may change between calls.  tokens (the rows of q), max_new and max_kv are
+    host numbers: bounds of the new tokens and of kv_lens of any request.
+    """
+
+    def __init__(self, q_start, kv_lens, page_table, max_new, max_kv, tokens=None):
+        import torch
+        dev = _device_of(kv_lens, "kv_lens")
+        requests = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+        _need(kv_lens, "kv_lens", torch.int32, dev, shape=(requests,))
+        _need(q_start, "q_start", torch.int32, dev, shape=(requests + 1,))
+        if not hasattr(page_table, "data_ptr") or page_table.dtype != torch.int32 or page_table.device != dev or \
+                page_table.dim() != 2 or page_table.shape[0] != requests or \
+                (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise OcqError(ERR_INVALID_ARG, "page_table must be int32 [%d, max_pages], its rows contiguous" % requests)
+        self.q_start, self.kv_lens, self.page_table, self.device = q_start, kv_lens, page_table, dev
+        self.requests, self.tokens = requests, None
+        self.struct = TokenBatchStruct(q_start.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
+                                       max(page_table.stride(0), page_table.shape[1]), requests, 0,
+                                       page_table.shape[1], max_new, max_kv)
+        self.ref = ctypes.byref(self.struct)
+        if tokens is not None:
+            self.of(tokens)
+
+    def of(self, tokens):
+        """The batch as an argument for a call over `tokens` rows."""
+        if self.tokens is None:
+            self.tokens = self.struct.tokens = int(tokens)
+        elif tokens != self.tokens:
+            raise OcqError(ERR_INVALID_ARG, "the batch has %d tokens, the tensor %d" % (self.tokens, tokens))
+        return self.ref
+
+
+def rope_frequencies(rot, base=10000.0, scaling="none", factor=1.0, context=4096, beta_fast=32.0, beta_slow=1.0):
+    """Rotary frequencies (float64 numpy [rot / 2]) and the multiplier of cos and sin; scaling: one of
+    ROPE_SCALINGS (none, positions divided by the factor, stretched base, YaRN)."""
+    if scaling not in ROPE_SCALINGS:
+        raise OcqError(ERR_INVALID_ARG, "scaling must be one of %s" % (ROPE_SCALINGS,))
+    inv = np.empty(max(1, int(rot) // 2), dtype=np.float64)
+    mult = ctypes.c_float()
+    _check(lib().ocq_rope_frequencies(int(rot), float(base), ROPE_SCALINGS.index(scaling), float(factor),
+                                      float(context), float(beta_fast), float(beta_slow), inv.ctypes.data,
+                                      ctypes.byref(mult)))
+    return inv, mult.value
+
+
+class Rope:
+    """Rotary frequencies on the GPU: inv_freq float64 [rot / 2], the multiplier of cos and sin, and whether pairs
+    are (2 j, 2 j + 1) (interleaved) or (j, j + rot / 2)."""
+
+    def __init__(self, inv_freq, multiplier=1.0, interleaved=False):
+        import torch
+        dev = _device_of(inv_freq, "inv_freq")
+        if inv_freq.dim() != 1:
+            raise OcqError(ERR_INVALID_ARG, "inv_freq must be [rot / 2]")
+        _need(inv_freq, "inv_freq", torch.float64, dev)
+        self.inv_freq, self.multiplier, self.interleaved = inv_freq, float(multiplier), int(bool(interleaved))
+        self.rot, self.device = 2 * inv_freq.shape[0], dev
+
+    @classmethod
+    def make(cls, rot, interleaved=False, device="cuda", **kw):
+        """From rope_frequencies(rot, **kw)."""
+        import torch
+        inv, mult = rope_frequencies(rot, **kw)
+        return cls(torch.from_numpy(inv).to(device), mult, interleaved)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor for a call on `stream`: allocated on it, so that its memory is not reused before the call."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _on(device, *handles):
+    for h in handles:
+        if h.device != device:
+            raise OcqError(ERR_INVALID_ARG, "%s is on %s, not %s" % (type(h).__name__, h.device, device))
+
+
+def rope_append(q, k, v, rope, cache, batch, positions=None, q_out=None, stream=None):
+    """Rotate q (bf16 [tokens, heads, head_dim]) and k ([tokens, kv_heads, head_dim]) and append k and v to the
+    cache; returns the rotated q (q_out, contiguous, or q itself).  Token and head strides are free.  positions:
+    None (each token's place in its request) or int32 [tokens]."""
+    import torch
+    dev = _device_of(q, "q")
+    _rows_view(q, "q", dev, 3)
+    tokens, heads, dim = q.shape
+    kv_shape = (tokens, cache.kv_heads, cache.head_dim)
+    for t, name in ((k, "k"), (v, "v")):
+        _rows_view(t, name, dev, 3)
+        if t.shape != kv_shape:
+            raise OcqError(ERR_INVALID_ARG, "%s has shape %s, expected %s" % (name, tuple(t.shape), kv_shape))
+    if dim != cache.head_dim:
+        raise OcqError(ERR_INVALID_ARG, "q has head size %d, the cache %d" % (dim, cache.head_dim))
+    _on(dev, rope, cache, batch)
+    if positions is not None:
+        _need(positions, "positions", torch.int32, dev, shape=(tokens,))
+    if q_out is None:
+        q_out = _empty((tokens, heads, dim), torch.bfloat16, dev, stream)
+    else:
+        _need(q_out, "q_out", torch.bfloat16, dev, shape=(tokens, heads, dim))
+    _check(lib().ocq_rope_append(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1),
+                                 v.data_ptr(), v.stride(0), v.stride(1), heads, rope.inv_freq.data_ptr(), rope.rot,
+                                 rope.interleaved, rope.multiplier, None if positions is None else positions.data_ptr(),
+                                 cache.ref, batch.of(tokens), q_out.data_ptr(), _stream_handle(stream)))
+    return q_out
+
+
+def attention_workspace_bytes(heads, cache, batch, window=0, sinks=0):
+    """Workspace of paged_attention for a batch whose tokens are known."""
+    return lib().ocq_attention_workspace_bytes(heads, cache.ref, batch.ref, window, sinks)
+
+
+def paged_attention(q, cache, batch, scale=None, window=0, sinks=0, want_lse=False, out=None, lse=None,
+                    workspace=None, stream=None):
+    """Attention of the new tokens q (bf16 [tokens, heads, head_dim], token and head strides free) over the paged
+    cache that already holds them; returns (out, lse): bf16 [tokens, heads, head_dim] and, if wanted or given,
+    float32 [tokens, heads].
+
+    scale: default head_dim ** -0.5.  window: keys up to window - 1 places back are visible (0: all); sinks: the
+    first tokens, which a window leaves visible.  A token that sees nothing has out 0 and lse -inf.  workspace: a
+    uint8 tensor of attention_workspace_bytes(...), allocated if None.
+    """
+    import torch
+    dev = _device_of(q, "q")
+    _rows_view(q, "q", dev, 3)
+    tokens, heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise OcqError(ERR_INVALID_ARG, "q has head size %d, the cache %d" % (dim, cache.head_dim))
+    _on(dev, cache, batch)
+    if out is None:
+        out = _empty((tokens, heads, dim), torch.bfloat16, dev, stream)
+    else:
+        _need(out, "out", torch.bfloat16, dev, shape=(tokens, heads, dim))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev, shape=(tokens, heads))
+    elif want_lse:
+        lse = _empty((tokens, heads), torch.float32, dev, stream)
+    ref, L = batch.of(tokens), lib()
+    need = 0
+    if workspace is None:
+        need = L.ocq_attention_workspace_bytes(heads, cache.ref, ref, window, sinks)
+        if need:
+            workspace = _empty(need, torch.uint8, dev, stream)
+    else:
+        _need(workspace, "workspace", torch.uint8, dev)
+        need = workspace.numel()
+    _check(L.ocq_paged_attention(q.data_ptr(), q.stride(0), q.stride(1), heads, cache.ref, ref,
+                                 dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
+                                 None if lse is None else lse.data_ptr(),
+                                 None if workspace is None else workspace.data_ptr(), need, _stream_handle(stream)))
+    return out, lse
 
 
 # ---------------------------------------------------------------- measurement helpers

@@ -1,0 +1,472 @@
+"""The operators around the block on the GPU against plain 64-bit implementations written here.
+
+Tolerances, fixed before the first run.  A bf16 output is rounded once: off by at most half a step, 2^-8 relative.
+Attention rounds each probability to bf16 as well, at most 2^-8 of each weight, which moves the output by at most 2^-8
+of sum_j w_j |v_j|: |out - ref| <= 2^-8 |ref| + 2^-8 sum_j w_j |v_j|.  That takes every rounding at its worst and of
+one sign, which leaves room for the fp32 sums and the hardware exponential (below 2^-15).  E4M3 codes are of fp32
+values and may differ from the 64-bit ones by one step next to a rounding border: a code's value is within 2^-4 |y| +
+2^-10 s (half a subnormal step) of the 64-bit value, widened by 2^-18 for the fp32 error; scales within 2^-20 relative.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from quantized_memory_bound_amd import ocq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+E4M3 = torch.float8_e4m3fn
+
+
+def _gen(seed):
+    return torch.Generator(DEV).manual_seed(seed)
+
+
+def _bf(shape, gen, scale=1.0):
+    return (torch.randn(shape, device=DEV, generator=gen) * scale).to(torch.bfloat16)
+
+
+def _check_bf16(got, ref, what, extra=None):
+    got, ref = got.double(), ref.double()
+    tol = ref.abs() * 2.0 ** -8 + 1e-30 + (0 if extra is None else extra)
+    bad = ~((got - ref).abs() <= tol)
+    assert not bad.any(), "%s: %d of %d off, worst %.3g" % (what, int(bad.sum()), bad.numel(), float((got - ref).abs().max()))
+
+
+def _check_codes(codes, scales, ref, what):
+    """codes [..., n], scales [...] against the 64-bit rows they stand for."""
+    s = ref.abs().amax(-1) / 448
+    assert torch.all((scales.double() - s).abs() <= s * 2.0 ** -20), what + ": scales"
+    got = codes.view(E4M3).double() * scales.double()[..., None]
+    tol = ref.abs() * (2.0 ** -4 + 2.0 ** -18) + s[..., None] * (2.0 ** -10 + 2.0 ** -18)
+    assert torch.all((got - ref).abs() <= tol), what + ": codes"
+
+
+# ---------------------------------------------------------------- norm
+
+def _norm_ref(x, w, eps, res):
+    h = x.double() + (0 if res is None else res.double())
+    return h, h / torch.sqrt(h.square().mean(-1, keepdim=True) + eps) * w.double()
+
+
+@pytest.mark.parametrize("rows", [1, 3, 130])
+@pytest.mark.parametrize("hidden", [8, 72, 512, 520, 2048, 4096, 4104, 8192, 16384, 20000, 32768, 65536])
+def test_norm(rows, hidden):
+    g = _gen(rows * 7 + hidden)
+    x, res, w = _bf((rows, hidden), g, 2.0), _bf((rows, hidden), g), _bf((hidden,), g)
+    r, y, c, s = ocq.add_rmsnorm(x, w, 1e-5, residual=res, want_y=True)
+    h, ref = _norm_ref(x, w, 1e-5, res)
+    # the fp32 sum of two bf16 values may itself round: 2^-24 of the larger
+    _check_bf16(r, h, "residual", extra=(x.double().abs() + res.double().abs()) * 2.0 ** -23)
+    _check_bf16(y, ref, "y", extra=(x.double().abs() + res.double().abs()) * ref.abs().amax() * 2.0 ** -20)
+    _check_codes(c, s, ref, "codes")
+
+
+def test_norm_without_residual_and_single_outputs():
+    g = _gen(5)
+    x, w = _bf((9, 1024), g), _bf((1024,), g)
+    _, ref = _norm_ref(x, w, 0.0, None)
+    r, y, c, s = ocq.add_rmsnorm(x, w, 0.0, want_y=True, want_codes=False)
+    assert r is None and c is None and s is None
+    _check_bf16(y, ref, "y")
+    r, y, c, s = ocq.add_rmsnorm(x, w, 0.0)
+    assert r is None and y is None
+    _check_codes(c, s, ref, "codes")
+    kept = ocq.add_rmsnorm(x, w, 0.0, residual_out=torch.empty_like(x))[0]
+    assert torch.equal(kept, x)
+
+
+def test_norm_strided_rows_in_place_and_given_outputs():
+    g = _gen(6)
+    wide = _bf((7, 3 * 256), g)
+    x, res, w = wide[:, 256:512], _bf((7, 256), g), _bf((256,), g)
+    h, ref = _norm_ref(x, w, 1e-6, res)
+    codes, scales = torch.empty((7, 256), dtype=torch.uint8, device=DEV), torch.empty(7, device=DEV)
+    r, y, c, s = ocq.add_rmsnorm(x, w, 1e-6, residual=res, residual_out=res, codes=codes, scales=scales)
+    assert r is res and c is codes and s is scales and y is None
+    _check_bf16(res, h, "residual", extra=h.abs().amax() * 2.0 ** -22)
+    _check_codes(codes, scales, ref, "codes")
+
+
+def test_norm_zero_rows_and_rows_without_a_finite_norm():
+    g = _gen(7)
+    x, w = _bf((4, 512), g), _bf((512,), g)
+    x[1] = 0
+    x[2, 17] = float("inf")
+    _, y, c, s = ocq.add_rmsnorm(x, w, 0.0, want_y=True)
+    _, y1, c1, s1 = ocq.add_rmsnorm(x, w, 1e-6, want_y=True)
+    assert s1[1] == 0 and not c1[1].view(torch.uint8).any() and not y1[1].float().any()
+    assert torch.isnan(s1[2]) and not c1[2].view(torch.uint8).any()
+    assert torch.isfinite(s1[[0, 1, 3]]).all()
+    assert torch.isnan(y[1].float()).all()   # 0 / sqrt(0 + 0)
+
+
+# ---------------------------------------------------------------- batches and caches
+
+def make_batch(news, kvs, page_size, gen, spare=3, table_pad=0):
+    need = [max(1, -(-kv // page_size)) for kv in kvs]
+    most, pages = max(need), sum(need) + spare
+    order = torch.randperm(pages, device=DEV, generator=gen).to(torch.int32)
+    table = torch.full((len(kvs), most + table_pad), -7, dtype=torch.int32, device=DEV)
+    at = 0
+    for r, c in enumerate(need):
+        table[r, :c] = order[at: at + c]
+        at += c
+    start = torch.tensor([0] + list(np.cumsum(news)), dtype=torch.int32, device=DEV)
+    batch = ocq.TokenBatch(start, torch.tensor(kvs, dtype=torch.int32, device=DEV), table[:, :most],
+                           max(1, max(news)), max(kvs))
+    return batch, pages
+
+
+def make_cache(pages, kv_heads, page_size, dim, e4m3, gen, order="heads"):
+    """A filled cache whose axes lie in memory as [pages, heads, tokens] or [pages, tokens, heads]."""
+    def pool(fill):
+        if order == "heads":
+            return fill((pages, kv_heads, page_size))
+        return fill((pages, page_size, kv_heads)).transpose(1, 2)
+    if not e4m3:
+        k, v = (pool(lambda s: _bf(s + (dim,), gen)) for _ in range(2))
+        return ocq.PagedKVCache(k, v)
+    def codes(s):
+        return (torch.randn(s + (dim,), device=DEV, generator=gen) * 100).clamp(-448, 448).to(E4M3)
+    def scale(s):
+        return torch.rand(s, device=DEV, generator=gen) * 0.02 + 0.001
+    k, v = pool(codes), pool(codes)
+    return ocq.PagedKVCache(k, v, pool(scale), pool(scale))
+
+
+def rows_of(cache, which, table_row, places):
+    """[len(places), kv_heads, dim] in 64 bits; zeros for pages that are none."""
+    x, s = (cache.k, cache.k_scale) if which == "k" else (cache.v, cache.v_scale)
+    ids = table_row[places // cache.page_size].long()
+    ok = (ids >= 0) & (ids < x.shape[0])
+    ids = ids.clamp(0, x.shape[0] - 1)
+    y = (x if s is None else x.view(E4M3)).double()[ids, :, places % cache.page_size]
+    if s is not None:
+        y = y * s.double()[ids, :, places % cache.page_size][..., None]
+    return torch.where(ok[:, None, None], y, torch.zeros_like(y))
+
+
+# ---------------------------------------------------------------- rotary + append
+
+def _turned(x, pos, inv, mult, interleaved):
+    x = x.double().clone()
+    rot = 2 * len(inv)
+    ang = pos.double()[:, None] * inv.double()[None]
+    c, s = (torch.cos(ang) * mult)[:, None], (torch.sin(ang) * mult)[:, None]
+    ia = torch.arange(0, rot, 2) if interleaved else torch.arange(rot // 2)
+    ib = ia + 1 if interleaved else ia + rot // 2
+    a, b = x[..., ia], x[..., ib]
+    x[..., ia], x[..., ib] = a * c - b * s, b * c + a * s
+    return x
+
+
+ROPES = [(64, 64, 2, 1, 16, False, False, "heads"), (64, 32, 3, 3, 1, True, True, "tokens"),
+         (128, 128, 8, 2, 64, False, True, "heads"), (128, 48, 5, 5, 32, True, False, "tokens"),
+         (256, 256, 6, 2, 8, False, True, "tokens"), (256, 16, 4, 4, 256, True, False, "heads"),
+         (128, 128, 40, 8, 16, True, True, "heads")]
+
+
+@pytest.mark.parametrize("dim,rot,heads,kv_heads,page,interleaved,e4m3,order", ROPES)
+@pytest.mark.parametrize("given", [False, True])
+def test_rope_append(dim, rot, heads, kv_heads, page, interleaved, e4m3, order, given):
+    g = _gen(dim + rot + heads)
+    news, kvs = [1, 0, 13, 70], [1, 5, 40, 300]
+    batch, pages = make_batch(news, kvs, page, g, table_pad=2)
+    cache = make_cache(pages, kv_heads, page, dim, e4m3, g, order)
+    t = sum(news)
+    qkv = _bf((t, heads + 2 * kv_heads, dim), g)
+    q, k, v = qkv.split([heads, kv_heads, kv_heads], 1)
+    if e4m3:
+        v[3] = 0
+    rope = ocq.Rope.make(rot, interleaved, DEV, scaling="yarn", factor=4.0, context=64)
+    place = torch.cat([torch.arange(kv - n, kv, device=DEV) for n, kv in zip(news, kvs)])
+    positions = (place * 1000 + 123456).to(torch.int32) if given else None
+    before = [x.clone() if x is not None else None for x in (cache.k, cache.v, cache.k_scale, cache.v_scale)]
+    out = ocq.rope_append(q, k, v, rope, cache, batch, positions=positions)
+    pos = place if positions is None else positions
+    ref = _turned(q, pos, rope.inv_freq, rope.multiplier, interleaved)
+    size = q.double().abs().amax() * rope.multiplier * 2
+    _check_bf16(out, ref, "q", extra=size * 2.0 ** -20)
+    kr = _turned(k, pos, rope.inv_freq, rope.multiplier, interleaved)
+    at, touched = 0, torch.zeros((pages, page), dtype=torch.bool, device=DEV)
+    for r, (n, kv) in enumerate(zip(news, kvs)):
+        p = torch.arange(kv - n, kv, device=DEV)
+        ids = batch.page_table[r][p // page].long()
+        touched[ids, p % page] = True
+        for which, x, y in (("k", cache.k, kr), ("v", cache.v, v.double())):
+            got, want = x[ids, :, p % page], y[at: at + n]
+            if e4m3:
+                sc = (cache.k_scale if which == "k" else cache.v_scale)[ids, :, p % page]
+                _check_codes(got, sc, want, which)
+            else:
+                _check_bf16(got, want, which, extra=size * 2.0 ** -20 if which == "k" else None)
+        at += n
+    for now, old in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), before):   # every other slot as it was
+        if now is not None:
+            keep = ~touched[:, None, :].expand(-1, kv_heads, -1)
+            a, b = (now.view(torch.uint8), old.view(torch.uint8)) if now.dtype == E4M3 else (now, old)
+            assert torch.equal(a[keep], b[keep])
+
+
+def test_rope_in_place_pages_that_are_none_and_places_past_the_table():
+    g = _gen(3)
+    batch, pages = make_batch([4, 4, 4], [4, 20, 20], 16, g)
+    cache = make_cache(pages, 2, 16, 64, False, g)
+    batch.page_table[1, 1] = pages          # tokens 16 .. 19 of request 1: a page past the pool
+    batch.page_table[2, 1] = -1
+    batch.kv_lens[0] = 3                    # its first new token stands at place -1
+    rope = ocq.Rope.make(64, device=DEV)
+    q, k, v = _bf((12, 4, 64), g), _bf((12, 2, 64), g), _bf((12, 2, 64), g)
+    want = ocq.rope_append(q, k, v, rope, cache, batch)
+    k0, v0 = cache.k.clone(), cache.v.clone()
+    got = ocq.rope_append(q, k, v, rope, cache, batch, q_out=q)
+    assert got is q and torch.equal(want, q)
+    assert torch.equal(cache.k, k0) and torch.equal(cache.v, v0)
+    page = int(batch.page_table[0, 0])
+    assert torch.equal(cache.v[page, :, :3], v[1:4].transpose(0, 1))
+    batch.kv_lens[1] = 1 << 20              # past the table: dropped
+    ocq.rope_append(q, k, v, rope, cache, batch)
+    others = [p for p in range(pages) if p != page]
+    assert torch.equal(cache.k[others], k0[others])
+
+
+# ---------------------------------------------------------------- attention
+
+def attention_ref(q, cache, batch, news, kvs, scale, window, sinks):
+    out, lse, mag, at = [], [], [], 0
+    group = q.shape[1] // cache.kv_heads
+    for r, (n, kv) in enumerate(zip(news, kvs)):
+        if n == 0:
+            continue
+        qq = q[at: at + n].double()
+        at += n
+        j = torch.arange(kv, device=DEV)
+        p = torch.arange(kv - n, kv, device=DEV)
+        k, v = (rows_of(cache, w, batch.page_table[r], j) for w in ("k", "v"))
+        seen = j[None] <= p[:, None]
+        if window:
+            seen = seen & ((j[None] > p[:, None] - window) | (j[None] < sinks))
+        kh, vh = (x.repeat_interleave(group, 1).permute(1, 0, 2).contiguous() for x in (k, v))   # [heads, kv, dim]
+        s = torch.matmul(qq.transpose(0, 1).contiguous(), kh.transpose(1, 2).contiguous()) * scale
+        s = s.masked_fill(~seen[None], -math.inf)
+        w = torch.softmax(s, -1) if kv else s
+        w = torch.where(seen[None].any(-1, keepdim=True), w, torch.zeros_like(w))
+        out.append(torch.matmul(w, vh).transpose(0, 1))
+        mag.append(torch.matmul(w, vh.abs()).transpose(0, 1))
+        lse.append((torch.logsumexp(s, -1) if kv else torch.full(s.shape[:2], -math.inf, device=DEV, dtype=torch.float64)).transpose(0, 1))
+    return torch.cat(out), torch.cat(lse), torch.cat(mag)
+
+
+def check_attention(q, cache, batch, news, kvs, scale=None, window=0, sinks=0, **kw):
+    out, lse = ocq.paged_attention(q, cache, batch, scale=scale, window=window, sinks=sinks, want_lse=True, **kw)
+    torch.cuda.synchronize()
+    sc = q.shape[2] ** -0.5 if scale is None else scale
+    ref, rl, mag = attention_ref(q, cache, batch, news, kvs, sc, window, sinks)
+    empty = torch.isinf(rl)
+    assert torch.equal(torch.isinf(lse), empty) and not out[empty].float().any()
+    d = (lse.double() - rl)[~empty].abs()
+    # scores are fp32 sums of exact products: 2^-20 of their size, and the sum of exponentials 2^-18
+    assert not d.numel() or d.max() <= 2.0 ** -18 + rl[~empty].abs().max() * 2.0 ** -18
+    _check_bf16(out, ref, "out", extra=mag * 2.0 ** -8)
+    return out, lse
+
+
+BATCHES = [([1], [1]), ([1], [257]), ([1, 1, 1], [31, 32, 33]), ([13, 13, 13, 13], [13, 700, 64, 129]),
+           ([5, 0, 1, 40, 200], [5, 9, 1000, 41, 333]), ([3, 150], [1, 100])]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("group,kv_heads", [(1, 3), (4, 2), (5, 1), (16, 1)])
+@pytest.mark.parametrize("news,kvs", BATCHES)
+def test_attention(dim, e4m3, group, kv_heads, news, kvs):
+    g = _gen(dim * group + len(news))
+    page = {64: 16, 128: 32, 256: 1}[dim]
+    batch, pages = make_batch(news, kvs, page, g, table_pad=1)
+    cache = make_cache(pages, kv_heads, page, dim, e4m3, g, "heads" if group % 2 else "tokens")
+    q = _bf((sum(news), group * kv_heads, dim), g)
+    check_attention(q, cache, batch, news, kvs)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (16, 0), (100, 1), (100, 130), (333, 4), (5000, 8)])
+def test_attention_window_and_sinks(e4m3, window, sinks):
+    g = _gen(window + sinks)
+    news, kvs = [1, 13, 90, 300], [2500, 1313, 1000, 300]
+    for dim, page in ((64, 64), (128, 16)):
+        batch, pages = make_batch(news, kvs, page, g)
+        cache = make_cache(pages, 2, page, dim, e4m3, g)
+        check_attention(_bf((sum(news), 8, dim), g), cache, batch, news, kvs, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dim,e4m3,news,kvs", [(128, False, [1, 1], [40001, 777]), (128, True, [1], [65539]),
+                                               (64, False, [13, 13], [20011, 31]), (256, True, [2], [9001]),
+                                               (128, False, [700], [4099]), (64, True, [513, 1], [513, 5001]),
+                                               (256, False, [129], [3001])])
+def test_attention_long(dim, e4m3, news, kvs):
+    g = _gen(kvs[0])
+    batch, pages = make_batch(news, kvs, 64, g)
+    cache = make_cache(pages, 2, 64, dim, e4m3, g)
+    check_attention(_bf((sum(news), 8, dim), g), cache, batch, news, kvs)
+
+
+@pytest.mark.parametrize("n", [1, 13, 70])
+def test_attention_scores_of_every_size(n):
+    """Large scores (one key takes all), a moving maximum, scores far below zero, equal keys."""
+    g = _gen(n)
+    kv = 900
+    batch, pages = make_batch([n], [kv], 16, g)
+    cache = make_cache(pages, 1, 16, 64, False, g)
+    q = _bf((n, 4, 64), g)
+    for scale in (1e-4, 1.0, 8.0):
+        check_attention(q, cache, batch, [n], [kv], scale=scale)
+    # every key's score below the one after it: the maximum moves in each tile
+    places = torch.arange(kv, device=DEV)
+    ids = batch.page_table[0][places // 16].long()
+    q[:] = 1
+    ramp = (places[:, None].float() / 64).expand(-1, 64).to(torch.bfloat16)
+    for k in (ramp, -ramp, torch.zeros_like(ramp), -8 * ramp):
+        cache.k[ids, 0, places % 16] = k
+        check_attention(q, cache, batch, [n], [kv], scale=0.25)
+
+
+def test_attention_what_lies_past_the_context_does_not_reach_it():
+    """NaN and infinities in unused rows of used pages and in unused pages, for keys and values."""
+    g = _gen(11)
+    for e4m3 in (False, True):
+        for n in (1, 13, 40):
+            news, kvs = [n, n], [n + 37, n + 5]
+            batch, pages = make_batch(news, kvs, 64, g)
+            cache = make_cache(pages, 2, 64, 128, e4m3, g)
+            used = torch.zeros((pages, 64), dtype=torch.bool, device=DEV)
+            for r, kv in enumerate(kvs):
+                p = torch.arange(kv, device=DEV)
+                used[batch.page_table[r][p // 64].long(), p % 64] = True
+            spoil = ~used[:, None, :].expand(-1, 2, -1)
+            if e4m3:
+                for x in (cache.k, cache.v):
+                    x.view(torch.uint8)[spoil] = 0x7F      # NaN
+                cache.k_scale[spoil] = float("inf")
+                cache.v_scale[spoil] = float("nan")
+            else:
+                cache.k[spoil] = float("nan")
+                cache.v[spoil] = float("inf")
+            check_attention(_bf((2 * n, 8, 128), g), cache, batch, news, kvs)
+
+
+def test_attention_pages_that_are_none_read_as_zeros():
+    g = _gen(12)
+    for e4m3 in (False, True):
+        news, kvs = [3, 20], [200, 300]
+        batch, pages = make_batch(news, kvs, 16, g)
+        cache = make_cache(pages, 2, 16, 64, e4m3, g)
+        batch.page_table[0, 2], batch.page_table[1, 0], batch.page_table[1, 7] = -1, pages, 2 ** 31 - 1
+        check_attention(_bf((23, 4, 64), g), cache, batch, news, kvs)
+
+
+def test_attention_views_streams_and_given_outputs():
+    g = _gen(13)
+    news, kvs = [13, 2], [500, 90]
+    batch, pages = make_batch(news, kvs, 32, g)
+    cache = make_cache(pages, 2, 32, 128, False, g, "tokens")
+    q = _bf((15, 8 + 4, 128), g)[:, 2:10]                 # heads of a wider projection
+    want, wl = check_attention(q, cache, batch, news, kvs)
+    nb = ocq.attention_workspace_bytes(8, cache, batch)
+    ws = torch.full((max(nb, 16),), 0xFF, dtype=torch.uint8, device=DEV)   # contents do not matter
+    out, lse = torch.empty_like(want), torch.empty_like(wl)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        a, b = ocq.paged_attention(q, cache, batch, out=out, lse=lse, workspace=ws, stream=side)
+        side.synchronize()
+        assert a is out and b is lse and torch.equal(a, want) and torch.equal(b, wl)
+    a, b = ocq.paged_attention(q, cache, batch, stream=side)
+    side.synchronize()
+    assert b is None and torch.equal(a, want)
+
+
+def test_attention_offsets_past_32_bits():
+    """A pool of more than 2^32 bytes whose used pages lie at its end."""
+    g = _gen(14)
+    pages = (1 << 32) // (64 * 256 * 2) + 40
+    k = torch.zeros((pages, 1, 64, 256), dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros_like(k)
+    k[-20:], v[-20:] = _bf((20, 1, 64, 256), g), _bf((20, 1, 64, 256), g)
+    cache = ocq.PagedKVCache(k, v)
+    start, kvs = torch.tensor([0, 2], dtype=torch.int32, device=DEV), [1200]
+    table = (pages - 1 - torch.arange(19, device=DEV)).to(torch.int32)[None]
+    batch = ocq.TokenBatch(start, torch.tensor(kvs, dtype=torch.int32, device=DEV), table, 2, 1200)
+    rope = ocq.Rope.make(256, device=DEV)
+    q, nk, nv = _bf((2, 4, 256), g), _bf((2, 1, 256), g), _bf((2, 1, 256), g)
+    q = ocq.rope_append(q, nk, nv, rope, cache, batch)
+    assert torch.equal(v[int(table[0, 18]), 0, 1198 % 64: 1200 % 64], nv[:, 0])
+    check_attention(q, cache, batch, [2], kvs)
+
+
+def test_captured_step_replays():
+    """rope_append and paged_attention in a graph: the device arrays change between replays."""
+    g = _gen(15)
+    n, heads = 5, 8
+    batch, pages = make_batch([n, n], [2000, 900], 64, g)
+    cache = make_cache(pages, 2, 64, 128, True, g)
+    rope = ocq.Rope.make(128, device=DEV)
+    q, k, v = _bf((2 * n, heads, 128), g), _bf((2 * n, 2, 128), g), _bf((2 * n, 2, 128), g)
+    x, w = _bf((2 * n, 512), g), _bf((512,), g)
+
+    def step():
+        r = ocq.rope_append(q, k, v, rope, cache, batch)
+        return ocq.paged_attention(r, cache, batch, want_lse=True) + ocq.add_rmsnorm(x, w, want_y=True)[1:]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for i in range(4):
+        q.copy_(_bf(q.shape, g))
+        x.copy_(_bf(x.shape, g))
+        batch.kv_lens.copy_(torch.tensor([1500 + i, 600 + 7 * i], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for a, b in zip(got, step()):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ---------------------------------------------------------------- refusals of the binding
+
+def test_binding_refusals():
+    g = _gen(16)
+    batch, pages = make_batch([2], [20], 16, g)
+    cache = make_cache(pages, 2, 16, 64, False, g)
+    rope = ocq.Rope.make(64, device=DEV)
+    q, k = _bf((2, 4, 64), g), _bf((2, 2, 64), g)
+    w = _bf((64,), g)
+    x = _bf((2, 64), g)
+    calls = [
+        lambda: ocq.paged_attention(q.float(), cache, batch), lambda: ocq.paged_attention(q[:, :, ::2], cache, batch),
+        lambda: ocq.paged_attention(q[:, :3], cache, batch), lambda: ocq.paged_attention(_bf((2, 4, 128), g), cache, batch),
+        lambda: ocq.paged_attention(_bf((3, 4, 64), g), cache, batch),
+        lambda: ocq.paged_attention(q, cache, batch, sinks=3), lambda: ocq.paged_attention(q, cache, batch, scale=-1.0),
+        lambda: ocq.paged_attention(q, cache, batch, out=torch.empty(2, 4, 64, device=DEV)),
+        lambda: ocq.rope_append(q, k, k[:, :1], rope, cache, batch),
+        lambda: ocq.rope_append(q, k, k, ocq.Rope.make(128, device=DEV), cache, batch),
+        lambda: ocq.rope_append(q, k, k, rope, cache, batch, positions=torch.zeros(2, device=DEV)),
+        lambda: ocq.add_rmsnorm(x, w[:32]), lambda: ocq.add_rmsnorm(x, w, residual=x[:1]),
+        lambda: ocq.add_rmsnorm(x, w, want_codes=False), lambda: ocq.add_rmsnorm(x.float(), w),
+        lambda: ocq.PagedKVCache(cache.k, cache.v.float()), lambda: ocq.PagedKVCache(cache.k, cache.v[:1]),
+        lambda: ocq.PagedKVCache(cache.k.view(torch.uint8), cache.v.view(torch.uint8)),
+        lambda: ocq.TokenBatch(batch.q_start.long(), batch.kv_lens, batch.page_table, 1, 1),
+        lambda: ocq.TokenBatch(batch.q_start, batch.kv_lens, batch.page_table[0], 1, 1),
+        lambda: ocq.Rope(rope.inv_freq.float()),
+    ]
+    for call in calls:
+        with pytest.raises(ocq.OcqError):
+            call()
+    assert batch.of(2) is not None
