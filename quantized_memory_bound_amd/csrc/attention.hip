@@ -40,6 +40,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLow = -3.4028234663852886e38f;   // below every score that is visible
 constexpr float kSlack = 8.0f;                    // see above
 
+constexpr int kTargetGroups = 512, kMinTiles = 4, kMaxSplits = 256;   // see attn_splits
+
 // what a table entry outside the pool reads as
 __device__ const v4i g_zero[1] = {};
 
@@ -82,6 +84,7 @@ struct Geo {
   static constexpr int KS = 512 / MT;                                   // inputs of one MFMA (32 or 16)
   static constexpr int QS = D / KS, DT = D / MT, LG = 64 / MT;          // steps of S, tiles of O, lane groups
   static constexpr int PS = TK / KS;                                    // steps of O
+  static constexpr int MINW = D == 256 && MT == 32 ? 1 : 2;             // waves per SIMD the registers leave room for
   static constexpr int JOIN = WK > 1 ? WK * ROWS * (D * 4 + 8) : 0;
   static constexpr int LDS = RING > JOIN ? RING : JOIN;
   static_assert(PART % (1024 * WR) == 0 && TK % 32 == 0 && LDS <= 160 * 1024 && PW * (NST - 1) < 64, "");
@@ -102,7 +105,7 @@ __device__ __forceinline__ int q_dim(int s, int g) {
 }
 
 template <class G>
-__global__ __launch_bounds__(G::THREADS) void k_attn(AttnArgs a) {
+__global__ __launch_bounds__(G::THREADS, G::MINW) void k_attn(AttnArgs a) {
   typedef typename Acc<G::MT>::T acc_t;
   constexpr int AN = G::MT == 16 ? 4 : 16;
   extern __shared__ __align__(16) uint8_t lds[];
@@ -454,21 +457,48 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int D, bool KV8>
-hipError_t pick(const AttnArgs& a, hipStream_t st) {
-  return run<Geo<D, KV8, 16, 4, 1, D == 256 ? 32 : 64, 2>>(a, st);
+// The kernel for a call whose largest request has `rows` rows per kv head.
+// Up to 16 and 32 rows each wave takes all of them and a part of the keys,
+// without barriers; up to 64, two waves share the keys of two; beyond, four
+// waves of 32 rows share every key tile.  Key groups and stages fill the LDS.
+template <int D, bool KV8, class F>
+auto visit_rows(int64_t rows, F f) {
+  constexpr int WK = D == 256 && !KV8 ? 2 : 4;
+  if (rows <= 16) return f(Geo<D, KV8, 16, 1, WK, 32, 2>{});
+  if (rows <= 32) return f(Geo<D, KV8, 32, 1, WK, 32, 2>{});
+  if (rows <= 64) return f(Geo<D, KV8, 32, 2, 2, 32, 2>{});
+  return f(Geo<D, KV8, 32, 4, 1, D == 256 ? 32 : 64, 2>{});
+}
+template <class F>
+auto visit(int dim, bool e4m3, int64_t rows, F f) {
+  if (dim == 64) return e4m3 ? visit_rows<64, true>(rows, f) : visit_rows<64, false>(rows, f);
+  if (dim == 128) return e4m3 ? visit_rows<128, true>(rows, f) : visit_rows<128, false>(rows, f);
+  return e4m3 ? visit_rows<256, true>(rows, f) : visit_rows<256, false>(rows, f);
 }
 
 }  // namespace
 
-int attn_splits(int, int, int, int, int, int, int, int, int, int) { return 1; }
+// Enough workgroups for two on every CU, but no split shorter than four key
+// tiles of the longest request: a split costs a launch and the traffic of its
+// partial outputs.
+int attn_splits(int, int requests, int max_new, int max_kv, int heads, int kv_heads, int dim, int e4m3, int window,
+                int sinks) {
+  const int64_t rows = (int64_t)max_new * (heads / kv_heads);
+  int64_t keys = max_kv;
+  if (window > 0 && (int64_t)window + sinks + max_new < keys) keys = (int64_t)window + sinks + max_new;
+  return visit(dim, e4m3 != 0, rows, [&](auto geo) {
+    typedef decltype(geo) G;
+    const int64_t groups = (int64_t)requests * kv_heads * ((rows + G::ROWS - 1) / G::ROWS);
+    const int64_t want = (kTargetGroups + groups - 1) / groups, most = keys / (kMinTiles * G::TT);
+    const int64_t s = want < most ? want : most;
+    return (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+  });
+}
 
 int launch_attn(const AttnArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  hipError_t e;
-  if (a.dim == 64) e = a.e4m3 ? pick<64, true>(a, st) : pick<64, false>(a, st);
-  else if (a.dim == 128) e = a.e4m3 ? pick<128, true>(a, st) : pick<128, false>(a, st);
-  else e = a.e4m3 ? pick<256, true>(a, st) : pick<256, false>(a, st);
+  hipError_t e = visit(a.dim, a.e4m3 != 0, (int64_t)a.max_new * a.group,
+                       [&](auto geo) { return run<decltype(geo)>(a, st); });
   if (e == hipSuccess && a.splits > 1) {
     const size_t rows = (size_t)a.b.tokens * a.heads, rpb = 1024 / a.dim;
     const dim3 grid((unsigned)((rows + rpb - 1) / rpb)), block(256);
