@@ -361,8 +361,10 @@ typedef enum {
 /* A paged cache of one layer.  k_dev, v_dev: [num_pages, kv_heads, page_size,
  * head_dim] elements (bf16 or E4M3 codes) with the strides below, the same
  * for k and v: any order of the first three axes.  Strides in elements; in
- * bytes they are multiples of 16.  k_scale_dev, v_scale_dev: float
- * [num_pages, kv_heads, page_size] with strides of their own (E4M3 only).
+ * bytes they are multiples of 16, a page's below 2^32 and a head's rows of one
+ * page within 2^31.  k_scale_dev, v_scale_dev: float
+ * [num_pages, kv_heads, page_size] with strides of their own (E4M3 only; the
+ * same bounds, in elements).
  * page_size: a power of two up to 1024; head_dim 64, 128 or 256. */
 typedef struct {
   void* k_dev;

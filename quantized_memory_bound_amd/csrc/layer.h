@@ -37,8 +37,8 @@ struct CacheArgs {
   uint8_t* v;
   float* k_scale;            // E4M3 only
   float* v_scale;
-  int64_t page, head, token;       // strides in bytes
-  int64_t s_page, s_head, s_token; // scale strides in elements
+  int64_t head, s_head;            // strides: of k and v in bytes, of the scales in elements
+  uint32_t page, token, s_page, s_token;
   int num_pages, page_shift, kv_heads;
 };
 
@@ -66,19 +66,24 @@ struct AttnArgs {
   int max_new;
   BatchArgs b;
   CacheArgs c;
-  // split over the keys: partial outputs and their log2-sum-exps
-  int splits;
-  float* part_o;             // [splits][tokens][heads][dim]
-  float* part_lse;           // [splits][tokens][heads]
+  // work over the keys cut into pieces for `slots` workgroups (`groups` launched) or split `splits` ways;
+  // partial outputs and their log2-sum-exps
+  int even, splits, groups, slots;
+  float* part_o;             // [part_rows][dim]
+  float* part_lse;           // [part_rows]
+};
+
+struct AttnPlan {
+  int even, splits, groups, slots;
+  size_t part_rows;          // rows of partial outputs in the workspace
 };
 
 // each enqueues on `stream` and returns 0 or a hipError_t value
 int launch_norm(const NormArgs& a, void* stream);
 int launch_rope(const RopeArgs& a, void* stream);
 int launch_attn(const AttnArgs& a, void* stream);
-// ways the keys of one (request, kv head, row tile) are split, for a call of
-// this shape (1 = not split)
-int attn_splits(int tokens, int requests, int max_new, int max_kv, int heads, int kv_heads, int dim, int e4m3,
-                int window, int sinks);
+// layout of a call of this shape (host numbers only; cap: keys that a request's row of the page table can name)
+AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads, int kv_heads, int dim, int e4m3,
+                   int window, int sinks, int64_t cap);
 
 }  // namespace ocq

@@ -25,6 +25,7 @@ bool aligned(const void* p, uintptr_t n = 16) { return ((uintptr_t)p & (n - 1)) 
 
 // strides that keep every byte offset far from 2^63, and 16-byte aligned in units of `per16` elements
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxPage = 0xFFFFFFFFll, kMaxInPage = 0x7FFFFFFFll;
 bool stride_ok(int64_t s, int per16) { return s >= 0 && s <= kMaxStride && s % per16 == 0; }
 
 ocq_status check_cache(const ocq_kv_cache* c) {
@@ -41,12 +42,17 @@ ocq_status check_cache(const ocq_kv_cache* c) {
   const int per16 = c->format == OCQ_CACHE_E4M3 ? 16 : 8;
   if (!stride_ok(c->page_stride, per16) || !stride_ok(c->head_stride, per16) || !stride_ok(c->token_stride, per16))
     return invalid("cache strides must be multiples of 16 bytes, not negative");
+  const int64_t esz = 16 / per16;
+  if (c->page_stride * esz > kMaxPage || (c->page_size - 1) * c->token_stride * esz > kMaxInPage)
+    return unsupported("page strides must be below 2^32 bytes, a page's rows within 2^31");
   if (c->format == OCQ_CACHE_E4M3) {
     if (!c->k_scale_dev || !c->v_scale_dev) return invalid("an E4M3 cache needs scales");
     if (!aligned(c->k_scale_dev, 4) || !aligned(c->v_scale_dev, 4)) return invalid("misaligned scale pointer");
     if (!stride_ok(c->scale_page_stride, 1) || !stride_ok(c->scale_head_stride, 1) ||
         !stride_ok(c->scale_token_stride, 1))
       return invalid("scale strides must not be negative");
+    if (c->scale_page_stride > kMaxPage || (c->page_size - 1) * c->scale_token_stride > kMaxInPage)
+      return unsupported("scale page strides must be below 2^32, a page's rows within 2^31");
   }
   return OCQ_OK;
 }
@@ -79,11 +85,17 @@ CacheArgs cache_args(const ocq_kv_cache* c) {
   int shift = 0;
   while ((1 << shift) < c->page_size) ++shift;
   return CacheArgs{(uint8_t*)c->k_dev, (uint8_t*)c->v_dev, (float*)c->k_scale_dev, (float*)c->v_scale_dev,
-                   c->page_stride * esz, c->head_stride * esz, c->token_stride * esz, c->scale_page_stride,
-                   c->scale_head_stride, c->scale_token_stride, c->num_pages, shift, c->kv_heads};
+                   c->head_stride * esz, c->scale_head_stride, (uint32_t)(c->page_stride * esz),
+                   (uint32_t)(c->token_stride * esz), (uint32_t)c->scale_page_stride, (uint32_t)c->scale_token_stride,
+                   c->num_pages, shift, c->kv_heads};
 }
 
 int max_new(const ocq_token_batch* b) { return b->max_new < b->tokens ? b->max_new : b->tokens; }
+
+AttnPlan plan_of(int heads, const ocq_kv_cache* c, const ocq_token_batch* b, int window, int sinks) {
+  return attn_plan(b->tokens, b->requests, max_new(b), b->max_kv, heads, c->kv_heads, c->head_dim, c->format, window,
+                   sinks, (int64_t)b->max_pages * c->page_size);
+}
 
 // the grid of the attention launch, an upper bound over its row tiles
 bool attn_grid_ok(const ocq_token_batch* b, const ocq_kv_cache* c, int heads, int splits) {
@@ -186,9 +198,7 @@ size_t ocq_attention_workspace_bytes(int heads, const ocq_kv_cache* cache, const
   set_error(OCQ_OK, "");
   if (check_cache(cache) != OCQ_OK || check_batch(batch, cache, heads) != OCQ_OK || window < 0 || sinks < 0) return 0;
   if (batch->requests == 0 || batch->tokens == 0) return 0;
-  const int splits = attn_splits(batch->tokens, batch->requests, max_new(batch), batch->max_kv, heads,
-                                 cache->kv_heads, cache->head_dim, cache->format, window, sinks);
-  return splits <= 1 ? 0 : (size_t)splits * batch->tokens * heads * (cache->head_dim + 1) * sizeof(float);
+  return plan_of(heads, cache, batch, window, sinks).part_rows * (cache->head_dim + 1) * sizeof(float);
 }
 
 ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, int heads,
@@ -209,11 +219,9 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
     return invalid("device pointers must be 16-byte aligned");
   if (!stride_ok(q_token_stride, 8) || !stride_ok(q_head_stride, 8))
     return invalid("strides must be multiples of 8, not negative");
-  const int splits = attn_splits(batch->tokens, batch->requests, max_new(batch), batch->max_kv, heads,
-                                 cache->kv_heads, cache->head_dim, cache->format, window, sinks);
-  if (!attn_grid_ok(batch, cache, heads, splits)) return unsupported("too many row tiles for one launch");
-  const size_t rows = (size_t)batch->tokens * heads;
-  const size_t need = splits <= 1 ? 0 : (size_t)splits * rows * (cache->head_dim + 1) * sizeof(float);
+  const AttnPlan plan = plan_of(heads, cache, batch, window, sinks);
+  if (!attn_grid_ok(batch, cache, heads, plan.splits)) return unsupported("too many row tiles for one launch");
+  const size_t need = plan.part_rows * (cache->head_dim + 1) * sizeof(float);
   if (workspace_bytes < need)
     return set_error(OCQ_ERR_BUFFER_TOO_SMALL, "workspace_bytes < ocq_attention_workspace_bytes()");
   if (need && !workspace_dev) return invalid("null workspace");
@@ -233,9 +241,12 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
   a.max_new = max_new(batch);
   a.b = batch_args(batch);
   a.c = cache_args(cache);
-  a.splits = splits;
+  a.even = plan.even;
+  a.splits = plan.splits;
+  a.groups = plan.groups;
+  a.slots = plan.slots;
   a.part_o = (float*)workspace_dev;
-  a.part_lse = (float*)workspace_dev + (size_t)splits * rows * cache->head_dim;
+  a.part_lse = (float*)workspace_dev + plan.part_rows * cache->head_dim;
   const int rc = launch_attn(a, stream);
   return rc ? hip_error(rc) : OCQ_OK;
 }

@@ -62,9 +62,27 @@ OCQ_HD int table_entry(int key, int kv, int page_shift) { return (key < kv ? key
 // Whether the row of `key` may be read from page `id`.
 OCQ_HD bool row_there(int key, int kv, int id, int num_pages) { return key < kv && id >= 0 && id < num_pages; }
 
-// Offset of a key's row in the pool, without the head's part.
-OCQ_HD int64_t row_offset(int key, int id, int page_shift, int64_t page, int64_t token) {
-  return id * page + (int64_t)(key & ((1 << page_shift) - 1)) * token;
+// Offset of a key's row in the pool, without the head's part.  The entry
+// points hold page strides below 2^32 and a page's rows within 2^31.
+OCQ_HD uint64_t row_offset(int key, int id, int page_shift, uint32_t page, uint32_t token) {
+  return (uint64_t)(uint32_t)id * page + (uint32_t)(key & ((1 << page_shift) - 1)) * token;
 }
+
+// Pieces.  Where every request's rows fit one row tile, the key tiles of each
+// (request, kv head) are cut into pieces of about `per` tiles and each piece is
+// one workgroup's work: as many pieces as the GPU holds workgroups at once,
+// whatever the contexts' lengths, which only the device knows.
+// Pieces of a request with T tiles (inv = 1 / per, rounded: any error moves
+// only the number), and the tiles of piece i of c.
+OCQ_HD int piece_count(int T, float inv) {
+  const float x = (float)T * inv;
+  int c = (int)x;
+  c += (float)c < x;
+  return T <= 0 ? 0 : c < 1 ? 1 : c > T ? T : c;
+}
+OCQ_HD int piece_begin(int T, int i, int c) { return (int)((int64_t)T * i / c); }
+// Tiles per piece that are enough for `slots` pieces of `segments` segments
+// with `total` tiles in all: sum of ceil(T / per) <= total / per + segments.
+OCQ_HD int piece_bound(int total, int segments, int slots) { return total / (slots - segments) + 1; }
 
 }  // namespace ocq

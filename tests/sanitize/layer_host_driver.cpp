@@ -12,7 +12,9 @@ ocq_status set_error(ocq_status st, const char*) { return st; }
 int launch_norm(const NormArgs&, void*) { unreachable(); }
 int launch_rope(const RopeArgs&, void*) { unreachable(); }
 int launch_attn(const AttnArgs&, void*) { unreachable(); }
-int attn_splits(int, int, int, int, int, int, int, int, int, int) { return 3; }
+AttnPlan attn_plan(int tokens, int, int, int, int heads, int, int, int, int, int, int64_t) {
+  return AttnPlan{0, 3, 0, 0, (size_t)3 * tokens * heads};
+}
 }  // namespace ocq
 
 static int failed = 0;

@@ -53,8 +53,8 @@ int main() {
               const int e = table_entry(key, kv, shift);
               CHECK(e >= 0 && e < max_pages);
               if (row_there(key, kv, table[e], num_pages)) {
-                const int64_t off = row_offset(key, table[e], shift, (int64_t)1 << (shift + 20), (int64_t)1 << 20);
-                CHECK(off >= 0 && off < (int64_t)num_pages << (shift + 20));
+                const uint64_t off = row_offset(key, table[e], shift, 1u << (shift + 20), 1u << 20);
+                CHECK(off < (uint64_t)num_pages << (shift + 20));
               }
             }
         }
@@ -65,6 +65,34 @@ int main() {
           CHECK(!key_seen(kv, place, window, sinks));
         }
       }
+    }
+  }
+  // pieces: never more than tiles, none empty, and no more than the slots at
+  // the bound
+  for (int trial = 0; trial < 20000; ++trial) {
+    const int requests = 1 + below(64), kv_heads = 1 + below(8), segments = requests * kv_heads;
+    const int slots = 2 * segments + below(600);
+    std::vector<int> T(requests);
+    int total = 0;
+    for (int& x : T) {
+      x = below(4) ? 1 + below(1 << below(20)) : 0;
+      if (x > (1 << 30) / segments) x = (1 << 30) / segments;
+      total += x * kv_heads;
+    }
+    const int bound = piece_bound(total, segments, slots);
+    for (int per : {1, 1 + below(50), bound}) {
+      long long pieces = 0;
+      for (int x : T) {
+        const int c = piece_count(x, 1.0f / (float)per);
+        CHECK(c >= (x > 0) && c <= x);
+        pieces += (long long)c * kv_heads;
+        for (int k = 0; c > 0 && k < 20; ++k) {
+          const int i = below(c);
+          CHECK(piece_begin(x, i + 1, c) > piece_begin(x, i, c) && piece_begin(x, 0, c) == 0 &&
+                piece_begin(x, c, c) == x);
+        }
+      }
+      if (per == bound) CHECK(pieces <= slots);
     }
   }
   std::printf("OK (%d failed checks)\n", failed);
