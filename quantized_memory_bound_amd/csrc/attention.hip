@@ -153,17 +153,15 @@ __device__ __forceinline__ int q_dim(int s, int g) {
   else return G::KS * s + 8 * g;
 }
 
-__device__ __forceinline__ int wave_add(int v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  return v;
-}
-__device__ __forceinline__ int wave_scan(int v) {   // inclusive sums over the lanes
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int up = __shfl_up(v, o);
-    if ((int)(threadIdx.x & 63) >= o) v += up;
-  }
+// Inclusive sums over the lanes: within rows of 16 (DPP row_shr 1, 2, 4, 8),
+// then each row's last into the next rows (row_bcast 15 and 31).
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
   return v;
 }
 
@@ -196,7 +194,7 @@ __device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int of_pi
     int x, y, z;
     total += load(base, x, y, z);
   }
-  total = wave_add(total) * kvh;
+  total = __builtin_amdgcn_readlane(wave_scan(total), 63) * kvh;
   const int segments = a.b.requests * kvh;
   float per;
   if (2 * segments > a.slots) {
@@ -204,18 +202,20 @@ __device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int of_pi
     // the last ones to run are short
     per = (float)(total / (2 * a.slots) + 1);
   } else {
-    // the smallest pieces that fit the slots: 64 candidates between the mean
-    // and the bound, one per lane
+    // the smallest pieces that fit the slots: eight candidates from the mean to
+    // the bound, each summed by eight lanes
     const int lo = total / a.slots + 1, hi = piece_bound(total, segments, a.slots);
     per = (float)hi;
     if (a.b.requests <= 64) {
-      const float mine = (float)lo + (float)(hi - lo) * (float)lane * (1.0f / 63.0f);
+      const float mine = (float)lo + (float)(hi - lo) * (float)(lane >> 3) * 0.125f;
       const float inv = 1.0f / mine;
       int sum = 0;
-      for (int r = 0; r < a.b.requests; ++r) sum += piece_count(__builtin_amdgcn_readlane(T, r), inv);
-      const uint64_t fits = __ballot(sum * kvh <= a.slots) | (1ull << 63);
-      per = __shfl(mine, __builtin_ctzll(fits));
-      if (!(fits & ((1ull << 63) - 1))) per = (float)hi;
+      for (int r = lane & 7; r - (lane & 7) < a.b.requests; r += 8) sum += piece_count(__shfl(T, r), inv);
+      sum += __builtin_amdgcn_update_dpp(0, sum, 0xB1, 0xF, 0xF, false);    // lane ^ 1
+      sum += __builtin_amdgcn_update_dpp(0, sum, 0x4E, 0xF, 0xF, false);    // lane ^ 2
+      sum += __builtin_amdgcn_update_dpp(0, sum, 0x141, 0xF, 0xF, false);   // 7 - lane of each eight
+      const uint64_t fits = __ballot(sum * kvh <= a.slots);
+      if (fits) per = __shfl(mine, __builtin_ctzll(fits));
     }
   }
   per = fmaxf(per, (float)kMinTiles);
