@@ -97,10 +97,30 @@ struct Geo {
   static_assert(!KV8 || 2 * TK >= 64, "whole scale loads");
 };
 
-// Chunk swizzle of row `row`: 256 bytes of LDS hold 256 / RB rows.
+// Chunk swizzle: chunk c of row `row` lies at chunk c ^ swz(row).  What one
+// pass of the banks (256 bytes) takes has to lie in different banks:
+//   K   16 rows (16-byte reads), one chunk of each: swz takes 16 values over
+//       16 rows, or 16 RB / 256 where a pass holds several rows;
+//   V   half a wave's transposing reads: for bf16 4 rows x 4 chunks (MT 32) or
+//       8 rows x 2 chunks (MT 16) from row 0 or 4 g, for codes 4 + 4 rows KB
+//       apart x 2 chunks, or 8 + 8 rows x 1 chunk.
+// So the row bits of V's pass go to the chunk bits above those it reads
+// together.  Linear in the bits (swz(a + b) = swz(a) ^ swz(b) without carries).
 template <class G>
 __device__ __forceinline__ constexpr int swz(int row) {
-  return G::CH >= 16 ? row & 15 : G::CH == 8 ? (row >> 1) & 7 : (row >> 2) & 3;
+  const int b0 = row & 1, b1 = row >> 1 & 1, b2 = row >> 2 & 1, b3 = row >> 3 & 1, b4 = row >> 4 & 1;
+  if constexpr (!G::KV8) {
+    if constexpr (G::MT == 32)
+      return G::CH >= 16 ? b0 << 2 | b1 << 3 | b2 | b3 << 1 : b1 << 2 | b2 | b3 << 1;
+    else
+      return G::CH >= 16 ? b0 << 1 | b1 << 2 | b2 << 3 | b3 : b1 << 1 | b2 << 2 | b3;
+  } else {
+    if constexpr (G::MT == 32)
+      return G::CH >= 16 ? b0 << 1 | b1 << 2 | b3 << 3 | b2 : G::CH == 8 ? b1 << 1 | b3 << 2 | b2 : b3 << 1 | b2;
+    else
+      return G::CH >= 16 ? b0 | b1 << 1 | b2 << 2 | (b3 ^ b4) << 3
+             : G::CH == 8 ? b1 | b2 << 1 | (b3 ^ b4) << 2 : b2 | (b3 ^ b4) << 1;
+  }
 }
 
 // p, or sixteen zero bytes; chosen by selects (a branch around each load would
@@ -371,7 +391,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
 #pragma unroll
         for (int i = 0; i < AN; ++i) s[t][kt][i] = 0.0f;
       const uint8_t* kr = slot + (kt * G::MT + r) * G::RB;
-      const int f = swz<G>(r);   // MT is a multiple of the swizzle's period
+      const int f = swz<G>(r) ^ swz<G>(kt * G::MT);
       if constexpr (!G::KV8) {
         v8bf ka[G::QS];
 #pragma unroll
