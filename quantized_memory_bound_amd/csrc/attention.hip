@@ -68,33 +68,38 @@ __device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// D: head size; KV8: E4M3 cache; MT x RT: rows of a wave, RT tiles of MT; WR x
-// WK waves: over the rows and over the keys; TK: keys of a wave's stage; NST:
-// stages; MINW: waves per SIMD that the registers leave room for.
-template <int D_, bool KV8_, int MT_, int RT_, int WR_, int WK_, int TK_, int NST_, int MINW_>
+// D: head size; KV8: E4M3 cache; MT: rows of a wave; WR x
+// WK waves: over the rows and over the keys; TK: keys of a wave's stage; MINW:
+// waves per SIMD that the registers leave room for.  NST: slots of each ring;
+// two, so that the loop over the stages, unrolled by two, has every LDS address
+// as a register that does not change plus a constant.
+template <int D_, bool KV8_, int MT_, int WR_, int WK_, int TK_, int MINW_>
 struct Geo {
-  static constexpr int RT = RT_, MINW = MINW_;
-  static constexpr int D = D_, MT = MT_, WR = WR_, WK = WK_, TK = TK_, NST = NST_;
+  static constexpr int MINW = MINW_, NST = 2;
+  static constexpr int D = D_, MT = MT_, WR = WR_, WK = WK_, TK = TK_;
   static constexpr bool KV8 = KV8_;
-  static constexpr int NW = WR * WK, THREADS = 64 * NW, ROWS = MT * RT * WR;
+  static constexpr int NW = WR * WK, THREADS = 64 * NW, ROWS = MT * WR;
   static constexpr int ESZ = KV8 ? 1 : 2, RB = D * ESZ, CH = RB / 16;   // bytes and chunks of a row
   static constexpr int PART = TK * RB;                                  // K (or V) bytes of a key group's stage
-  static constexpr int SCB = KV8 ? 2 * TK * 4 : 0;                      // its scales, K's then V's
-  static constexpr int IDO = 2 * PART + SCB, STG = IDO + 256, RING = WK * NST * STG;   // 64 page ids at IDO
+  static constexpr int SCB = KV8 ? 256 : 0;                             // its scales
+  static constexpr int KSTG = PART + SCB + 256, VSTG = PART + SCB;      // a stage of K (with 64 page ids) and of V
+  static constexpr int RING = WK * NST * (KSTG + VSTG);
   static constexpr int QI = PART / 1024 / WR;                           // K (or V) loads per wave and stage
-  static constexpr int SI = KV8 ? (2 * TK / 64 + WR - 1) / WR : 0;      // scale loads per wave and stage
-  static constexpr int PW = 2 * QI + SI + 1;
+  static constexpr int PW = 2 * QI + 1 + (KV8 ? 2 : 0);                 // all loads per wave and stage
+  static constexpr int AHEAD = WR > 1 ? NST - 1 : NST;                  // stages on their way, see the ring
   static constexpr int TT = TK * WK;                                    // keys of a tile, all key groups
   static constexpr int NKT = TK / MT;                                   // key tiles of a stage
   static constexpr int KS = 512 / MT;                                   // inputs of one MFMA (32 or 16)
   static constexpr int QS = D / KS, DT = D / MT, LG = 64 / MT;          // steps of S, tiles of O, lane groups
   static constexpr int PS = TK / KS;                                    // steps of O
-  static constexpr int JOIN = WK > 1 ? WK * ROWS * (D * 4 + 8) : 0;
+  static constexpr int SO = D + 4;                                      // floats of a joined row: 16 bytes further per row
+  static constexpr int JOIN = WK > 1 ? WK * ROWS * (SO * 4 + 8) : 0;
   static constexpr int LDS = RING > JOIN ? RING : JOIN;
   static constexpr bool EVEN = ROWS <= 64;                              // see layer_index.h, pieces
-  static constexpr int RESIDENT = 256 * (MINW > 1 && LDS <= 78 * 1024 ? 2 : 1);   // workgroups at once, 256 CUs
-  static_assert(PART % (1024 * WR) == 0 && TK % 32 == 0 && LDS <= 160 * 1024 && PW * (WR > 1 ? NST - 2 : NST - 1) < 64, "");
-  static_assert(!KV8 || 2 * TK >= 64, "whole scale loads");
+  static constexpr int PER_CU = 160 * 1024 / (LDS + 1024) < 4 * MINW / NW ? 160 * 1024 / (LDS + 1024) : 4 * MINW / NW;
+  static constexpr int RESIDENT = 256 * (PER_CU > 0 ? PER_CU : 1);      // workgroups at once, 256 CUs
+  static_assert(PART % (1024 * WR) == 0 && TK % 32 == 0 && LDS <= 160 * 1024, "");
+  static_assert(TK <= 64, "one load for the ids, and for the scales");
 };
 
 // Chunk swizzle: chunk c of row `row` lies at chunk c ^ swz(row).  What one
@@ -123,12 +128,15 @@ __device__ __forceinline__ constexpr int swz(int row) {
   }
 }
 
-// p, or sixteen zero bytes; chosen by selects (a branch around each load would
-// cost more than the load)
-__device__ __forceinline__ const void* ok_or_zero(bool ok, const void* p) {
-  uint64_t u = ok ? (uint64_t)p : (uint64_t)g_zero;
-  asm("" : "+v"(u));
-  return (const void*)u;
+// 16 (or 4) bytes from p for each lane to LDS, lane after lane from `to`.  The
+// address is a chosen one, not a branch to one of two loads.
+__device__ __forceinline__ void dma16(uint64_t p, uint8_t* to) {
+  asm("" : "+v"(p));
+  __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)to, 16, 0, 0);
+}
+__device__ __forceinline__ void dma4(uint64_t p, uint8_t* to) {
+  asm("" : "+v"(p));
+  __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)to, 4, 0, 0);
 }
 
 // Four V^T fragments (eight keys of one d per lane each) through the
@@ -286,83 +294,84 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   const int n = pc.n, t0 = pc.t0, kv = pc.kv, base = pc.base, row0 = pc.row0, kvh = pc.kvh;
   const int p_lo = pc.p_lo, p_hi = pc.p_hi, ns = pc.s1 - pc.s0;
 
-  // this lane's rows
-  const int rl0 = wr * G::MT * G::RT + r;                    // in the tile; the next ones MT apart
-  int place[G::RT];
-  size_t at[G::RT];                                         // row of the output
-  v8bf q[G::RT][G::QS];
+  // this lane's row: in the tile, of the request, of the output
+  const int rl = wr * G::MT + r, row = row0 + rl;
+  const bool live = row < n * a.group;
+  const int tok = live ? row / a.group : 0, head = kvh * a.group + (live ? row % a.group : 0);
+  const int place = live ? base + tok : -1;
+  const size_t at = (size_t)(t0 + tok) * a.heads + head;
+  v8bf q[G::QS];
+  const uint16_t* qp = a.q + (t0 + tok) * a.q_token + head * a.q_head;
 #pragma unroll
-  for (int t = 0; t < G::RT; ++t) {
-    const int row = row0 + rl0 + t * G::MT;
-    const bool live = row < n * a.group;
-    const int tok = live ? row / a.group : 0, head = kvh * a.group + (live ? row % a.group : 0);
-    place[t] = live ? base + tok : -1;
-    at[t] = (size_t)(t0 + tok) * a.heads + head;
-    const uint16_t* qp = a.q + (t0 + tok) * a.q_token + head * a.q_head;
-#pragma unroll
-    for (int s = 0; s < G::QS; ++s) {
-      const v4i u = live ? *(const v4i*)(qp + q_dim<G>(s, g)) : v4i{0, 0, 0, 0};
-      q[t][s] = __builtin_bit_cast(v8bf, u);
-    }
+  for (int s = 0; s < G::QS; ++s) {
+    const v4i u = live ? *(const v4i*)(qp + q_dim<G>(s, g)) : v4i{0, 0, 0, 0};
+    q[s] = __builtin_bit_cast(v8bf, u);
   }
   const float c = a.scale * kLog2e;
 
-  // ---- loads: rows of this wave's part of its key group's stage
-  uint8_t* const ring = lds + wk * (G::NST * G::STG);
+  // ---- loads: rows of this wave's part of its key group's stage.  V of a stage
+  // goes after K of it, with the same offsets.
+  uint8_t* const ring = lds + wk * G::RING / G::WK;
+  auto k_slot = [](int i) constexpr { return i * G::KSTG; };                       // offsets in the ring
+  auto v_slot = [](int i) constexpr { return G::NST * G::KSTG + i * G::VSTG; };
   const int32_t* const table = a.b.table + pc.req * a.b.table_stride;
-  const uint8_t* const k_head = a.c.k + kvh * a.c.head;
-  const uint8_t* const v_head = a.c.v + kvh * a.c.head;
-  const float* const ks_head = a.c.k_scale + (G::KV8 ? kvh * a.c.s_head : 0);
-  const float* const vs_head = a.c.v_scale + (G::KV8 ? kvh * a.c.s_head : 0);
-  // first key of the wave's key group in stage st
+  const int page_mask = (1 << a.c.page_shift) - 1;
+  const uint64_t k_head = (uint64_t)a.c.k + kvh * a.c.head, v_less_k = (uint64_t)a.c.v - (uint64_t)a.c.k;
+  const uint64_t ks_head = (uint64_t)(a.c.k_scale + (G::KV8 ? kvh * a.c.s_head : 0));
+  const uint64_t vs_less_ks = (uint64_t)a.c.v_scale - (uint64_t)a.c.k_scale;
+  // first key of the wave's key group in stage st: a multiple of TK, so that a
+  // row's place in its page is that of the first key plus a part of its own
   auto tile_key = [&](int st) { return tile_of(pc.tiles, pc.s0 + st) * G::TT + wk * G::TK; };
-  constexpr int AHEAD = G::WR > 1 ? G::NST - 1 : G::NST;   // stages on their way, see the ring below
-  auto q_row = [&](int i) { return ((i * G::WR + wr) * 64 + lane) / G::CH; };          // row of load i
-  auto sc_key = [&](int i) { return (((i * G::WR + wr) * 64 + lane) % (2 * G::TK)) % G::TK; };   // key of scale load i
-  // Page ids come with the stage AHEAD before the one that they are for: a
+  auto q_row = [&](int i) { return ((i * G::WR + wr) * 64 + lane) / G::CH; };   // row of load i
+  uint32_t part[G::QI];
+#pragma unroll
+  for (int i = 0; i < G::QI; ++i) {
+    const int rw = q_row(i), lin = ((i * G::WR + wr) * 64 + lane) % G::CH;
+    part[i] = (rw & page_mask) * a.c.token + ((lin ^ swz<G>(rw)) << 4);
+  }
+  const uint32_t s_part = (lane % G::TK & page_mask) * a.c.s_token * 4;
+  const uint64_t zero = (uint64_t)g_zero;
+  uint64_t src[G::QI], s_src = 0;   // rows of the last K stage issued
+  bool there[G::QI], s_there = false;
+  // Page ids come with the K stage AHEAD before the one that they are for: a
   // load into registers would have to be waited for together with every
   // earlier load of the wave.
   auto entry = [&](int st, int row) { return table + table_entry(tile_key(st) + row, kv, a.c.page_shift); };
-  auto issue = [&](int st, uint8_t* slot, auto id_of) {
+  auto issue_k = [&](int st, int slot, auto id_of) {
     const int key0 = tile_key(st);
-    int ids[G::QI + G::SI];
+    int ids[G::QI], sid = 0;
 #pragma unroll
-    for (int i = 0; i < G::QI + G::SI; ++i) ids[i] = id_of(i < G::QI ? q_row(i) : sc_key(i - G::QI));
-    const int later = st + AHEAD < ns ? st + AHEAD : st;
-    __builtin_amdgcn_global_load_lds((const void*)entry(later, lane % G::TK), (lds_void*)(slot + G::IDO), 4, 0, 0);
+    for (int i = 0; i < G::QI; ++i) ids[i] = id_of(q_row(i));
+    if constexpr (G::KV8) sid = id_of(lane % G::TK);
+    uint8_t* const to = ring + slot;
+    dma4((uint64_t)entry(st + G::AHEAD < ns ? st + G::AHEAD : st, lane % G::TK), to + G::PART + G::SCB);
+    const uint64_t first = k_head + (uint32_t)(key0 & page_mask) * a.c.token;
 #pragma unroll
     for (int i = 0; i < G::QI; ++i) {
-      const int rw = q_row(i), key = key0 + rw, lin = ((i * G::WR + wr) * 64 + lane) % G::CH;
-      const bool ok = row_there(key, kv, ids[i], a.c.num_pages);
-      const uint64_t off = row_offset(key, ids[i], a.c.page_shift, a.c.page, a.c.token) + ((lin ^ swz<G>(rw)) << 4);
-      uint8_t* dst = slot + (i * G::WR + wr) * 1024;
-      __builtin_amdgcn_global_load_lds(ok_or_zero(ok, k_head + off), (lds_void*)dst, 16, 0, 0);
-      __builtin_amdgcn_global_load_lds(ok_or_zero(ok, v_head + off), (lds_void*)(dst + G::PART), 16, 0, 0);
+      there[i] = row_there(key0 + q_row(i), kv, ids[i], a.c.num_pages);
+      src[i] = first + (uint64_t)(uint32_t)ids[i] * a.c.page + part[i];
+      dma16(there[i] ? src[i] : zero, to + (i * G::WR + wr) * 1024);
     }
     if constexpr (G::KV8) {
-#pragma unroll
-      for (int i = 0; i < G::SI; ++i) {
-        const int lin = ((i * G::WR + wr) * 64) % (2 * G::TK);   // where this load's 64 scales go
-        const int key = key0 + sc_key(i);
-        const bool ok = row_there(key, kv, ids[G::QI + i], a.c.num_pages);
-        const uint64_t off = row_offset(key, ids[G::QI + i], a.c.page_shift, a.c.s_page, a.c.s_token);
-        const float* src = (lin + lane >= G::TK ? vs_head : ks_head) + off;
-        __builtin_amdgcn_global_load_lds(ok_or_zero(ok, src), (lds_void*)(slot + 2 * G::PART + lin * 4), 4, 0, 0);
-      }
+      s_there = row_there(key0 + lane % G::TK, kv, sid, a.c.num_pages);
+      s_src = ks_head + (uint64_t)(uint32_t)(key0 & page_mask) * a.c.s_token * 4 +
+              (uint64_t)(uint32_t)sid * a.c.s_page * 4 + s_part;
+      dma4(s_there ? s_src : zero, to + G::PART);
     }
   };
+  auto issue_v = [&](int slot) {
+    uint8_t* const to = ring + slot;
+#pragma unroll
+    for (int i = 0; i < G::QI; ++i) dma16(there[i] ? src[i] + v_less_k : zero, to + (i * G::WR + wr) * 1024);
+    if constexpr (G::KV8) dma4(s_there ? s_src + vs_less_ks : zero, to + G::PART);
+  };
 
-  acc_t o[G::RT][G::DT];
-  float m[G::RT], l[G::RT];
+  acc_t o[G::DT];
+  float m = kLow, l = 0.0f;
 #pragma unroll
-  for (int t = 0; t < G::RT; ++t) {
-    m[t] = kLow;
-    l[t] = 0.0f;
+  for (int d = 0; d < G::DT; ++d)
 #pragma unroll
-    for (int d = 0; d < G::DT; ++d)
-#pragma unroll
-      for (int i = 0; i < AN; ++i) o[t][d][i] = 0.0f;
-  }
+    for (int i = 0; i < AN; ++i) o[d][i] = 0.0f;
 
   // where the lane's part of a V^T fragment lies in a stage: tile d of the
   // output, keys kb + 4 g + {0..3} (first half) and kb + KB + 4 g + {0..3}
@@ -376,126 +385,118 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
       for (int h = 0; h < (G::KV8 ? 1 : 2); ++h) {
         const int key = G::KV8 ? (i16 >> 3) * KB + 4 * g + ((i16 >> 1) & 3) : h * KB + 4 * g + (i16 >> 2);
         const int ch = G::KV8 ? (d * G::MT + dh) / 16 : (d * G::MT + dh) / 8 + ((i16 >> 1) & 1);
-        v_off[d][h] = key * G::RB + ((ch ^ swz<G>(key)) << 4) + 8 * (i16 & 1);
+        v_off[d][h] = (uint32_t)(uintptr_t)(lds_void*)ring + key * G::RB + ((ch ^ swz<G>(key)) << 4) + 8 * (i16 & 1);
       }
   }
 
-  // ---- one stage
-  auto compute = [&](int st, const uint8_t* slot) {
-    const int key0 = tile_key(st);
-    acc_t s[G::RT][G::NKT];
+  // ---- one stage: S^T = K Q^T
+  typedef acc_t scores[G::NKT];
+  uint32_t k_off[G::KV8 ? G::QS / 2 : G::QS];   // the lane's part of the K fragments, key tile 0
+#pragma unroll
+  for (int x = 0; x < (G::KV8 ? G::QS / 2 : G::QS); ++x)
+    k_off[x] = r * G::RB + (((x * G::LG + g) ^ swz<G>(r)) << 4);
+  auto products = [&](auto slot_c, scores& s) {
+    constexpr int slot = decltype(slot_c)::value;
 #pragma unroll
     for (int kt = 0; kt < G::NKT; ++kt) {
 #pragma unroll
-      for (int t = 0; t < G::RT; ++t)
-#pragma unroll
-        for (int i = 0; i < AN; ++i) s[t][kt][i] = 0.0f;
-      const uint8_t* kr = slot + (kt * G::MT + r) * G::RB;
-      const int f = swz<G>(r) ^ swz<G>(kt * G::MT);
+      for (int i = 0; i < AN; ++i) s[kt][i] = 0.0f;
+      // (swz of the tile's first row is not 0 in the E4M3 layouts of 16-row tiles)
+      const int at = slot + kt * G::MT * G::RB, f = swz<G>(kt * G::MT) << 4;
       if constexpr (!G::KV8) {
-        v8bf ka[G::QS];
 #pragma unroll
-        for (int x = 0; x < G::QS; ++x) ka[x] = *(const v8bf*)(kr + (((x * G::LG + g) ^ f) << 4));
-        __builtin_amdgcn_sched_barrier(0);   // every read on its way before the first product waits
-#pragma unroll
-        for (int x = 0; x < G::QS; ++x)
-#pragma unroll
-          for (int t = 0; t < G::RT; ++t) s[t][kt] = mfma(ka[x], q[t][x], s[t][kt]);
+        for (int x = 0; x < G::QS; ++x) {
+          const v8bf ka = *(const v8bf*)(ring + at + (k_off[x] ^ f));
+          s[kt] = mfma(ka, q[x], s[kt]);
+        }
       } else {
-        v4i ku[G::QS / 2];
-#pragma unroll
-        for (int x = 0; x < G::QS; x += 2) ku[x / 2] = *(const v4i*)(kr + (((x / 2 * G::LG + g) ^ f) << 4));
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int x = 0; x < G::QS; x += 2) {
-          const v4i u = ku[x / 2];
+          const v4i u = *(const v4i*)(ring + at + (k_off[x / 2] ^ f));
           const v8bf k0 = e4m3x8_to_bf16(u[0], u[1]), k1 = e4m3x8_to_bf16(u[2], u[3]);
-#pragma unroll
-          for (int t = 0; t < G::RT; ++t) {
-            s[t][kt] = mfma(k0, q[t][x], s[t][kt]);
-            s[t][kt] = mfma(k1, q[t][x + 1], s[t][kt]);
-          }
+          s[kt] = mfma(k0, q[x], s[kt]);
+          s[kt] = mfma(k1, q[x + 1], s[kt]);
         }
       }
     }
-    const float* sc = (const float*)(slot + 2 * G::PART);
-    const bool whole = key0 + G::TK - 1 <= p_lo && (a.window <= 0 || key0 > p_hi - a.window);
-    uint32_t p[G::RT][G::NKT * AN / 2];
-#pragma unroll
-    for (int t = 0; t < G::RT; ++t) {
+  };
+  // the keys' scales and the mask
+  auto finish = [&](int st, auto slot_c, scores& s) {
+    const int key0 = tile_key(st);
+    const float* sc = (const float*)(ring + decltype(slot_c)::value + G::PART);
+    if constexpr (G::KV8) {
 #pragma unroll
       for (int kt = 0; kt < G::NKT; ++kt)
 #pragma unroll
         for (int i4 = 0; i4 < AN / 4; ++i4) {
-          const int kk = kt * G::MT + 8 * i4 + 4 * g;   // first of four keys
-          v4f ks = {1.0f, 1.0f, 1.0f, 1.0f};
-          if constexpr (G::KV8) ks = *(const v4f*)(sc + kk);
+          const v4f ks = *(const v4f*)(sc + kt * G::MT + 8 * i4 + 4 * g);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = s[t][kt][4 * i4 + i];
-            if constexpr (G::KV8) x *= ks[i];
-            s[t][kt][4 * i4 + i] = x;
-          }
-        }
-      if (!whole) {
-#pragma unroll
-        for (int kt = 0; kt < G::NKT; ++kt)
-#pragma unroll
-          for (int i = 0; i < AN; ++i) {
-            const int j = key0 + kt * G::MT + 8 * (i >> 2) + 4 * g + (i & 3);
-            s[t][kt][i] = key_seen(j, place[t], a.window, a.sinks) ? s[t][kt][i] : -__builtin_inff();
-          }
-      }
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int kt = 0; kt < G::NKT; ++kt)
-#pragma unroll
-        for (int i = 0; i < AN; ++i) top = fmaxf(top, s[t][kt][i]);
-      // scores in the exponent of 2 from here on: c s - m
-      if (__any(top * c > m[t] + kSlack)) {
-        float nm = top * c;
-#pragma unroll
-        for (int x = G::MT; x < 64; x <<= 1) nm = fmaxf(nm, __shfl_xor(nm, x));
-        nm = fmaxf(nm, m[t]);
-        const float f = __builtin_amdgcn_exp2f(m[t] - nm);
-        m[t] = nm;
-        l[t] *= f;
-#pragma unroll
-        for (int d = 0; d < G::DT; ++d)
-#pragma unroll
-          for (int i = 0; i < AN; ++i) o[t][d][i] *= f;
-      }
-#pragma unroll
-      for (int kt = 0; kt < G::NKT; ++kt)
-#pragma unroll
-        for (int i4 = 0; i4 < AN / 4; ++i4) {
-          float e[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][kt][4 * i4 + i], c, -m[t]));
-            l[t] += e[i];
-          }
-          if constexpr (G::KV8) {
-            const v4f vs = *(const v4f*)(sc + G::TK + kt * G::MT + 8 * i4 + 4 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] *= vs[i];
-          }
-          p[t][(kt * AN + 4 * i4) / 2] = pack_bf16(e[0], e[1]);
-          p[t][(kt * AN + 4 * i4) / 2 + 1] = pack_bf16(e[2], e[3]);
+          for (int i = 0; i < 4; ++i) s[kt][4 * i4 + i] *= ks[i];
         }
     }
+    if (key0 + G::TK - 1 > p_lo || (a.window > 0 && key0 <= p_hi - a.window)) {
+      asm volatile("");   // a branch, not selects in every stage
+#pragma unroll
+      for (int kt = 0; kt < G::NKT; ++kt)
+#pragma unroll
+        for (int i = 0; i < AN; ++i) {
+          const int j = key0 + kt * G::MT + 8 * (i >> 2) + 4 * g + (i & 3);
+          s[kt][i] = key_seen(j, place, a.window, a.sinks) ? s[kt][i] : -__builtin_inff();
+        }
+    }
+  };
+  // Stage st from its scores sa: the maximum, then the probabilities while the
+  // products of the next stage (into sb) run on the matrix cores, then O.
+  auto step = [&](auto k_next, auto v_at, scores& sa, scores& sb) {
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int kt = 0; kt < G::NKT; ++kt)
+#pragma unroll
+      for (int i = 0; i < AN; ++i) top = fmaxf(top, sa[kt][i]);
+    // scores in the exponent of 2 from here on: c s - m
+    if (__any(top * c > m + kSlack)) {
+      float nm = top * c;
+#pragma unroll
+      for (int x = G::MT; x < 64; x <<= 1) nm = fmaxf(nm, __shfl_xor(nm, x));
+      nm = fmaxf(nm, m);
+      const float f = __builtin_amdgcn_exp2f(m - nm);
+      m = nm;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < G::DT; ++d)
+#pragma unroll
+        for (int i = 0; i < AN; ++i) o[d][i] *= f;
+    }
+    products(k_next, sb);
+    const float* sc = (const float*)(ring + decltype(v_at)::value + G::PART);
+    uint32_t p[G::NKT * AN / 2];
+#pragma unroll
+    for (int kt = 0; kt < G::NKT; ++kt)
+#pragma unroll
+      for (int i4 = 0; i4 < AN / 4; ++i4) {
+        v4f vs = {1.0f, 1.0f, 1.0f, 1.0f};
+        if constexpr (G::KV8) vs = *(const v4f*)(sc + kt * G::MT + 8 * i4 + 4 * g);
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sa[kt][4 * i4 + i], c, -m));
+          l += e[i];
+          if constexpr (G::KV8) e[i] *= vs[i];
+        }
+        p[(kt * AN + 4 * i4) / 2] = pack_bf16(e[0], e[1]);
+        p[(kt * AN + 4 * i4) / 2 + 1] = pack_bf16(e[2], e[3]);
+      }
     // O^T += V^T P^T, four fragments (step x of the keys, tile d of the output) at a time
-    const uint32_t sb = (uint32_t)(uintptr_t)(lds_void*)slot;
     unrolled<G::PS * G::DT / 4>([&](auto blk) {
       constexpr int F0 = 4 * decltype(blk)::value;
-      auto off = [](int f) constexpr { return G::PART + f / G::DT * G::KS * G::RB; };
+      auto at_key = [](int f) constexpr { return decltype(v_at)::value + f / G::DT * G::KS * G::RB; };
       v8bf va[4];
       if constexpr (!G::KV8) {
         uint32_t ad[8];
         v2i x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ad[j] = sb + v_off[(F0 + j / 2) % G::DT][j & 1];
-        read_tr16<off(F0), off(F0 + 1), off(F0 + 2), off(F0 + 3)>(x, ad);
+        for (int j = 0; j < 8; ++j) ad[j] = v_off[(F0 + j / 2) % G::DT][j & 1];
+        read_tr16<at_key(F0), at_key(F0 + 1), at_key(F0 + 2), at_key(F0 + 3)>(x, ad);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           va[j] = __builtin_bit_cast(v8bf, __builtin_shufflevector(x[2 * j], x[2 * j + 1], 0, 1, 2, 3));
@@ -503,8 +504,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
         uint32_t ad[4];
         v2i x[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ad[j] = sb + v_off[(F0 + j) % G::DT][0];
-        read_tr8<off(F0), off(F0 + 1), off(F0 + 2), off(F0 + 3)>(x, ad);
+        for (int j = 0; j < 4; ++j) ad[j] = v_off[(F0 + j) % G::DT][0];
+        read_tr8<at_key(F0), at_key(F0 + 1), at_key(F0 + 2), at_key(F0 + 3)>(x, ad);
 #pragma unroll
         for (int j = 0; j < 4; ++j) va[j] = e4m3x8_to_bf16((uint32_t)x[j][0], (uint32_t)x[j][1]);
       }
@@ -512,96 +513,109 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
       for (int j = 0; j < 4; ++j) {
         constexpr int DT = G::DT;
         const int x = (F0 + j) / DT, d = (F0 + j) % DT;
-#pragma unroll
-        for (int t = 0; t < G::RT; ++t) {
-          const v8bf pb = __builtin_bit_cast(
-              v8bf, (v4i{(int)p[t][4 * x], (int)p[t][4 * x + 1], (int)p[t][4 * x + 2], (int)p[t][4 * x + 3]}));
-          o[t][d] = mfma(va[j], pb, o[t][d]);
-        }
+        const v8bf pb = __builtin_bit_cast(
+            v8bf, (v4i{(int)p[4 * x], (int)p[4 * x + 1], (int)p[4 * x + 2], (int)p[4 * x + 3]}));
+        o[d] = mfma(va[j], pb, o[d]);
       }
     });
   };
 
-  // ---- the ring.  Waves that share a stage meet once for it: then its loads
-  // have landed and stage st - 1 is done with, so stage st + NST - 1 goes where
-  // that was.  A wave alone refills a slot as soon as it has read it, so that
-  // NST stages are on their way while it waits.
+  // ---- the rings.  Iteration st takes V of stage st and K of stage st + 1 (the
+  // last one multiplies a K that nobody uses).  Waves that share a stage meet
+  // once per iteration: then its loads have landed, K of stage st and V of stage
+  // st - 1 are done with, and the stages AHEAD of it go where they were.  A wave
+  // alone refills a slot as soon as it has read it.  Loads are issued in the
+  // order K 0, V 0, K 1, V 1, K 2, ...
   if (ns > 0) {
+    constexpr auto most = [](int n) constexpr { return n < 63 ? n : 63; };
+    auto held = [&](int slot) {   // page ids that came with the K stage in `slot`
+      return [&, slot](int row) { return *(const int*)(ring + slot + G::PART + G::SCB + 4 * row); };
+    };
 #pragma unroll
-    for (int st = 0; st < AHEAD; ++st)
-      if (st < ns) issue(st, ring + st * G::STG, [&](int row) { return *entry(st, row); });
-    int slot = 0;
-    for (int st = 0; st < ns; ++st) {
-      uint8_t* const at_st = ring + slot * G::STG;
-      // stage st has landed once at most the later ones' loads are outstanding
-      if (st + AHEAD - 1 < ns) wait_vm<(AHEAD - 1) * G::PW>();
+    for (int st = 0; st < G::NST; ++st)
+      if (st < ns) {
+        if (st > 0) issue_v(v_slot(st - 1));
+        issue_k(st, k_slot(st), [&](int row) { return *entry(st, row); });
+      }
+    if (ns < G::NST) issue_v(v_slot(0));
+    if (G::NST <= ns) wait_vm<most((G::NST - 1) * G::PW)>();
+    else wait_vm<0>();
+    if constexpr (G::WR > 1) lds_barrier();
+    else asm volatile("" ::: "memory");
+    scores s0, s1;
+    products(std::integral_constant<int, k_slot(0)>{}, s0);
+    finish(0, std::integral_constant<int, k_slot(0)>{}, s0);
+    if constexpr (G::WR == 1) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (G::NST <= ns) issue_v(v_slot(1));
+      if (G::NST < ns) issue_k(G::NST, k_slot(0), held(k_slot(0)));
+    }
+    // stage st, whose slots are i = st % 2; the next one's are 1 - i
+    auto iterate = [&](int st, auto parity, scores& sa, scores& sb) {
+      constexpr int i = decltype(parity)::value, j = 1 - i;
+      // the later stages' loads may be outstanding
+      if (st + G::AHEAD < ns) wait_vm<most((G::AHEAD - 1) * G::PW)>();
       else wait_vm<0>();
-      auto next = [&](uint8_t* to) {
-        issue(st + AHEAD, to, [&](int row) { return *(const int*)(at_st + G::IDO + 4 * row); });
+      auto refill = [&](int k_to, int v_to) {
+        if (st + G::AHEAD < ns) issue_v(v_to);
+        if (st + 1 + G::AHEAD < ns) issue_k(st + 1 + G::AHEAD, k_to, held(k_slot(j)));
       };
       if constexpr (G::WR > 1) {
         lds_barrier();
-        if (st + AHEAD < ns) next(ring + (slot == 0 ? G::NST - 1 : slot - 1) * G::STG);
-        compute(st, at_st);
+        refill(k_slot(i), v_slot(j));
       } else {
         asm volatile("" ::: "memory");
-        compute(st, at_st);
-        if (st + AHEAD < ns) {
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          next(at_st);
-        }
       }
-      slot = slot + 1 == G::NST ? 0 : slot + 1;
+      step(std::integral_constant<int, k_slot(j)>{}, std::integral_constant<int, v_slot(i)>{}, sa, sb);
+      if (st + 1 < ns) finish(st + 1, std::integral_constant<int, k_slot(j)>{}, sb);
+      if constexpr (G::WR == 1) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        refill(k_slot(j), v_slot(i));
+      }
+    };
+    for (int st = 0; st < ns; st += 2) {
+      iterate(st, std::integral_constant<int, 0>{}, s0, s1);
+      if (st + 1 < ns) iterate(st + 1, std::integral_constant<int, 1>{}, s1, s0);
     }
   }
 
   // ---- join the lane groups' sums and the key groups' parts, and write
 #pragma unroll
-  for (int t = 0; t < G::RT; ++t)
-#pragma unroll
-    for (int x = G::MT; x < 64; x <<= 1) l[t] += __shfl_xor(l[t], x);
+  for (int x = G::MT; x < 64; x <<= 1) l += __shfl_xor(l, x);
   // where row rl of the tile (row `at` of the output) goes if it is a part
   auto part_at = [&](int rl, size_t at) { return pc.part + (a.even ? (size_t)rl : at); };
   if constexpr (G::WK == 1) {
+    if (!live) return;
+    const float inv = l > 0.0f ? 1.0f / l : l;   // l: 0, or NaN kept
+    const float lse2 = l == 0.0f ? -__builtin_inff() : m + __builtin_amdgcn_logf(l);
+    const size_t ps = part_at(rl, at);
 #pragma unroll
-    for (int t = 0; t < G::RT; ++t) {
-      if (row0 + rl0 + t * G::MT >= n * a.group) continue;
-      const float inv = l[t] > 0.0f ? 1.0f / l[t] : l[t];   // l: 0, or NaN kept
-      const float lse2 = l[t] == 0.0f ? -__builtin_inff() : m[t] + __builtin_amdgcn_logf(l[t]);
-      const size_t ps = part_at(rl0 + t * G::MT, at[t]);
+    for (int d = 0; d < G::DT; ++d)
 #pragma unroll
-      for (int d = 0; d < G::DT; ++d)
-#pragma unroll
-        for (int i4 = 0; i4 < AN / 4; ++i4) {
-          const int d4 = d * G::MT + 8 * i4 + 4 * g;
-          const v4f y = {o[t][d][4 * i4] * inv, o[t][d][4 * i4 + 1] * inv, o[t][d][4 * i4 + 2] * inv,
-                         o[t][d][4 * i4 + 3] * inv};
-          if (pc.direct)
-            *(v2i*)(a.out + at[t] * G::D + d4) = v2i{(int)pack_bf16(y[0], y[1]), (int)pack_bf16(y[2], y[3])};
-          else if (ns > 0)
-            *(v4f*)(a.part_o + ps * G::D + d4) = y;
-        }
-      if (g == 0 && pc.direct && a.lse) a.lse[at[t]] = lse2 * kLn2;
-      if (g == 0 && !pc.direct) a.part_lse[ps] = lse2;
-    }
-  } else {
-    float* const so = (float*)lds;                          // [WK][ROWS][D]
-    float* const sm = so + G::WK * G::ROWS * G::D;          // [2][WK][ROWS]: m, l
-    __syncthreads();                                        // the ring is no longer read
-#pragma unroll
-    for (int t = 0; t < G::RT; ++t) {
-      const int rl = rl0 + t * G::MT;
-      if (g == 0) {
-        sm[wk * G::ROWS + rl] = m[t];
-        sm[(G::WK + wk) * G::ROWS + rl] = l[t];
+      for (int i4 = 0; i4 < AN / 4; ++i4) {
+        const int d4 = d * G::MT + 8 * i4 + 4 * g;
+        const v4f y = {o[d][4 * i4] * inv, o[d][4 * i4 + 1] * inv, o[d][4 * i4 + 2] * inv, o[d][4 * i4 + 3] * inv};
+        if (pc.direct)
+          *(v2i*)(a.out + at * G::D + d4) = v2i{(int)pack_bf16(y[0], y[1]), (int)pack_bf16(y[2], y[3])};
+        else if (ns > 0)
+          *(v4f*)(a.part_o + ps * G::D + d4) = y;
       }
-#pragma unroll
-      for (int d = 0; d < G::DT; ++d)
-#pragma unroll
-        for (int i4 = 0; i4 < AN / 4; ++i4)
-          *(v4f*)(so + (wk * G::ROWS + rl) * G::D + d * G::MT + 8 * i4 + 4 * g) =
-              v4f{o[t][d][4 * i4], o[t][d][4 * i4 + 1], o[t][d][4 * i4 + 2], o[t][d][4 * i4 + 3]};
+    if (g == 0 && pc.direct && a.lse) a.lse[at] = lse2 * kLn2;
+    if (g == 0 && !pc.direct) a.part_lse[ps] = lse2;
+  } else {
+    float* const so = (float*)lds;                          // [WK][ROWS][SO]
+    float* const sm = so + G::WK * G::ROWS * G::SO;         // [2][WK][ROWS]: m, l
+    __syncthreads();                                        // the ring is no longer read
+    if (g == 0) {
+      sm[wk * G::ROWS + rl] = m;
+      sm[(G::WK + wk) * G::ROWS + rl] = l;
     }
+#pragma unroll
+    for (int d = 0; d < G::DT; ++d)
+#pragma unroll
+      for (int i4 = 0; i4 < AN / 4; ++i4)
+        *(v4f*)(so + (wk * G::ROWS + rl) * G::SO + d * G::MT + 8 * i4 + 4 * g) =
+            v4f{o[d][4 * i4], o[d][4 * i4 + 1], o[d][4 * i4 + 2], o[d][4 * i4 + 3]};
     __syncthreads();
     constexpr int LPR = G::D / 4;                           // lanes per row, 4 values each
     for (int it = threadIdx.x; it < G::ROWS * LPR; it += G::THREADS) {
@@ -616,7 +630,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
       for (int x = 0; x < G::WK; ++x) {
         const float f = __builtin_amdgcn_exp2f(sm[x * G::ROWS + rw] - mm);
         ll += sm[(G::WK + x) * G::ROWS + rw] * f;
-        const v4f y = *(const v4f*)(so + (x * G::ROWS + rw) * G::D + d);
+        const v4f y = *(const v4f*)(so + (x * G::ROWS + rw) * G::SO + d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) ov[i] += y[i] * f;
       }
@@ -791,11 +805,11 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
 // waves of 32 rows share every key tile.  Key groups and stages fill the LDS.
 template <int D, bool KV8, class F>
 auto visit_rows(int64_t rows, F f) {
-  if (rows <= 16) return f(Geo<D, KV8, 16, 1, 1, D == 256 && !KV8 ? 2 : 4, 32, 2, D == 256 ? 1 : 2>{});
+  if (rows <= 16) return f(Geo<D, KV8, 16, 1, D == 256 && !KV8 ? 2 : 4, 32, D == 256 ? 1 : 2>{});
   if constexpr (D < 256)
-    if (rows <= 32) return f(Geo<D, KV8, 32, 1, 1, 4, 32, 2, 2>{});
-  if (rows <= 64) return f(Geo<D, KV8, 32, 1, 2, 2, 32, 2, D == 256 ? 1 : 2>{});
-  return f(Geo<D, KV8, 32, 1, 4, 1, D == 256 ? 32 : 64, 2, D == 256 ? 1 : 2>{});
+    if (rows <= 32) return f(Geo<D, KV8, 32, 1, 4, 32, 2>{});
+  if (rows <= 64) return f(Geo<D, KV8, 32, 2, 2, 32, D == 256 ? 1 : 2>{});
+  return f(Geo<D, KV8, 32, 4, 1, D == 256 ? 32 : 64, D == 256 ? 1 : D == 64 ? 3 : 2>{});
 }
 template <class F>
 auto visit(int dim, bool e4m3, int64_t rows, F f) {
