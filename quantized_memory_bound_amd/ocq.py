@@ -403,24 +403,58 @@ class QuantizedMLP:
 ROPE_SCALINGS = ("none", "linear", "ntk", "yarn")
 
 
-def _rows_view(t, name, device, dims):
-    """Raise unless t is a bf16 tensor of `dims` axes on `device` with its last axis contiguous."""
-    import torch
-    if t is None or not hasattr(t, "data_ptr"):
-        raise OcqError(ERR_INVALID_ARG, "%s must be a tensor" % name)
-    if t.dtype != torch.bfloat16 or t.device != device:
-        raise OcqError(ERR_INVALID_ARG, "%s must be bfloat16 on %s, got %s on %s" % (name, device, t.dtype, t.device))
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise OcqError(ERR_INVALID_ARG, "%s must have %d axes, the last one contiguous" % (name, dims))
+_torch = None
+_raw_stream = None
 
 
-def _device_of(t, name):
-    import torch
-    if t is None or not hasattr(t, "data_ptr") or not t.is_cuda:
+def _gpu(t, name):
+    """The device index of the CUDA tensor t, which must be the current device's."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _torch = torch
+        # the handle of the current stream without a Stream object: 0.1 us instead of 2.8
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda i: torch.cuda.current_stream(i).cuda_stream)
+    i = t.get_device() if hasattr(t, "get_device") else -1
+    if i < 0:
         raise OcqError(ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
-    if t.device.index != torch.cuda.current_device():
-        raise OcqError(ERR_INVALID_ARG, "%s is on %s, not on the current device" % (name, t.device))
-    return t.device
+    if i != _torch.cuda.current_device():
+        raise OcqError(ERR_INVALID_ARG, "%s is on cuda:%d, not on the current device" % (name, i))
+    return i
+
+
+def _bf16_rows(t, name, index, shape):
+    """Raise unless t is a bf16 tensor of this shape on device `index`, its last axis contiguous."""
+    if not hasattr(t, "get_device"):
+        raise OcqError(ERR_INVALID_ARG, "%s must be a tensor" % name)
+    if t.dtype is not _torch.bfloat16 or t.get_device() != index:
+        raise OcqError(ERR_INVALID_ARG, "%s must be bfloat16 on cuda:%d, got %s on %s" %
+                       (name, index, t.dtype, t.device))
+    if t.shape != shape:
+        raise OcqError(ERR_INVALID_ARG, "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise OcqError(ERR_INVALID_ARG, "the last axis of %s must be contiguous" % name)
+
+
+def _empty(shape, dtype, index, stream):
+    """A new tensor for a call on `stream`: allocated on it, so that its memory is not reused before the call."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=index)
+    cuda = _torch.cuda
+    with cuda.stream(stream if hasattr(stream, "cuda_stream") else cuda.ExternalStream(stream, index)):
+        return _torch.empty(shape, dtype=dtype, device=index)
+
+
+def _empty_as(t, shape, dtype, index, stream):
+    """_empty of t's shape (the cheapest allocation where t is contiguous)."""
+    if stream is None and t.is_contiguous():
+        return _torch.empty_like(t, dtype=dtype)
+    return _empty(shape, dtype, index, stream)
+
+
+def _stream_of(stream, index):
+    return _raw_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 def add_rmsnorm(x, weight, eps=1e-6, residual=None, want_y=False, want_codes=True, residual_out=None, y=None,
@@ -432,37 +466,37 @@ def add_rmsnorm(x, weight, eps=1e-6, residual=None, want_y=False, want_codes=Tru
     [rows, hidden]) and scales (float32 [rows]): its E4M3 quantization if wanted or given.  Outputs that are not
     given are allocated; given codes may be uint8.
     """
-    import torch
-    dev = _device_of(x, "x")
-    _rows_view(x, "x", dev, 2)
-    rows, hidden = x.shape
-    _need(weight, "weight", torch.bfloat16, dev, shape=(hidden,))
+    i = _gpu(x, "x")
+    if x.dim() != 2:
+        raise OcqError(ERR_INVALID_ARG, "x must be [rows, hidden], got %s" % (tuple(x.shape),))
+    shape = rows, hidden = x.shape
+    _bf16_rows(x, "x", i, shape)
+    _bf16_rows(weight, "weight", i, (hidden,))
+    bf16, res, res_stride = _torch.bfloat16, None, 0
     if residual is not None:
-        _rows_view(residual, "residual", dev, 2)
-        if residual.shape != x.shape:
-            raise OcqError(ERR_INVALID_ARG, "residual has shape %s, x %s" % (tuple(residual.shape), tuple(x.shape)))
-        if residual_out is None:
-            residual_out = _empty((rows, hidden), torch.bfloat16, dev, stream)
+        _bf16_rows(residual, "residual", i, shape)
+        res, res_stride = residual.data_ptr(), residual.stride(0)
     if residual_out is not None:
-        _need(residual_out, "residual_out", torch.bfloat16, dev, shape=(rows, hidden))
+        _need(residual_out, "residual_out", bf16, x.device, shape)
+    elif residual is not None:
+        residual_out = _empty_as(x, shape, bf16, i, stream)
     if y is not None:
-        _need(y, "y", torch.bfloat16, dev, shape=(rows, hidden))
+        _need(y, "y", bf16, x.device, shape)
     elif want_y:
-        y = _empty((rows, hidden), torch.bfloat16, dev, stream)
+        y = _empty_as(x, shape, bf16, i, stream)
     if codes is not None or scales is not None or want_codes:
         if codes is None:
-            codes = _empty((rows, hidden), torch.float8_e4m3fn, dev, stream)
+            codes = _empty_as(x, shape, _torch.float8_e4m3fn, i, stream)
         else:
-            _need(codes, "codes", (torch.float8_e4m3fn, torch.uint8), dev, shape=(rows, hidden))
+            _need(codes, "codes", (_torch.float8_e4m3fn, _torch.uint8), x.device, shape)
         if scales is None:
-            scales = _empty(rows, torch.float32, dev, stream)
+            scales = _empty(rows, _torch.float32, i, stream)
         else:
-            _need(scales, "scales", torch.float32, dev, shape=(rows,))
-    _check(lib().ocq_add_rmsnorm(x.data_ptr(), x.stride(0), None if residual is None else residual.data_ptr(),
-                                 0 if residual is None else residual.stride(0), weight.data_ptr(), eps, rows, hidden,
+            _need(scales, "scales", _torch.float32, x.device, (rows,))
+    _check(lib().ocq_add_rmsnorm(x.data_ptr(), x.stride(0), res, res_stride, weight.data_ptr(), eps, rows, hidden,
                                  None if residual_out is None else residual_out.data_ptr(),
                                  None if y is None else y.data_ptr(), None if codes is None else codes.data_ptr(),
-                                 None if scales is None else scales.data_ptr(), _stream_handle(stream)))
+                                 None if scales is None else scales.data_ptr(), _stream_of(stream, i)))
     return residual_out, y, codes, scales
 
 
@@ -476,7 +510,8 @@ class PagedKVCache:
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
-        dev = _device_of(k, "k")
+        self.index = _gpu(k, "k")
+        dev = k.device
         if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
             raise OcqError(ERR_INVALID_ARG, "k must be [pages, kv_heads, page_size, head_dim], bf16 or E4M3 codes")
         if v is None or not hasattr(v, "data_ptr") or v.device != dev or v.dtype != k.dtype or v.shape != k.shape or \
@@ -523,7 +558,8 @@ class TokenBatch:
 
     def __init__(self, q_start, kv_lens, page_table, max_new, max_kv, tokens=None):
         import torch
-        dev = _device_of(kv_lens, "kv_lens")
+        self.index = _gpu(kv_lens, "kv_lens")
+        dev = kv_lens.device
         requests = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
         _need(kv_lens, "kv_lens", torch.int32, dev, shape=(requests,))
         _need(q_start, "q_start", torch.int32, dev, shape=(requests + 1,))
@@ -568,7 +604,8 @@ class Rope:
 
     def __init__(self, inv_freq, multiplier=1.0, interleaved=False):
         import torch
-        dev = _device_of(inv_freq, "inv_freq")
+        self.index = _gpu(inv_freq, "inv_freq")
+        dev = inv_freq.device
         if inv_freq.dim() != 1:
             raise OcqError(ERR_INVALID_ARG, "inv_freq must be [rot / 2]")
         _need(inv_freq, "inv_freq", torch.float64, dev)
@@ -583,47 +620,37 @@ class Rope:
         return cls(torch.from_numpy(inv).to(device), mult, interleaved)
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor for a call on `stream`: allocated on it, so that its memory is not reused before the call."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, device)):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _on(device, *handles):
+def _on(index, *handles):
     for h in handles:
-        if h.device != device:
-            raise OcqError(ERR_INVALID_ARG, "%s is on %s, not %s" % (type(h).__name__, h.device, device))
+        if h.index != index:
+            raise OcqError(ERR_INVALID_ARG, "%s is on %s, not on cuda:%d" % (type(h).__name__, h.device, index))
 
 
 def rope_append(q, k, v, rope, cache, batch, positions=None, q_out=None, stream=None):
     """Rotate q (bf16 [tokens, heads, head_dim]) and k ([tokens, kv_heads, head_dim]) and append k and v to the
     cache; returns the rotated q (q_out, contiguous, or q itself).  Token and head strides are free.  positions:
     None (each token's place in its request) or int32 [tokens]."""
-    import torch
-    dev = _device_of(q, "q")
-    _rows_view(q, "q", dev, 3)
-    tokens, heads, dim = q.shape
-    kv_shape = (tokens, cache.kv_heads, cache.head_dim)
-    for t, name in ((k, "k"), (v, "v")):
-        _rows_view(t, name, dev, 3)
-        if t.shape != kv_shape:
-            raise OcqError(ERR_INVALID_ARG, "%s has shape %s, expected %s" % (name, tuple(t.shape), kv_shape))
+    i = _gpu(q, "q")
+    if q.dim() != 3:
+        raise OcqError(ERR_INVALID_ARG, "q must be [tokens, heads, head_dim], got %s" % (tuple(q.shape),))
+    shape = tokens, heads, dim = q.shape
     if dim != cache.head_dim:
         raise OcqError(ERR_INVALID_ARG, "q has head size %d, the cache %d" % (dim, cache.head_dim))
-    _on(dev, rope, cache, batch)
+    _bf16_rows(q, "q", i, shape)
+    kv_shape = (tokens, cache.kv_heads, dim)
+    _bf16_rows(k, "k", i, kv_shape)
+    _bf16_rows(v, "v", i, kv_shape)
+    _on(i, rope, cache, batch)
     if positions is not None:
-        _need(positions, "positions", torch.int32, dev, shape=(tokens,))
+        _need(positions, "positions", _torch.int32, q.device, (tokens,))
     if q_out is None:
-        q_out = _empty((tokens, heads, dim), torch.bfloat16, dev, stream)
+        q_out = _empty_as(q, shape, _torch.bfloat16, i, stream)
     else:
-        _need(q_out, "q_out", torch.bfloat16, dev, shape=(tokens, heads, dim))
+        _need(q_out, "q_out", _torch.bfloat16, q.device, shape)
     _check(lib().ocq_rope_append(q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1),
                                  v.data_ptr(), v.stride(0), v.stride(1), heads, rope.inv_freq.data_ptr(), rope.rot,
                                  rope.interleaved, rope.multiplier, None if positions is None else positions.data_ptr(),
-                                 cache.ref, batch.of(tokens), q_out.data_ptr(), _stream_handle(stream)))
+                                 cache.ref, batch.of(tokens), q_out.data_ptr(), _stream_of(stream, i)))
     return q_out
 
 
@@ -642,34 +669,34 @@ def paged_attention(q, cache, batch, scale=None, window=0, sinks=0, want_lse=Fal
     first tokens, which a window leaves visible.  A token that sees nothing has out 0 and lse -inf.  workspace: a
     uint8 tensor of attention_workspace_bytes(...), allocated if None.
     """
-    import torch
-    dev = _device_of(q, "q")
-    _rows_view(q, "q", dev, 3)
-    tokens, heads, dim = q.shape
+    i = _gpu(q, "q")
+    if q.dim() != 3:
+        raise OcqError(ERR_INVALID_ARG, "q must be [tokens, heads, head_dim], got %s" % (tuple(q.shape),))
+    shape = tokens, heads, dim = q.shape
     if dim != cache.head_dim:
         raise OcqError(ERR_INVALID_ARG, "q has head size %d, the cache %d" % (dim, cache.head_dim))
-    _on(dev, cache, batch)
+    _bf16_rows(q, "q", i, shape)
+    _on(i, cache, batch)
     if out is None:
-        out = _empty((tokens, heads, dim), torch.bfloat16, dev, stream)
+        out = _empty_as(q, shape, _torch.bfloat16, i, stream)
     else:
-        _need(out, "out", torch.bfloat16, dev, shape=(tokens, heads, dim))
+        _need(out, "out", _torch.bfloat16, q.device, shape)
     if lse is not None:
-        _need(lse, "lse", torch.float32, dev, shape=(tokens, heads))
+        _need(lse, "lse", _torch.float32, q.device, (tokens, heads))
     elif want_lse:
-        lse = _empty((tokens, heads), torch.float32, dev, stream)
+        lse = _empty((tokens, heads), _torch.float32, i, stream)
     ref, L = batch.of(tokens), lib()
-    need = 0
     if workspace is None:
         need = L.ocq_attention_workspace_bytes(heads, cache.ref, ref, window, sinks)
         if need:
-            workspace = _empty(need, torch.uint8, dev, stream)
+            workspace = _empty(need, _torch.uint8, i, stream)
     else:
-        _need(workspace, "workspace", torch.uint8, dev)
+        _need(workspace, "workspace", _torch.uint8, q.device)
         need = workspace.numel()
     _check(L.ocq_paged_attention(q.data_ptr(), q.stride(0), q.stride(1), heads, cache.ref, ref,
                                  dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
                                  None if lse is None else lse.data_ptr(),
-                                 None if workspace is None else workspace.data_ptr(), need, _stream_handle(stream)))
+                                 None if workspace is None else workspace.data_ptr(), need, _stream_of(stream, i)))
     return out, lse
 
 
