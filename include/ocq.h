@@ -387,7 +387,10 @@ typedef struct {
  * page_table_dev int32 [requests, max_pages] with row stride table_stride.
  * max_new, max_kv: host bounds of the new tokens and of kv_lens of any
  * request.  Tokens past max_new of a request are not attended; max_kv only
- * shapes the split of the work.  tokens * heads and max_pages * page_size
+ * shapes the split of the work.
+ * counters_dev: uint32 [OCQ_ATTENTION_COUNTERS] for ocq_paged_attention (not
+ * read by the others): zeroed once by the caller, zero again after every call;
+ * attention calls that share it must be ordered on one stream.  tokens * heads and max_pages * page_size
  * stay below 2^31. */
 typedef struct {
   const void* q_start_dev;
@@ -395,7 +398,9 @@ typedef struct {
   const void* page_table_dev;
   int64_t table_stride;
   int requests, tokens, max_pages, max_new, max_kv;
+  void* counters_dev;
 } ocq_token_batch;
+#define OCQ_ATTENTION_COUNTERS 4096
 
 /* Rotary frequencies of rot dimensions (float64 [rot / 2] to inv_freq_out,
  * and to multiplier_out the factor of cos and sin), by a published rule:

@@ -93,9 +93,9 @@ struct Geo {
   static constexpr int QS = D / KS, DT = D / MT, LG = 64 / MT;          // steps of S, tiles of O, lane groups
   static constexpr int PS = TK / KS;                                    // steps of O
   static constexpr int SO = D + 4;                                      // floats of a joined row: 16 bytes further per row
-  static constexpr int JOIN = WK > 1 ? WK * ROWS * (SO * 4 + 8) : 0;
+  static constexpr int JOIN = WK > 1 ? WK * ROWS * (SO * 4 + 8) + 4 : 0;
   static constexpr int LDS = RING > JOIN ? RING : JOIN;
-  static constexpr bool EVEN = ROWS <= 64;                              // see layer_index.h, pieces
+  static constexpr bool EVEN = WK > 1;                                  // may be cut into pieces (layer_index.h)
   static constexpr int PER_CU = 160 * 1024 / (LDS + 1024) < 4 * MINW / NW ? 160 * 1024 / (LDS + 1024) : 4 * MINW / NW;
   static constexpr int RESIDENT = 256 * (PER_CU > 0 ? PER_CU : 1);      // workgroups at once, 256 CUs
   static_assert(PART % (1024 * WR) == 0 && TK % 32 == 0 && LDS <= 160 * 1024, "");
@@ -130,9 +130,13 @@ __device__ __forceinline__ constexpr int swz(int row) {
 
 // 16 (or 4) bytes from p for each lane to LDS, lane after lane from `to`.  The
 // address is a chosen one, not a branch to one of two loads.
+// ONCE: nobody else reads these bytes (non-temporal: they pass through L2
+// without staying; 4 x 131072 keys: 314 -> 280 us).
+template <bool ONCE>
 __device__ __forceinline__ void dma16(uint64_t p, uint8_t* to) {
   asm("" : "+v"(p));
-  __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)to, 16, 0, 0);
+  if constexpr (ONCE) __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)to, 16, 0, 2);
+  else __builtin_amdgcn_global_load_lds((const void*)p, (lds_void*)to, 16, 0, 0);
 }
 __device__ __forceinline__ void dma4(uint64_t p, uint8_t* to) {
   asm("" : "+v"(p));
@@ -193,7 +197,7 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// The request that a workgroup (or a segment of the join) belongs to.
+// The request that a workgroup belongs to.
 struct Found {
   int req, t0, n, kv;   // request (-1: none), its first new token, their number, its cached tokens
   int tiles, pieces;    // of each of its segments
@@ -201,9 +205,8 @@ struct Found {
 };
 
 // Every wave cuts the batch into pieces by itself, in registers: lane l holds
-// request base + l.  of_piece >= 0: the request of that piece; else: request
-// of_request.
-__device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int of_piece, int of_request) {
+// request base + l.
+__device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int piece) {
   const int lane = threadIdx.x & 63, kvh = a.c.kv_heads;
   auto load = [&](int base, int& t0, int& n, int& kv) {
     const int r = base + lane;
@@ -226,9 +229,10 @@ __device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int of_pi
   const int segments = a.b.requests * kvh;
   float per;
   if (2 * segments > a.slots) {
-    // about as many segments as slots: pieces of half a slot's share, so that
-    // the last ones to run are short
-    per = (float)(total / (2 * a.slots) + 1);
+    // about as many segments as slots, or more: only those of one and a half
+    // mean shares and more are cut (pieces of half a share: 64 x 13 rows over
+    // 8192 keys in E4M3 221 us instead of 203)
+    per = (float)(total / 2 * 3 / a.slots + 1);
   } else {
     // the smallest pieces that fit the slots: eight candidates from the mean to
     // the bound, each summed by eight lanes
@@ -254,8 +258,7 @@ __device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int of_pi
     if (base > 0) T = load(base, t0, n, kv);
     const int c = piece_count(T, inv), end = wave_scan(c * kvh) + carry;
     // the lane whose request it is
-    const bool mine = of_piece >= 0 ? of_piece < end && of_piece >= end - c * kvh : base + lane == of_request;
-    const uint64_t who = __ballot(mine);
+    const uint64_t who = __ballot(piece < end && piece >= end - c * kvh);
     if (who) {
       const int l = __builtin_ctzll(who);
       f.req = base + l;
@@ -282,7 +285,83 @@ struct Piece {
   int s0, s1;
   bool direct;          // the rows' whole result, or a part of it that goes to `part`
   size_t part;
+  int pieces, index;    // of the segment, and which one this is
 };
+
+// Joins N rows' parts: ov[k] = sum_i 2^(lse_i - mm) out_i and ll[k] = sum_i
+// 2^(lse_i - mm) over the `parts` parts of row k (part i at row_of(i, k)), mm[k]
+// the largest lse; a part without keys (lse -inf) has no output.  B parts of
+// every row are read at a time.  SHARED: other workgroups of the same launch
+// wrote the parts, which lie past the L2 of one XCD (see put_part).
+template <bool SHARED, int N, int B, class F>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, int parts, const int (&d)[N], int D, F row_of,
+                                           float (&mm)[N], float (&ll)[N], v4f (&ov)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    mm[k] = -__builtin_inff();
+    ll[k] = 0.0f;
+    ov[k] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  for (int i0 = 0; i0 < parts; i0 += B) {
+    float x[N][B];
+    v4f y[N][B];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const size_t r = row_of(i0 + j < parts ? i0 + j : parts - 1, k);
+        if constexpr (SHARED) {
+          x[k][j] = __hip_atomic_load(a.part_lse + r, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          const uint64_t* p = (const uint64_t*)(a.part_o + r * D + d[k]);
+          const uint64_t lo = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          const uint64_t hi = __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          const v2f a0 = __builtin_bit_cast(v2f, lo), a1 = __builtin_bit_cast(v2f, hi);
+          y[k][j] = v4f{a0[0], a0[1], a1[0], a1[1]};
+        } else {
+          x[k][j] = a.part_lse[r];
+          y[k][j] = *(const v4f*)(a.part_o + r * D + d[k]);
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float nm = mm[k];
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        if (i0 + j >= parts) x[k][j] = -__builtin_inff();
+        nm = fmaxf(nm, x[k][j]);
+      }
+      const bool none = nm == -__builtin_inff();   // nothing yet (NaN goes on)
+      const float f = none ? 1.0f : __builtin_amdgcn_exp2f(mm[k] - nm);
+      ll[k] *= f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ov[k][i] *= f;
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const float e = x[k][j] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x[k][j] - nm);
+        ll[k] += e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ov[k][i] += x[k][j] == -__builtin_inff() ? 0.0f : y[k][j][i] * e;
+      }
+      mm[k] = nm;
+    }
+  }
+}
+
+// A joined row's four values and its lse.
+__device__ __forceinline__ void put_joined(const AttnArgs& a, size_t at, int d, int D, v4f ov, float mm, float ll) {
+  const float inv = ll > 0.0f ? 1.0f / ll : ll;
+  *(v2i*)(a.out + at * D + d) = v2i{(int)pack_bf16(ov[0] * inv, ov[1] * inv), (int)pack_bf16(ov[2] * inv, ov[3] * inv)};
+  if (d == 0 && a.lse) a.lse[at] = ll == 0.0f ? -__builtin_inff() : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+}
+
+// A part's four values (and its lse with d = 0), for a workgroup on any XCD to
+// read in the same launch: device-scope stores (sc1) write through the XCD's
+// L2.  They are visible to device-scope loads once the wave's count of
+// outstanding stores is 0.
+__device__ __forceinline__ void put_part(const AttnArgs& a, size_t row, int d, int D, v4f y, float lse2) {
+  asm volatile("global_store_dwordx4 %0, %1, off sc1" ::"v"(a.part_o + row * D + d), "v"(y) : "memory");
+  if (d == 0) __hip_atomic_store(a.part_lse + row, lse2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
 template <class G>
 __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8_t* lds) {
@@ -350,7 +429,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
     for (int i = 0; i < G::QI; ++i) {
       there[i] = row_there(key0 + q_row(i), kv, ids[i], a.c.num_pages);
       src[i] = first + (uint64_t)(uint32_t)ids[i] * a.c.page + part[i];
-      dma16(there[i] ? src[i] : zero, to + (i * G::WR + wr) * 1024);
+      dma16<G::EVEN>(there[i] ? src[i] : zero, to + (i * G::WR + wr) * 1024);
     }
     if constexpr (G::KV8) {
       s_there = row_there(key0 + lane % G::TK, kv, sid, a.c.num_pages);
@@ -362,7 +441,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   auto issue_v = [&](int slot) {
     uint8_t* const to = ring + slot;
 #pragma unroll
-    for (int i = 0; i < G::QI; ++i) dma16(there[i] ? src[i] + v_less_k : zero, to + (i * G::WR + wr) * 1024);
+    for (int i = 0; i < G::QI; ++i) dma16<G::EVEN>(there[i] ? src[i] + v_less_k : zero, to + (i * G::WR + wr) * 1024);
     if constexpr (G::KV8) dma4(s_there ? s_src + vs_less_ks : zero, to + G::PART);
   };
 
@@ -582,13 +661,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   // ---- join the lane groups' sums and the key groups' parts, and write
 #pragma unroll
   for (int x = G::MT; x < 64; x <<= 1) l += __shfl_xor(l, x);
-  // where row rl of the tile (row `at` of the output) goes if it is a part
-  auto part_at = [&](int rl, size_t at) { return pc.part + (a.even ? (size_t)rl : at); };
   if constexpr (G::WK == 1) {
     if (!live) return;
     const float inv = l > 0.0f ? 1.0f / l : l;   // l: 0, or NaN kept
     const float lse2 = l == 0.0f ? -__builtin_inff() : m + __builtin_amdgcn_logf(l);
-    const size_t ps = part_at(rl, at);
+    const size_t ps = pc.part + at;
 #pragma unroll
     for (int d = 0; d < G::DT; ++d)
 #pragma unroll
@@ -642,9 +719,49 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
                                              (int)pack_bf16(ov[2] * inv, ov[3] * inv)};
         if (d == 0 && a.lse) a.lse[ar] = lse2 * kLn2;
       } else {
-        const size_t ps = part_at(rw, ar);
-        if (ns > 0) *(v4f*)(a.part_o + ps * G::D + d) = v4f{ov[0] * inv, ov[1] * inv, ov[2] * inv, ov[3] * inv};
-        if (d == 0) a.part_lse[ps] = lse2;
+        const v4f y = {ov[0] * inv, ov[1] * inv, ov[2] * inv, ov[3] * inv};
+        if (a.even) {
+          put_part(a, pc.part + rw, d, G::D, y, lse2);
+        } else {
+          const size_t ps = pc.part + ar;
+          if (ns > 0) *(v4f*)(a.part_o + ps * G::D + d) = y;
+          if (d == 0) a.part_lse[ps] = lse2;
+        }
+      }
+    }
+    // the workgroup that ends a segment's last piece joins them all
+    if (a.even && !pc.direct) {
+      int* const last = (int*)(sm + 2 * G::WK * G::ROWS);
+      uint32_t* const count = a.counters + pc.req * a.c.kv_heads + kvh;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // this wave's part is written
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const uint32_t before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *last = before + 1 == (uint32_t)pc.pieces;
+        if (*last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // for the next call
+      }
+      __syncthreads();
+      if (!*last) return;
+      const size_t first = pc.part - (size_t)pc.index * G::ROWS;
+      constexpr int N = G::ROWS * LPR / G::THREADS;         // a thread's rows, THREADS / LPR apart
+      static_assert(G::THREADS % LPR == 0, "one d per thread");
+      const int rw0 = threadIdx.x / LPR, d0 = (threadIdx.x % LPR) * 4;
+      int d[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) d[k] = d0;
+      float mm[N], ll[N];
+      v4f ov[N];
+      auto row_of = [&](int i, int k) {                     // a row that is not there reads the first
+        const int rw = rw0 + k * (G::THREADS / LPR);
+        return first + (size_t)i * G::ROWS + (rw < n * a.group ? rw : 0);
+      };
+      join_parts<true, N, (N < 16 ? 16 / N : 1)>(a, pc.pieces, d, G::D, row_of, mm, ll, ov);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int rw = rw0 + k * (G::THREADS / LPR);
+        if (rw < n * a.group)
+          put_joined(a, (size_t)(t0 + rw / a.group) * a.heads + kvh * a.group + rw % a.group, d0, G::D, ov[k], mm[k],
+                     ll[k]);
       }
     }
   }
@@ -656,7 +773,7 @@ __global__ __launch_bounds__(G::THREADS, G::MINW) void k_attn(AttnArgs a) {
   Piece pc;
   if constexpr (G::EVEN) {
     if (a.even) {
-      const Found f = find_piece(a, G::TT, blockIdx.x, 0);
+      const Found f = find_piece(a, G::TT, blockIdx.x);
       if (f.req < 0) return;
       const int in = blockIdx.x - f.first, i = in % f.pieces;
       pc.req = f.req;
@@ -672,6 +789,8 @@ __global__ __launch_bounds__(G::THREADS, G::MINW) void k_attn(AttnArgs a) {
       pc.s1 = pc.tiles.total ? piece_begin(f.tiles, i + 1, f.pieces) : 0;
       pc.direct = f.pieces == 1;
       pc.part = (size_t)blockIdx.x * G::ROWS;
+      pc.pieces = f.pieces;
+      pc.index = i;
       attend<G>(a, pc, lds);
       return;
     }
@@ -703,47 +822,6 @@ __global__ __launch_bounds__(G::THREADS, G::MINW) void k_attn(AttnArgs a) {
   attend<G>(a, pc, lds);
 }
 
-// sum_i 2^(lse_i - mm) out_i and ll = sum_i 2^(lse_i - mm) over the n parts of a
-// row (part i at row_of(i)), mm the largest lse; a part without keys (lse
-// -inf) has no output.  Eight parts are read at a time.
-template <class F>
-__device__ __forceinline__ v4f join_parts(const AttnArgs& a, int n, int d, int D, F row_of, float& mm, float& ll) {
-  constexpr int B = 8;
-  mm = -__builtin_inff();
-  ll = 0.0f;
-  v4f ov = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i0 = 0; i0 < n; i0 += B) {
-    float x[B];
-    v4f y[B];
-#pragma unroll
-    for (int j = 0; j < B; ++j) {
-      const size_t r = row_of(i0 + j < n ? i0 + j : n - 1);
-      x[j] = a.part_lse[r];
-      y[j] = *(const v4f*)(a.part_o + r * D + d);
-    }
-    float nm = mm;
-#pragma unroll
-    for (int j = 0; j < B; ++j) {
-      if (i0 + j >= n) x[j] = -__builtin_inff();
-      nm = fmaxf(nm, x[j]);
-    }
-    if (nm == -__builtin_inff()) continue;   // nothing yet (NaN goes on)
-    const float f = __builtin_amdgcn_exp2f(mm - nm);
-    ll *= f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ov[i] *= f;
-#pragma unroll
-    for (int j = 0; j < B; ++j) {
-      const float e = __builtin_amdgcn_exp2f(x[j] - nm);
-      ll += e;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ov[i] += x[j] == -__builtin_inff() ? 0.0f : y[j][i] * e;
-    }
-    mm = nm;
-  }
-  return ov;
-}
-
 // Joins the splits: out = sum_s 2^(lse_s - lse) out_s.  D / 4 lanes per row;
 // a split without keys (lse -inf) has no output and is skipped.
 template <int D>
@@ -753,29 +831,10 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   const size_t at = (size_t)blockIdx.x * RPB + threadIdx.x / LPR;
   const int d = (threadIdx.x % LPR) * 4;
   if (at >= rows) return;
-  float ll, mm;
-  const v4f ov = join_parts(a, a.splits, d, D, [&](int s) { return s * rows + at; }, mm, ll);
-  const float inv = ll > 0.0f ? 1.0f / ll : ll;
-  *(v2i*)(a.out + at * D + d) = v2i{(int)pack_bf16(ov[0] * inv, ov[1] * inv), (int)pack_bf16(ov[2] * inv, ov[3] * inv)};
-  if (d == 0 && a.lse) a.lse[at] = ll == 0.0f ? -__builtin_inff() : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
-}
-
-// Joins the pieces of the segments that were cut.
-template <class G>
-__global__ __launch_bounds__(256) void k_attn_join_pieces(AttnArgs a) {
-  constexpr int LPR = G::D / 4, RPB = 256 / LPR, BPS = G::ROWS / RPB;   // rows a block, blocks a segment
-  const int pair = blockIdx.x / BPS, kvh = pair % a.c.kv_heads;
-  const int rw = blockIdx.x % BPS * RPB + threadIdx.x / LPR, d = (threadIdx.x % LPR) * 4;
-  const Found f = find_piece(a, G::TT, -1, pair / a.c.kv_heads);
-  if (f.req < 0 || f.pieces <= 1 || rw >= f.n * a.group) return;
-  auto slot = [&](int i) { return (size_t)(f.first + kvh * f.pieces + i) * G::ROWS + rw; };
-  float ll, mm;
-  const v4f ov = join_parts(a, f.pieces, d, G::D, slot, mm, ll);
-  const float inv = ll > 0.0f ? 1.0f / ll : ll;
-  const size_t at = (size_t)(f.t0 + rw / a.group) * a.heads + kvh * a.group + rw % a.group;
-  *(v2i*)(a.out + at * G::D + d) =
-      v2i{(int)pack_bf16(ov[0] * inv, ov[1] * inv), (int)pack_bf16(ov[2] * inv, ov[3] * inv)};
-  if (d == 0 && a.lse) a.lse[at] = ll == 0.0f ? -__builtin_inff() : (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+  float mm[1], ll[1];
+  v4f ov[1];
+  join_parts<false, 1, 8>(a, a.splits, {d}, D, [&](int s, int) { return s * rows + at; }, mm, ll, ov);
+  put_joined(a, at, d, D, ov[0], mm[0], ll[0]);
 }
 
 template <class G>
@@ -786,8 +845,6 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
   const int pairs = a.b.requests * a.c.kv_heads;
   if (a.even) {
     hipLaunchKernelGGL((k_attn<G>), dim3(a.groups), dim3(G::THREADS), G::LDS, st, a);
-    if constexpr (G::EVEN)
-      hipLaunchKernelGGL((k_attn_join_pieces<G>), dim3(pairs * (G::ROWS * G::D / 1024)), dim3(256), 0, st, a);
     return hipGetLastError();
   }
   const int tiles = (int)(((int64_t)a.max_new * a.group + G::ROWS - 1) / G::ROWS);
@@ -838,7 +895,7 @@ AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads,
     const int64_t pairs = (int64_t)requests * kv_heads, tiles = (rows + G::ROWS - 1) / G::ROWS;
     const int64_t key_tiles = (keys + G::TT - 1) / G::TT;
     if (key_tiles <= kMinTiles) return p;
-    if (G::EVEN && requests <= kEvenRequests && pairs < 4 * G::RESIDENT && pairs * (cap / G::TT + 1) < (1 << 30)) {
+    if (G::EVEN && requests <= kEvenRequests && pairs < 4 * G::RESIDENT && pairs <= OCQ_ATTENTION_COUNTERS && pairs * (cap / G::TT + 1) < (1 << 30)) {
       p.even = 1;
       p.slots = G::RESIDENT;
       p.groups = (int)(2 * pairs > p.slots ? 2 * p.slots + pairs : p.slots);   // no fewer than there can be pieces

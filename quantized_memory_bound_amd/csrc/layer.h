@@ -71,6 +71,7 @@ struct AttnArgs {
   int even, splits, groups, slots;
   float* part_o;             // [part_rows][dim]
   float* part_lse;           // [part_rows]
+  uint32_t* counters;        // [OCQ_ATTENTION_COUNTERS], 0 between calls
 };
 
 struct AttnPlan {

@@ -214,8 +214,8 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
   if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
     return invalid("window and sinks must not be negative, and sinks need a window");
   if (batch->requests == 0 || batch->tokens == 0) return OCQ_OK;
-  if (!q_dev || !out_dev) return invalid("null device pointer");
-  if (!aligned(q_dev) || !aligned(out_dev) || !aligned(lse_dev, 4) || !aligned(workspace_dev))
+  if (!q_dev || !out_dev || !batch->counters_dev) return invalid("null device pointer");
+  if (!aligned(q_dev) || !aligned(out_dev) || !aligned(lse_dev, 4) || !aligned(batch->counters_dev, 4) || !aligned(workspace_dev))
     return invalid("device pointers must be 16-byte aligned");
   if (!stride_ok(q_token_stride, 8) || !stride_ok(q_head_stride, 8))
     return invalid("strides must be multiples of 8, not negative");
@@ -245,6 +245,7 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
   a.splits = plan.splits;
   a.groups = plan.groups;
   a.slots = plan.slots;
+  a.counters = (uint32_t*)batch->counters_dev;
   a.part_o = (float*)workspace_dev;
   a.part_lse = (float*)workspace_dev + plan.part_rows * cache->head_dim;
   const int rc = launch_attn(a, stream);

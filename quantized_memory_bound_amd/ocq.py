@@ -58,7 +58,8 @@ class KVCacheStruct(ctypes.Structure):
 class TokenBatchStruct(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("q_start_dev", "kv_lens_dev", "page_table_dev")] +
                 [("table_stride", ctypes.c_int64)] +
-                [(n, ctypes.c_int) for n in ("requests", "tokens", "max_pages", "max_new", "max_kv")])
+                [(n, ctypes.c_int) for n in ("requests", "tokens", "max_pages", "max_new", "max_kv")] +
+                [("counters_dev", ctypes.c_void_p)])
 
 
 _lib = None
@@ -400,6 +401,7 @@ class QuantizedMLP:
 
 # ---------------------------------------------------------------- the operators around the block
 
+ATTENTION_COUNTERS = 4096
 ROPE_SCALINGS = ("none", "linear", "ntk", "yarn")
 
 
@@ -553,7 +555,8 @@ class TokenBatch:
 
     q_start int32 [requests + 1], kv_lens int32 [requests], page_table int32 [requests, max_pages] (rows strided at
     will): CUDA tensors whose contents may change between calls.  tokens (the rows of q), max_new and max_kv are
-    host numbers: bounds of the new tokens and of kv_lens of any request.
+    host numbers: bounds of the new tokens and of kv_lens of any request.  Attention calls over one batch use its
+    counters: they are ordered on one stream.
     """
 
     def __init__(self, q_start, kv_lens, page_table, max_new, max_kv, tokens=None):
@@ -569,9 +572,10 @@ class TokenBatch:
             raise OcqError(ERR_INVALID_ARG, "page_table must be int32 [%d, max_pages], its rows contiguous" % requests)
         self.q_start, self.kv_lens, self.page_table, self.device = q_start, kv_lens, page_table, dev
         self.requests, self.tokens = requests, None
+        self.counters = torch.zeros(ATTENTION_COUNTERS, dtype=torch.int32, device=dev)   # 0 between calls
         self.struct = TokenBatchStruct(q_start.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
                                        max(page_table.stride(0), page_table.shape[1]), requests, 0,
-                                       page_table.shape[1], max_new, max_kv)
+                                       page_table.shape[1], max_new, max_kv, self.counters.data_ptr())
         self.ref = ctypes.byref(self.struct)
         if tokens is not None:
             self.of(tokens)

@@ -31,7 +31,7 @@ int main() {
     }
   CHECK(ocq_rope_frequencies(24, 1e4, 0, 1, 1, 2, 1, inv, &mult) == OCQ_ERR_UNSUPPORTED);
   const ocq_kv_cache good{p, p, p, p, 8 * 16 * 128, 16 * 128, 128, 128, 16, 1, 7, 16, 8, 128, OCQ_CACHE_E4M3};
-  const ocq_token_batch step{p, p, p, 9, 2, 5, 9, 3, 40};
+  const ocq_token_batch step{p, p, p, 9, 2, 5, 9, 3, 40, p};
   auto attn = [&](const ocq_kv_cache& c, const ocq_token_batch& b, int heads, float scale, int window, int sinks,
                   size_t ws) {
     return ocq_paged_attention(p, 4096, 128, heads, &c, &b, scale, window, sinks, p, p, p, ws, nullptr);

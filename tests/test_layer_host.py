@@ -86,7 +86,7 @@ def _cache(**kw):
 
 def _batch(**kw):
     d = dict(q_start_dev=P, kv_lens_dev=P, page_table_dev=P, table_stride=4, requests=2, tokens=5, max_pages=4,
-             max_new=3, max_kv=60)
+             max_new=3, max_kv=60, counters_dev=P)
     d.update(kw)
     return ocq.TokenBatchStruct(**d)
 
@@ -127,6 +127,11 @@ def test_batch_refusals(fault, status):
     (dict(qs=260), -1), (dict(qh=-64), -1)])
 def test_attention_refusals(fault, status):
     assert _attention(_cache(), _batch(), **fault) == status and ocq.last_error()
+
+
+def test_attention_needs_counters():
+    assert _attention(_cache(), _batch(counters_dev=None)) == -1
+    assert _attention(_cache(), _batch(counters_dev=P + 2)) == -1
 
 
 def _rope(cache=None, batch=None, q=P, k=P, v=P, qs=256, ks=128, heads=4, inv=P, rot=64, inter=0, mult=1.0,
