@@ -767,6 +767,20 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   }
 }
 
+// The request whose context is the want-th longest (in batches of up to 64
+// requests, one per lane; in larger ones the want-th).
+__device__ __forceinline__ int ranked_request(const AttnArgs& a, int want) {
+  if (a.b.requests > 64) return want;
+  const int lane = threadIdx.x & 63;
+  const int kv = lane < a.b.requests ? a.b.kv_lens[lane] : 0;
+  int rank = 0;
+  for (int r = 0; r < a.b.requests; ++r) {
+    const int other = __builtin_amdgcn_readlane(kv, r);
+    rank += other > kv || (other == kv && r < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < a.b.requests && rank == want));
+}
+
 template <class G>
 __global__ __launch_bounds__(G::THREADS, G::MINW) void k_attn(AttnArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -795,14 +809,18 @@ __global__ __launch_bounds__(G::THREADS, G::MINW) void k_attn(AttnArgs a) {
       return;
     }
   }
-  // One row tile: pair (request, kv head) fastest, so that workgroups that
-  // share keys are 8 apart where the pairs are a multiple of 8 and meet in one
-  // XCD's L2; row tiles from the last (most keys) to the first.
-  const int pairs = a.b.requests * a.c.kv_heads, pair = blockIdx.x % pairs;
-  const int rest = blockIdx.x / pairs, split = rest % a.splits;
-  const int tile = (int)(gridDim.x / pairs / a.splits) - 1 - rest / a.splits;
-  pc.req = pair / a.c.kv_heads;
-  pc.kvh = pair % a.c.kv_heads;
+  // One row tile, those with the most keys first, so that short ones end the
+  // launch: requests from the longest context on, row tiles from the last to
+  // the first.  The kv head runs fastest: workgroups that share keys are 8 apart
+  // where the heads are a multiple of 8 and meet in one XCD's L2.
+  const int tiles = (int)(gridDim.x / a.splits) / (a.b.requests * a.c.kv_heads);
+  int x = blockIdx.x;
+  pc.kvh = x % a.c.kv_heads;
+  x /= a.c.kv_heads;
+  const int split = x % a.splits;
+  x /= a.splits;
+  const int tile = tiles - 1 - x % tiles;
+  pc.req = ranked_request(a, x / tiles);
   const Span span = token_span(a.b.q_start, pc.req, a.b.tokens);
   pc.t0 = span.t0;
   pc.n = span.n;
