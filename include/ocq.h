@@ -446,9 +446,11 @@ ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_
  * scale > 0 and finite, window >= 0 (0: none), sinks >= 0 (0 without a
  * window).  Scores, softmax statistics and sums are fp32; probabilities are
  * rounded to bf16 for the second product.
- * Keys and values past kv_len are not read into the result, whatever the
- * pages hold there.  A page outside [0, num_pages) reads as zeros.  A value
- * row that one token of the batch sees and another does not must be finite.
+ * Rows that no token of the request sees (past kv_len, behind a window) never
+ * reach a result, whatever the pages hold there.  A page outside [0,
+ * num_pages) reads as zeros.  Where a token's value row is not finite, the
+ * results of tokens of its request that do not see it may be NaN too, as 0 x
+ * inf is.
  * workspace_dev: ocq_attention_workspace_bytes(...) bytes (may be 0), contents
  * need not be initialized; calls that share it must be ordered on one stream. */
 size_t ocq_attention_workspace_bytes(int heads, const ocq_kv_cache* cache, const ocq_token_batch* batch, int window,

@@ -410,6 +410,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   }
   const uint32_t s_part = (lane % G::TK & page_mask) * a.c.s_token * 4;
   const uint64_t zero = (uint64_t)g_zero;
+  const KeyRange range = key_range(p_lo, p_hi, a.window, a.sinks);
   uint64_t src[G::QI], s_src = 0;   // rows of the last K stage issued
   bool there[G::QI], s_there = false;
   // Page ids come with the K stage AHEAD before the one that they are for: a
@@ -426,13 +427,20 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
     dma4((uint64_t)entry(st + G::AHEAD < ns ? st + G::AHEAD : st, lane % G::TK), to + G::PART + G::SCB);
     const uint64_t first = k_head + (uint32_t)(key0 & page_mask) * a.c.token;
 #pragma unroll
+    for (int i = 0; i < G::QI; ++i) there[i] = page_there(ids[i], a.c.num_pages);
+    if constexpr (G::KV8) s_there = page_there(sid, a.c.num_pages);
+    if (key0 + G::TK - 1 > range.to || key0 <= range.from) {   // a stage at the edge of what the rows see
+      asm volatile("");
+#pragma unroll
+      for (int i = 0; i < G::QI; ++i) there[i] = there[i] && key_in(key0 + q_row(i), range);
+      if constexpr (G::KV8) s_there = s_there && key_in(key0 + lane % G::TK, range);
+    }
+#pragma unroll
     for (int i = 0; i < G::QI; ++i) {
-      there[i] = row_there(key0 + q_row(i), kv, ids[i], a.c.num_pages);
       src[i] = first + (uint64_t)(uint32_t)ids[i] * a.c.page + part[i];
       dma16<G::EVEN>(there[i] ? src[i] : zero, to + (i * G::WR + wr) * 1024);
     }
     if constexpr (G::KV8) {
-      s_there = row_there(key0 + lane % G::TK, kv, sid, a.c.num_pages);
       s_src = ks_head + (uint64_t)(uint32_t)(key0 & page_mask) * a.c.s_token * 4 +
               (uint64_t)(uint32_t)sid * a.c.s_page * 4 + s_part;
       dma4(s_there ? s_src : zero, to + G::PART);

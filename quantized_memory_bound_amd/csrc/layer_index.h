@@ -59,8 +59,19 @@ OCQ_HD bool key_seen(int j, int place, int window, int sinks) {
 // last one take the last one's (their rows are not loaded).
 OCQ_HD int table_entry(int key, int kv, int page_shift) { return (key < kv ? key : kv - 1) >> page_shift; }
 
-// Whether the row of `key` may be read from page `id`.
-OCQ_HD bool row_there(int key, int kv, int id, int num_pages) { return key < kv && id >= 0 && id < num_pages; }
+// Keys that some row at places p_lo .. p_hi sees: those up to p_hi that lie past
+// `from` or are among the first `sinks`.
+struct KeyRange {
+  int from, to, sinks;
+};
+OCQ_HD KeyRange key_range(int p_lo, int p_hi, int window, int sinks) {
+  return KeyRange{window > 0 && p_lo >= window ? p_lo - window : -1, p_hi, sinks};
+}
+// A row is read if its page is there and some row sees it; else it is taken as
+// zeros: what lies in rows that no token sees (past the context, behind a
+// window) never reaches a sum.
+OCQ_HD bool page_there(int id, int num_pages) { return id >= 0 && id < num_pages; }
+OCQ_HD bool key_in(int key, const KeyRange& k) { return key <= k.to && (key > k.from || key < k.sinks); }
 
 // Offset of a key's row in the pool, without the head's part.  The entry
 // points hold page strides below 2^32 and a page's rows within 2^31.

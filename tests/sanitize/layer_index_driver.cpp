@@ -52,7 +52,14 @@ int main() {
               ++met[key];
               const int e = table_entry(key, kv, shift);
               CHECK(e >= 0 && e < max_pages);
-              if (row_there(key, kv, table[e], num_pages)) {
+              const KeyRange range = key_range(base + row0 / group, base + last / group, window, sinks);
+              bool any = false;
+              for (int row = row0; row <= last; row += group) any |= key_seen(key, base + row / group, window, sinks);
+              any |= key_seen(key, base + last / group, window, sinks);
+              CHECK(key_in(key, range) == any);
+              if (key > range.from && key <= range.to) CHECK(any);   // no test needed inside
+              if (page_there(table[e], num_pages) && key_in(key, range)) {
+                CHECK(key < kv);
                 const uint64_t off = row_offset(key, table[e], shift, 1u << (shift + 20), 1u << 20);
                 CHECK(off < (uint64_t)num_pages << (shift + 20));
               }

@@ -358,6 +358,36 @@ def test_attention_what_lies_past_the_context_does_not_reach_it():
             check_attention(_bf((2 * n, 8, 128), g), cache, batch, news, kvs)
 
 
+def test_attention_what_lies_behind_a_window_does_not_reach_it():
+    """NaN in the rows that no token of a batch sees any more, some of their pages gone from the table."""
+    g = _gen(17)
+    for e4m3 in (False, True):
+        for n, kv, window, sinks in ((1, 1000, 100, 3), (13, 700, 64, 0), (3, 2000, 333, 17), (1, 90, 7, 70)):
+            batch, pages = make_batch([n], [kv], 16, g)
+            cache = make_cache(pages, 2, 16, 128, e4m3, g)
+            p = torch.arange(sinks, kv - n - window + 1, device=DEV)       # behind the first token's window
+            ids = batch.page_table[0][p // 16].long()
+            if e4m3:
+                cache.k.view(torch.uint8)[ids, :, p % 16] = 0x7F
+                cache.v.view(torch.uint8)[ids, :, p % 16] = 0x7F
+                cache.v_scale[ids, :, p % 16] = float("inf")
+            else:
+                cache.k[ids, :, p % 16] = float("inf")
+                cache.v[ids, :, p % 16] = float("nan")
+            q = _bf((n, 8, 128), g)
+            out, lse = ocq.paged_attention(q, cache, batch, window=window, sinks=sinks, want_lse=True)
+            full = torch.arange(max(1, -(-sinks // 16)), (kv - n - window + 1) // 16, device=DEV)   # whole pages gone
+            batch.page_table[0, full] = -1
+            again = ocq.paged_attention(q, cache, batch, window=window, sinks=sinks, want_lse=True)
+            assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+            for x in (cache.k, cache.v):
+                x.view(torch.uint8 if e4m3 else torch.int16)[ids, :, p % 16] = 0
+            if e4m3:
+                cache.v_scale[ids, :, p % 16] = 0
+            a, b = check_attention(q, cache, batch, [n], [kv], window=window, sinks=sinks)
+            assert torch.equal(out, a) and torch.equal(lse, b)
+
+
 def test_attention_pages_that_are_none_read_as_zeros():
     g = _gen(12)
     for e4m3 in (False, True):
