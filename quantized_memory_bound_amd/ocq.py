@@ -407,29 +407,33 @@ ROPE_SCALINGS = ("none", "linear", "ntk", "yarn")
 
 _torch = None
 _raw_stream = None
+_current_device = None
 
 
 def _gpu(t, name):
     """The device index of the CUDA tensor t, which must be the current device's."""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     if _torch is None:
         import torch
         _torch = torch
         # the handle of the current stream without a Stream object: 0.1 us instead of 2.8
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda i: torch.cuda.current_stream(i).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     i = t.get_device() if hasattr(t, "get_device") else -1
     if i < 0:
         raise OcqError(ERR_INVALID_ARG, "%s must be a CUDA tensor" % name)
-    if i != _torch.cuda.current_device():
+    if i != _current_device():
         raise OcqError(ERR_INVALID_ARG, "%s is on cuda:%d, not on the current device" % (name, i))
     return i
 
 
 def _bf16_rows(t, name, index, shape):
     """Raise unless t is a bf16 tensor of this shape on device `index`, its last axis contiguous."""
-    if not hasattr(t, "get_device"):
+    if t is None or not hasattr(t, "get_device"):
         raise OcqError(ERR_INVALID_ARG, "%s must be a tensor" % name)
+    if t.dtype is _torch.bfloat16 and t.get_device() == index and t.shape == shape and t.stride(-1) == 1:
+        return
     if t.dtype is not _torch.bfloat16 or t.get_device() != index:
         raise OcqError(ERR_INVALID_ARG, "%s must be bfloat16 on cuda:%d, got %s on %s" %
                        (name, index, t.dtype, t.device))

@@ -314,6 +314,46 @@ def test_attention_long(dim, e4m3, news, kvs):
     check_attention(_bf((sum(news), 8, dim), g), cache, batch, news, kvs)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,group", [(1, 4), (5, 5), (13, 4), (3, 40)])
+@pytest.mark.parametrize("kv", [511, 512, 513, 640, 1024, 1025, 4097])
+def test_attention_cut_contexts(n, group, kv, e4m3):
+    """Contexts around whole numbers of tiles and pieces, for each kernel by the rows of a request."""
+    g = _gen(kv + n)
+    news, kvs = [n, n, n], [kv, kv // 3 + n, n]
+    batch, pages = make_batch(news, kvs, 32, g)
+    cache = make_cache(pages, 1, 32, 64, e4m3, g)
+    check_attention(_bf((sum(news), group, 64), g), cache, batch, news, kvs)
+    assert not batch.counters.any()
+
+
+@pytest.mark.parametrize("requests", [64, 65, 200, 256, 300])
+@pytest.mark.parametrize("new", [1, 13])
+def test_attention_many_requests(requests, new):
+    rng = np.random.default_rng(requests + new)
+    news = [int(x) for x in rng.integers(0, new + 1, requests)]
+    news[0] = new
+    kvs = [n + int(x) for n, x in zip(news, rng.integers(0, 90, requests))]
+    kvs[1], kvs[-1] = news[1] + 3000, news[-1] + 5000
+    g = _gen(requests)
+    batch, pages = make_batch(news, kvs, 16, g)
+    for e4m3 in (False, True):
+        cache = make_cache(pages, 2, 16, 64, e4m3, g)
+        check_attention(_bf((sum(news), 8, 64), g), cache, batch, news, kvs)
+
+
+def test_attention_rows_that_see_nothing():
+    """Contexts shorter than the new tokens, and empty ones: out 0, lse -inf, the other rows as ever."""
+    g = _gen(18)
+    for news, kvs in (([3, 5, 1, 2], [0, 2, 0, 900]), ([70, 9], [64, 0]), ([13, 13], [6, 2000])):
+        batch, pages = make_batch(news, kvs, 16, g)
+        for e4m3 in (False, True):
+            cache = make_cache(pages, 2, 16, 128, e4m3, g)
+            q = _bf((sum(news), 8, 128), g)
+            out, lse = check_attention(q, cache, batch, news, kvs)
+            assert torch.isinf(lse).any()
+
+
 @pytest.mark.parametrize("n", [1, 13, 70])
 def test_attention_scores_of_every_size(n):
     """Large scores (one key takes all), a moving maximum, scores far below zero, equal keys."""
