@@ -401,7 +401,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   // first key of the wave's key group in stage st: a multiple of TK, so that a
   // row's place in its page is that of the first key plus a part of its own
   auto tile_key = [&](int st) { return tile_of(pc.tiles, pc.s0 + st) * G::TT + wk * G::TK; };
-  auto q_row = [&](int i) { return ((i * G::WR + wr) * 64 + lane) / G::CH; };   // row of load i
+  auto q_row = [&](int i) {   // row of load i of K and V, or (i = QI) of the scales
+    return i < G::QI ? ((i * G::WR + wr) * 64 + lane) / G::CH : lane % G::TK;
+  };
   uint32_t part[G::QI];
 #pragma unroll
   for (int i = 0; i < G::QI; ++i) {
@@ -421,8 +423,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
     const int key0 = tile_key(st);
     int ids[G::QI], sid = 0;
 #pragma unroll
-    for (int i = 0; i < G::QI; ++i) ids[i] = id_of(q_row(i));
-    if constexpr (G::KV8) sid = id_of(lane % G::TK);
+    for (int i = 0; i < G::QI; ++i) ids[i] = id_of(i);
+    if constexpr (G::KV8) sid = id_of(G::QI);
     uint8_t* const to = ring + slot;
     dma4((uint64_t)entry(st + G::AHEAD < ns ? st + G::AHEAD : st, lane % G::TK), to + G::PART + G::SCB);
     const uint64_t first = k_head + (uint32_t)(key0 & page_mask) * a.c.token;
@@ -616,13 +618,20 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   if (ns > 0) {
     constexpr auto most = [](int n) constexpr { return n < 63 ? n : 63; };
     auto held = [&](int slot) {   // page ids that came with the K stage in `slot`
-      return [&, slot](int row) { return *(const int*)(ring + slot + G::PART + G::SCB + 4 * row); };
+      return [&, slot](int i) { return *(const int*)(ring + slot + G::PART + G::SCB + 4 * q_row(i)); };
     };
+    // the first stages' ids before any of their loads: a wait for an id is one
+    // for every load before it
+    int first_ids[G::NST][G::QI + 1];
+#pragma unroll
+    for (int st = 0; st < G::NST; ++st)
+#pragma unroll
+      for (int i = 0; i < G::QI + G::KV8; ++i) first_ids[st][i] = *entry(st < ns ? st : 0, q_row(i));
 #pragma unroll
     for (int st = 0; st < G::NST; ++st)
       if (st < ns) {
         if (st > 0) issue_v(v_slot(st - 1));
-        issue_k(st, k_slot(st), [&](int row) { return *entry(st, row); });
+        issue_k(st, k_slot(st), [&](int i) { return first_ids[st][i]; });
       }
     if (ns < G::NST) issue_v(v_slot(0));
     if (G::NST <= ns) wait_vm<most((G::NST - 1) * G::PW)>();
