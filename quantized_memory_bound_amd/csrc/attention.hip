@@ -900,7 +900,7 @@ auto visit_rows(int64_t rows, F f) {
   if (rows <= 16) return f(Geo<D, KV8, 16, 1, D == 256 && !KV8 ? 2 : 4, 32, D == 256 ? 1 : 2>{});
   if constexpr (D < 256)
     if (rows <= 32) return f(Geo<D, KV8, 32, 1, 4, 32, 2>{});
-  if (rows <= 64) return f(Geo<D, KV8, 32, 2, 2, 32, D == 256 ? 1 : 2>{});
+  if (rows <= 64) return f(Geo<D, KV8, 32, 2, 2, D == 128 ? 64 : 32, D == 256 ? 1 : 2>{});
   return f(Geo<D, KV8, 32, 4, 1, D == 256 ? 32 : 64, D == 256 ? 1 : D == 64 ? 3 : 2>{});
 }
 template <class F>
