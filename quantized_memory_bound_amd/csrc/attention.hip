@@ -14,15 +14,30 @@
 //                  second operand: only the order in which a step's keys are
 //                  summed is fixed by the layout, and V is read in that order.
 // Row statistics and the output's rescaling stay within a lane.  K and V come
-// by direct-to-LDS loads into a ring of NST stages (16-byte chunks of a row
-// xor-swizzled by the row, so that both the row reads of K and the transposing
-// reads of V spread over the banks); V^T fragments come from LDS through the
+// by direct-to-LDS loads into rings of two stages (16-byte chunks of a row
+// xor-swizzled by the row, see swz), K one stage ahead of V: the products of
+// the next stage run on the matrix cores while the vector unit forms the
+// probabilities of this one.  V^T fragments come from LDS through the
 // transposing reads.  E4M3 codes are converted exactly to bf16; the scale of a
 // key multiplies its score, the scale of a value its probability.
 //
 // The maximum moves only when a score exceeds it by 2^8 (in the exponent of
 // 2): probabilities up to 256 are as exact in bf16 and fp32 as those up to 1,
 // and most tiles then need neither a cross-lane maximum nor a rescaling.
+//
+// Four kernels by the rows of a request (visit_rows), two ways to cut the work
+// (attn_plan).  Measured on MI355X, head size 128, 32 heads on 8 kv heads, and
+// what bounds each:
+//   4 requests, one token over 131072 keys, bf16: 268-280 us, 6.3-6.6 TB/s of
+//     the 7.1 that a streaming read reaches: HBM;
+//   16 x 13 tokens over up to 4096 keys, bf16: 49-52 us, 29 of them reading at
+//     the streaming rate: before the first keys are there (5.7 us), writing and
+//     joining the parts (about 9 us) and pieces that end at different times;
+//   64 x 13 over up to 8192, E4M3: 175-188 us (HBM alone 119, products 69):
+//     conversions and softmax on the vector unit, matrix cores 32 % busy;
+//   2048 new tokens over 10007 keys, bf16: 920-945 TFLOP/s (8192 over 12288:
+//     1005; a library product of 8192^3: 1202): vector unit and matrix cores
+//     together, 45 % of the matrix cores' cycles.
 #include "gemm_core.h"
 #include "layer_dev.h"
 #include "layer_index.h"
@@ -42,8 +57,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLow = -3.4028234663852886e38f;   // below every score that is visible
 constexpr float kSlack = 8.0f;                    // see above
 
-constexpr int kTargetGroups = 512, kMinTiles = 4, kMaxSplits = 256;   // see plan_of
-constexpr int kEvenRequests = 256;                // requests of a batch shared out evenly
+constexpr int kTargetGroups = 512, kMinTiles = 4, kMaxSplits = 256;   // see attn_plan
+constexpr int kEvenRequests = 256;                // requests of a batch that is cut into pieces
 
 // what a table entry outside the pool reads as
 __device__ const v4i g_zero[1] = {};
@@ -227,12 +242,29 @@ __device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int piece
   }
   total = __builtin_amdgcn_readlane(wave_scan(total), 63) * kvh;
   const int segments = a.b.requests * kvh;
+  int id = lane;   // the request that a lane holds (less its base)
   float per;
   if (2 * segments > a.slots) {
     // about as many segments as slots, or more: only those of one and a half
     // mean shares and more are cut (pieces of half a share: 64 x 13 rows over
     // 8192 keys in E4M3 221 us instead of 203)
     per = (float)(total / 2 * 3 / a.slots + 1);
+    if (a.e4m3 && a.b.requests <= 64) {
+      // The longest first, so that a CU's second workgroup is a short one: E4M3
+      // keys are bound by the CUs' vector units (64 x 13 rows over 8192: 189 ->
+      // 181 us), bf16 keys by HBM (40 x 13 rows over 4096: 99 -> 102).
+      int rank = 0;
+      for (int r = 0; r < a.b.requests; ++r) {
+        const int other = __builtin_amdgcn_readlane(T, r);
+        rank += other > T || (other == T && r < lane);
+      }
+      rank = lane < a.b.requests ? 4 * rank : 4 * lane;
+      T = __builtin_amdgcn_ds_permute(rank, T);
+      t0 = __builtin_amdgcn_ds_permute(rank, t0);
+      n = __builtin_amdgcn_ds_permute(rank, n);
+      kv = __builtin_amdgcn_ds_permute(rank, kv);
+      id = __builtin_amdgcn_ds_permute(rank, id);
+    }
   } else {
     // the smallest pieces that fit the slots: eight candidates from the mean to
     // the bound, each summed by eight lanes
@@ -261,7 +293,7 @@ __device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int piece
     const uint64_t who = __ballot(piece < end && piece >= end - c * kvh);
     if (who) {
       const int l = __builtin_ctzll(who);
-      f.req = base + l;
+      f.req = base + __builtin_amdgcn_readlane(id, l);
       f.t0 = __builtin_amdgcn_readlane(t0, l);
       f.n = __builtin_amdgcn_readlane(n, l);
       f.kv = __builtin_amdgcn_readlane(kv, l);
@@ -894,13 +926,23 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
 // The kernel for a call whose largest request has `rows` rows per kv head.
 // Up to 16 and 32 rows each wave takes all of them and a part of the keys,
 // without barriers; up to 64, two waves share the keys of two; beyond, four
-// waves of 32 rows share every key tile.  Key groups and stages fill the LDS.
+// waves of 32 rows share every key tile.  Against the next kernel, us:
+//   16-row tiles: one token of one request over 131072 keys 92 (98), E4M3, four
+//     requests 153 (158), 16 x 13 rows of one query head a kv head 38.4 (39.2);
+//   32 rows: 16 x 13 tokens x 2 heads over 4096 keys 44.9 (47.6);
+//   64 rows: 16 x 13 x 4 over 4096 keys 49.7 (54.5), 64 x 13 x 4 over 8192 in
+//     E4M3 195 (272); a 13-row window of 1024 at head size 64 19.6 (21.9).
+// At most 160 KB of LDS: two key waves for bf16 rows of 256, which have no 32-row
+// kernel either (its registers do not fit).  64-key stages where the registers
+// and two workgroups a CU allow them (E4M3 at 128: 198 -> 189; bf16 would leave
+// one workgroup a CU: 40 x 13 rows over 4096 keys 99 -> 131).  Three waves a SIMD
+// at head size 64 for many rows (309 against 348), two for up to 64 (20.5, 22.8).
 template <int D, bool KV8, class F>
 auto visit_rows(int64_t rows, F f) {
   if (rows <= 16) return f(Geo<D, KV8, 16, 1, D == 256 && !KV8 ? 2 : 4, 32, D == 256 ? 1 : 2>{});
   if constexpr (D < 256)
     if (rows <= 32) return f(Geo<D, KV8, 32, 1, 4, 32, 2>{});
-  if (rows <= 64) return f(Geo<D, KV8, 32, 2, 2, D == 128 ? 64 : 32, D == 256 ? 1 : 2>{});
+  if (rows <= 64) return f(Geo<D, KV8, 32, 2, 2, KV8 && D == 128 ? 64 : 32, D == 256 ? 1 : 2>{});
   return f(Geo<D, KV8, 32, 4, 1, D == 256 ? 32 : 64, D == 256 ? 1 : D == 64 ? 3 : 2>{});
 }
 template <class F>
@@ -914,11 +956,15 @@ auto visit(int dim, bool e4m3, int64_t rows, F f) {
 
 // How a call is laid out.
 //  * All rows of a request in one tile and more keys than one piece: pieces,
-//    for two workgroups' worth of LDS (or one) on every CU.
+//    for two workgroups' worth of LDS (or one) on every CU.  Against splits of
+//    equal number, or none where there are 512 pairs: 16 x 13 x 4 rows over 4096
+//    keys 49.7 us (60.3), 16 x 13 over 2048 38.8 (46.0), a window of 1024 19.6
+//    (20.6); 512 equal pairs lose 1 to 2 %, a batch with one long context gains.
 //  * Several row tiles per request but few in all: each tile's keys in equal
 //    splits, none below four key tiles of the longest request.
 //  * Else one workgroup per row tile, all its keys: enough of them to fill the
-//    GPU by themselves, or too few keys to be worth a second launch.
+//    GPU by themselves, or at most four key tiles (a join takes longer than
+//    those: 257 keys 8.7 us in all).
 AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads, int kv_heads, int dim, int e4m3,
                    int window, int sinks, int64_t cap) {
   const int64_t rows = (int64_t)max_new * (heads / kv_heads);
@@ -930,10 +976,11 @@ AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads,
     const int64_t pairs = (int64_t)requests * kv_heads, tiles = (rows + G::ROWS - 1) / G::ROWS;
     const int64_t key_tiles = (keys + G::TT - 1) / G::TT;
     if (key_tiles <= kMinTiles) return p;
-    if (G::EVEN && requests <= kEvenRequests && pairs < 4 * G::RESIDENT && pairs <= OCQ_ATTENTION_COUNTERS && pairs * (cap / G::TT + 1) < (1 << 30)) {
+    if (G::EVEN && requests <= kEvenRequests && pairs < 4 * G::RESIDENT && pairs <= OCQ_ATTENTION_COUNTERS &&
+        pairs * (cap / G::TT + 1) < (1 << 30)) {
       p.even = 1;
       p.slots = G::RESIDENT;
-      p.groups = (int)(2 * pairs > p.slots ? 2 * p.slots + pairs : p.slots);   // no fewer than there can be pieces
+      p.groups = (int)(2 * pairs > p.slots ? p.slots + pairs : p.slots);   // no fewer than there can be pieces
       p.part_rows = (size_t)p.groups * G::ROWS;
       return p;
     }
