@@ -389,9 +389,11 @@ __device__ __forceinline__ void put_joined(const AttnArgs& a, size_t at, int d, 
 // A part's four values (and its lse with d = 0), for a workgroup on any XCD to
 // read in the same launch: device-scope stores (sc1) write through the XCD's
 // L2.  They are visible to device-scope loads once the wave's count of
-// outstanding stores is 0.
+// outstanding stores is 0.  The wait state keeps the compiler's next instruction
+// from overwriting the data as the store reads it (it inserts one itself after
+// stores of more than 8 bytes that it can see).
 __device__ __forceinline__ void put_part(const AttnArgs& a, size_t row, int d, int D, v4f y, float lse2) {
-  asm volatile("global_store_dwordx4 %0, %1, off sc1" ::"v"(a.part_o + row * D + d), "v"(y) : "memory");
+  asm volatile("global_store_dwordx4 %0, %1, off sc1\n\ts_nop 0" ::"v"(a.part_o + row * D + d), "v"(y) : "memory");
   if (d == 0) __hip_atomic_store(a.part_lse + row, lse2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
