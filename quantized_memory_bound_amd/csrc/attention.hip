@@ -459,6 +459,13 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
 #pragma unroll
     for (int i = 0; i < G::QI; ++i) ids[i] = id_of(i);
     if constexpr (G::KV8) sid = id_of(G::QI);
+    if constexpr (G::WR == 1) {
+      // The next ids go where these lay: they have to be read, not only asked
+      // for, before (waves that share a stage read them from the other slot).
+#pragma unroll
+      for (int i = 0; i < G::QI; ++i) asm volatile("" : "+v"(ids[i]) : : "memory");
+      if constexpr (G::KV8) asm volatile("" : "+v"(sid) : : "memory");
+    }
     uint8_t* const to = ring + slot;
     dma4((uint64_t)entry(st + G::AHEAD < ns ? st + G::AHEAD : st, lane % G::TK), to + G::PART + G::SCB);
     const uint64_t first = k_head + (uint32_t)(key0 & page_mask) * a.c.token;

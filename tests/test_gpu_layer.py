@@ -342,6 +342,31 @@ def test_attention_many_requests(requests, new):
         check_attention(_bf((sum(news), 8, 64), g), cache, batch, news, kvs)
 
 
+@pytest.mark.parametrize("dim,e4m3,requests,n,kv", [(128, False, 1, 1, 51877), (256, False, 5, 2, 11420),
+                                                    (256, False, 30, 1, 4000), (128, True, 8, 13, 6000),
+                                                    (128, False, 16, 13, 4096)])
+def test_attention_of_long_cut_contexts_call_after_call(dim, e4m3, requests, n, kv):
+    """Two batches in turn, many pieces and stages each, over one workspace: the formula's values, and every further
+    call the same bits (a stage that reads another page's keys, or a part of the call before, differs)."""
+    g = _gen(kv)
+    ws, sides = None, []
+    for _ in range(2):
+        news, kvs = [n] * requests, [kv - 37 * r for r in range(requests)]
+        batch, pages = make_batch(news, kvs, 32, g)
+        cache = make_cache(pages, 4, 32, dim, e4m3, g)
+        q = _bf((n * requests, 4 * (8 if n == 1 else 4), dim), g)
+        batch.of(len(q))
+        if ws is None:
+            ws = torch.empty(max(16, ocq.attention_workspace_bytes(q.shape[1], cache, batch)),
+                             dtype=torch.uint8, device=DEV)
+        out, lse = check_attention(q, cache, batch, news, kvs, workspace=ws)
+        sides.append((q, cache, batch, out.clone(), lse.clone()))
+    for _ in range(40):
+        for q, cache, batch, out, lse in sides:
+            a, b = ocq.paged_attention(q, cache, batch, want_lse=True, workspace=ws)
+            assert torch.equal(a, out) and torch.equal(b, lse)
+
+
 def test_attention_rows_that_see_nothing():
     """Contexts shorter than the new tokens, and empty ones: out 0, lse -inf, the other rows as ever."""
     g = _gen(18)
