@@ -557,10 +557,10 @@ class TokenBatch:
     """The new tokens of one step: request r has rows q_start[r] .. q_start[r + 1] of the token axis, kv_lens[r]
     tokens in the cache with the new ones, and pages page_table[r].
 
-    q_start int32 [requests + 1], kv_lens int32 [requests], page_table int32 [requests, max_pages] (rows strided at
-    will): CUDA tensors whose contents may change between calls.  tokens (the rows of q), max_new and max_kv are
-    host numbers: bounds of the new tokens and of kv_lens of any request.  Attention calls over one batch use its
-    counters: they are ordered on one stream.
+    q_start int32 [requests + 1], kv_lens int32 [requests], page_table int32 [requests, max_pages] (its rows max_pages
+    entries or more apart): CUDA tensors whose contents may change between calls.  tokens (the rows of q), max_new and
+    max_kv are host numbers: bounds of the new tokens and of kv_lens of any request.  Attention calls over one batch use
+    its counters: they are ordered on one stream.
     """
 
     def __init__(self, q_start, kv_lens, page_table, max_new, max_kv, tokens=None):
@@ -574,12 +574,18 @@ class TokenBatch:
                 page_table.dim() != 2 or page_table.shape[0] != requests or \
                 (page_table.shape[1] > 1 and page_table.stride(1) != 1):
             raise OcqError(ERR_INVALID_ARG, "page_table must be int32 [%d, max_pages], its rows contiguous" % requests)
+        stride = page_table.stride(0)
+        if requests <= 1:
+            stride = max(stride, page_table.shape[1])   # of a row that has no next one: any
+        elif stride < page_table.shape[1]:
+            raise OcqError(ERR_INVALID_ARG, "rows of page_table are %d entries apart, fewer than their %d (a table "
+                           "that requests share has to be copied: .contiguous())" % (stride, page_table.shape[1]))
         self.q_start, self.kv_lens, self.page_table, self.device = q_start, kv_lens, page_table, dev
         self.requests, self.tokens = requests, None
         self.counters = torch.zeros(ATTENTION_COUNTERS, dtype=torch.int32, device=dev)   # 0 between calls
         self.struct = TokenBatchStruct(q_start.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
-                                       max(page_table.stride(0), page_table.shape[1]), requests, 0,
-                                       page_table.shape[1], max_new, max_kv, self.counters.data_ptr())
+                                       stride, requests, 0, page_table.shape[1], max_new, max_kv,
+                                       self.counters.data_ptr())
         self.ref = ctypes.byref(self.struct)
         if tokens is not None:
             self.of(tokens)
