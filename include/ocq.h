@@ -426,7 +426,8 @@ ocq_status ocq_rope_frequencies(int rot, double base, int scaling, double factor
  * place in its request.  q_out_dev: [tokens, heads, head_dim] contiguous, or q
  * itself where that is contiguous.
  * bf16 caches receive bf16(k'), bf16(v); E4M3 caches the codes of the fp32 k'
- * and of v and their scales.  A token whose place is outside [0, max_pages *
+ * and of v and their scales (a token's head with a value that is not finite:
+ * scale NaN, codes 0).  A token whose place is outside [0, max_pages *
  * page_size) or whose page is outside [0, num_pages) is not appended (its q is
  * rotated all the same).  Two new tokens must not share a cache slot. */
 ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, const void* k_dev,

@@ -10,7 +10,8 @@
 // The angle is reduced to a fraction of a turn in 64 bits (at position 10^6 a
 // product in 32 bits would be off by a tenth of a radian), the sine and
 // cosine are taken of that fraction in 32.  An E4M3 cache takes codes of the
-// rotated 32-bit values with one scale per token and head, max / 448.
+// rotated 32-bit values with one scale per token and head, max / 448; a head with
+// a value that is not finite has scale NaN, so that it stays visible.
 //
 // One workgroup per token: the token's rot/2 sines and cosines are made once,
 // in LDS, for all heads.  A lane owns 16 elements of a head, both halves of
@@ -115,12 +116,15 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
         store8((uint16_t*)pool + d1, x + 8);
       }
     } else {
-      float amax = 0.0f;
+      uint32_t amax = 0u;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(x[j]));
+      for (int j = 0; j < 16; ++j) amax = max_mag(amax, x[j]);
 #pragma unroll
-      for (int o = 1; o < LPH; o <<= 1) amax = fmaxf(amax, __shfl_xor(amax, o));
-      const float s = amax / 448.0f;
+      for (int o = 1; o < LPH; o <<= 1) {
+        const uint32_t other = __shfl_xor(amax, o);
+        amax = other > amax ? other : amax;
+      }
+      const float s = e4m3_scale(amax);
       const float rcp = s > 0.0f ? 1.0f / s : 0.0f;
       float lo[8], hi[8];
 #pragma unroll
