@@ -339,7 +339,7 @@ int ocq_last_requant_in_gateup(void);
  *   y = h / sqrt(mean(h^2) + eps) * weight (fp32, of the unrounded h)
  *   scales = fl32(max|y| / 448), codes = E4M3(fl32(y / scale)); a zero row has
  *   scale 0 and codes 0, a row whose squares do not sum to a finite fp32
- *   number has scale NaN and codes 0.
+ *   number, or with a y that is not finite, has scale NaN and codes 0.
  * x_bf16_dev, residual_bf16_dev: [rows, hidden] with row strides x_stride and
  * residual_stride; weight_bf16_dev [hidden]; residual_out_bf16_dev and
  * y_bf16_dev: [rows, hidden] contiguous, each nullable; codes_dev (uint8

@@ -26,17 +26,10 @@ __device__ __forceinline__ void unpack8_bf16(const v4i& u, float* f) {
   }
 }
 
-// Largest magnitude of a row's values, as bits: those of finite values order as
-// the values do, below infinity's and every NaN's (a floating maximum would skip
-// a NaN).
-__device__ __forceinline__ uint32_t max_mag(uint32_t m, float v) {
-  const uint32_t u = __float_as_uint(v) & 0x7FFFFFFFu;
-  return u > m ? u : m;
-}
+// The larger of m and |v|, NaN if either is one (fmaxf would skip it).
+__device__ __forceinline__ float max_mag(float m, float v) { return __builtin_elementwise_maximum(m, fabsf(v)); }
 // The scale of an E4M3 row whose largest magnitude is m; NaN (with codes 0) if one
 // of its values is not finite, so that whoever reads the row sees it.
-__device__ __forceinline__ float e4m3_scale(uint32_t m) {
-  return m < 0x7F800000u ? __uint_as_float(m) / 448.0f : __builtin_nanf("");
-}
+__device__ __forceinline__ float e4m3_scale(float m) { return m < __builtin_inff() ? m / 448.0f : __builtin_nanf(""); }
 
 }  // namespace ocq

@@ -75,14 +75,14 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_norm(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       h[p][j] = h[p][j] * inv * wf[j];
-      amax = fmaxf(amax, fabsf(h[p][j]));
+      amax = max_mag(amax, h[p][j]);
     }
     if (live && u < units && a.y)
       *(v4i*)(a.y + (size_t)row * a.hidden + u * 8) =
           pack8_bf16(h[p]);
   }
   if (!a.codes) return;
-  amax = wave_max(amax);
+  amax = wave_max(amax < __builtin_inff() ? amax : __builtin_inff());   // NaN as infinity, which fmaxf keeps
   if constexpr (WPR > 1) {
     if (lane == 0) s_max[slot][wr] = amax;
     lds_barrier();
@@ -90,8 +90,8 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_norm(NormArgs a) {
     for (int k = 0; k < WPR; ++k) amax = fmaxf(amax, s_max[slot][k]);
   }
   // a row whose squares do not sum to a finite number has no norm: its scale
-  // says so (the maximum skips NaN)
-  const float s = ss < __builtin_inff() ? amax / 448.0f : __builtin_nanf("");
+  // says so, as it does for a y that is not finite
+  const float s = ss < __builtin_inff() ? e4m3_scale(amax) : __builtin_nanf("");
   const float rcp = s > 0.0f ? 1.0f / s : 0.0f;
   if (!live) return;
 #pragma unroll

@@ -116,14 +116,11 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
         store8((uint16_t*)pool + d1, x + 8);
       }
     } else {
-      uint32_t amax = 0u;
+      float amax = 0.0f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) amax = max_mag(amax, x[j]);
 #pragma unroll
-      for (int o = 1; o < LPH; o <<= 1) {
-        const uint32_t other = __shfl_xor(amax, o);
-        amax = other > amax ? other : amax;
-      }
+      for (int o = 1; o < LPH; o <<= 1) amax = max_mag(amax, __shfl_xor(amax, o));
       const float s = e4m3_scale(amax);
       const float rcp = s > 0.0f ? 1.0f / s : 0.0f;
       float lo[8], hi[8];

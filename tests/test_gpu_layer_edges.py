@@ -52,3 +52,22 @@ def test_append_of_values_that_are_not_finite(dim, rot, which):
     assert torch.isnan(out[sees].float()).all()
     if which == "k":
         assert torch.isnan(lse[sees]).all() and torch.isfinite(out[~sees].float()).all()
+
+
+# ---------------------------------------------------------------- norm
+
+@pytest.mark.parametrize("hidden", [72, 2048, 4096, 8192, 16384, 32768, 65536])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_norm_with_a_weight_that_is_not_finite(hidden, value):
+    """Every row's y is not finite in that place: scale NaN, codes 0; where the row is 0 there (0 x inf) as well."""
+    g = _gen(hidden)
+    x, w = _bf((5, hidden), g), _bf((hidden,), g)
+    w[hidden - 3] = value
+    x[2, hidden - 3] = 0
+    _, y, c, s = ocq.add_rmsnorm(x, w, 1e-6, want_y=True)
+    assert torch.isnan(s).all() and not c.view(torch.uint8).any()
+    got = y.float().isfinite()
+    assert not got[:, hidden - 3].any() and got[:, : hidden - 3].all() and got[:, hidden - 2:].all()
+    w[hidden - 3] = 1
+    s = ocq.add_rmsnorm(x, w, 1e-6)[3]
+    assert torch.isfinite(s).all()
