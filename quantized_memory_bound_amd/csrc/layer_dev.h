@@ -32,4 +32,16 @@ __device__ __forceinline__ float max_mag(float m, float v) { return __builtin_el
 // of its values is not finite, so that whoever reads the row sees it.
 __device__ __forceinline__ float e4m3_scale(float m) { return m < __builtin_inff() ? m / 448.0f : __builtin_nanf(""); }
 
+// What e4m3x8_quot takes for a row of scale s: s and its reciprocal (0 for a zero
+// row), of the values times `up`.  up is 1 but for scales below 2^-126: from 2^-128
+// down the reciprocal would overflow, so values and scale grow by 2^64 first,
+// which is exact and leaves the quotients as they are.
+struct Quot {
+  float s, rcp, up;
+};
+__device__ __forceinline__ Quot e4m3_quot_of(float s) {
+  const float up = s > 0.0f && s < 0x1p-126f ? 0x1p64f : 1.0f;
+  return Quot{s * up, s > 0.0f ? 1.0f / (s * up) : 0.0f, up};
+}
+
 }  // namespace ocq

@@ -92,13 +92,20 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_norm(NormArgs a) {
   // a row whose squares do not sum to a finite number has no norm: its scale
   // says so, as it does for a y that is not finite
   const float s = ss < __builtin_inff() ? e4m3_scale(amax) : __builtin_nanf("");
-  const float rcp = s > 0.0f ? 1.0f / s : 0.0f;
+  const Quot qt = e4m3_quot_of(s);
   if (!live) return;
+  if (qt.up > 1.0f) {
+    asm volatile("");   // a branch that is hardly ever taken
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[p][j] *= qt.up;
+  }
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     const int u = (p * WPR + wr) * 64 + lane;
     if (u < units) {
-      const v2u c = s > 0.0f ? e4m3x8_quot(h[p], s, rcp) : v2u{0u, 0u};
+      const v2u c = s > 0.0f ? e4m3x8_quot(h[p], qt.s, qt.rcp) : v2u{0u, 0u};
       *(v2u*)(a.codes + (size_t)row * a.hidden + u * 8) = c;
     }
   }

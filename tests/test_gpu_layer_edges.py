@@ -71,3 +71,52 @@ def test_norm_with_a_weight_that_is_not_finite(hidden, value):
     w[hidden - 3] = 1
     s = ocq.add_rmsnorm(x, w, 1e-6)[3]
     assert torch.isfinite(s).all()
+
+
+# ---------------------------------------------------------------- rows next to zero
+
+TINY = [2.0 ** -110, 2.0 ** -119, 2.0 ** -121, 2.0 ** -124, 2.0 ** -126]
+
+
+def _check_tiny(codes, scales, ref, what):
+    """Scales below 2^-126 are rounded to a multiple of 2^-149; each code is the nearest to the quotient by its own
+    scale: half a step of 2^-4 relative or 2^-10 (subnormal), and the largest may be clipped by the scale's rounding."""
+    ref = ref.double()
+    s, got = scales.double(), codes.view(E4M3).double() * scales.double()[..., None]
+    exact = ref.abs().amax(-1) / 448
+    assert torch.all((s - exact).abs() <= exact * 2.0 ** -20 + 2.0 ** -149), what
+    tol = ref.abs() * (2.0 ** -4 + 2.0 ** -18) + s[..., None] * (2.0 ** -10 + 2.0 ** -18) + 448 * 2.0 ** -149
+    bad = ~((got - ref).abs() <= tol)
+    assert not bad.any(), "%s: %d of %d codes off" % (what, int(bad.sum()), bad.numel())
+
+
+@pytest.mark.parametrize("size", TINY)
+def test_append_of_tiny_values(size):
+    """The scale of a head may be so small that its reciprocal overflows."""
+    g = _gen(21)
+    batch, pages = make_batch([13], [40], 16, g)
+    cache = make_cache(pages, 2, 16, 128, True, g)
+    k, v = ((_bf((13, 2, 128), g).clamp(-4, 4).float() * size).to(torch.bfloat16) for _ in range(2))
+    k[3, 0, 1:] = v[3, 0, 1:] = 0
+    zero = torch.zeros(13, dtype=torch.int32, device=DEV)                 # position 0: nothing is turned
+    ocq.rope_append(_bf((13, 4, 128), g), k, v, ocq.Rope.make(128, device=DEV), cache, batch, positions=zero)
+    ids, rows = _slots(batch, cache, 0, torch.arange(27, 40, device=DEV))
+    _check_tiny(cache.k[ids, :, rows], cache.k_scale[ids, :, rows], k, "k")
+    _check_tiny(cache.v[ids, :, rows], cache.v_scale[ids, :, rows], v, "v")
+
+
+@pytest.mark.parametrize("size", TINY)
+@pytest.mark.parametrize("hidden", [512, 2048, 16384, 65536])
+def test_norm_to_tiny_values(size, hidden):
+    g = _gen(22)
+    x, w = _bf((3, hidden), g).clamp(-4, 4), (_bf((hidden,), g).clamp(-2, 2).float() * size).to(torch.bfloat16)
+    x[:, ::5] = 0
+    _, _, c, s = ocq.add_rmsnorm(x, w, 0.0)
+    h = x.double()
+    y = h / torch.sqrt(h.square().mean(-1, keepdim=True)) * w.double()
+    # y itself is rounded to a multiple of 2^-149 below 2^-126
+    err = 2.0 ** -149
+    assert torch.all((s.double() - y.abs().amax(-1) / 448).abs() <= s.double() * 2.0 ** -20 + 2 * err)
+    got = c.view(E4M3).double() * s.double()[:, None]
+    tol = y.abs() * (2.0 ** -4 + 2.0 ** -18) + s.double()[:, None] * (2.0 ** -10 + 2.0 ** -18) + 450 * err
+    assert torch.all((got - y).abs() <= tol)
