@@ -389,9 +389,11 @@ typedef struct {
  * request.  Tokens past max_new of a request are not attended; max_kv only
  * shapes the split of the work.
  * counters_dev: uint32 [OCQ_ATTENTION_COUNTERS] for ocq_paged_attention (not
- * read by the others): zeroed once by the caller, zero again after every call;
- * attention calls that share it must be ordered on one stream.  tokens * heads and max_pages * page_size
- * stay below 2^31. */
+ * read by the others): zeroed by the caller before the first call in that
+ * call's order, zero again after every call; attention calls that share it must
+ * be ordered on one stream.  If the device arrays change while a call runs its
+ * counts may stay wrong: zero them again.
+ * tokens * heads and max_pages * page_size stay below 2^31. */
 typedef struct {
   const void* q_start_dev;
   const void* kv_lens_dev;

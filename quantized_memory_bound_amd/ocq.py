@@ -559,8 +559,12 @@ class TokenBatch:
 
     q_start int32 [requests + 1], kv_lens int32 [requests], page_table int32 [requests, max_pages] (its rows max_pages
     entries or more apart): CUDA tensors whose contents may change between calls.  tokens (the rows of q), max_new and
-    max_kv are host numbers: bounds of the new tokens and of kv_lens of any request.  Attention calls over one batch use
-    its counters: they are ordered on one stream.
+    max_kv are host numbers: bounds of the new tokens and of kv_lens of any request.
+
+    Attention calls over one batch count their finished work in memory of the batch, 0 between calls, apart for every
+    stream that they run on.  A captured call counts where calls on the stream that the batch was made on do: its replays
+    are ordered with those, and the batch outlives the graph.  The device arrays must not change while a call runs (its
+    counts could stay wrong for the next one).
     """
 
     def __init__(self, q_start, kv_lens, page_table, max_new, max_kv, tokens=None):
@@ -582,7 +586,9 @@ class TokenBatch:
                            "that requests share has to be copied: .contiguous())" % (stride, page_table.shape[1]))
         self.q_start, self.kv_lens, self.page_table, self.device = q_start, kv_lens, page_table, dev
         self.requests, self.tokens = requests, None
-        self.counters = torch.zeros(ATTENTION_COUNTERS, dtype=torch.int32, device=dev)   # 0 between calls
+        self.counters = torch.zeros(ATTENTION_COUNTERS, dtype=torch.int32, device=dev)   # of the stream it is made on
+        self.stream = _raw_stream(self.index)             # the stream whose counters the struct holds
+        self.counters_of = {self.stream: self.counters}
         self.struct = TokenBatchStruct(q_start.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
                                        stride, requests, 0, page_table.shape[1], max_new, max_kv,
                                        self.counters.data_ptr())
@@ -597,6 +603,20 @@ class TokenBatch:
         elif tokens != self.tokens:
             raise OcqError(ERR_INVALID_ARG, "the batch has %d tokens, the tensor %d" % (self.tokens, tokens))
         return self.ref
+
+
+    def move_to(self, stream):
+        """Count the attention calls that follow in memory of this stream (a raw handle): zeroed in its order and not
+        reused before what it has queued is done, also if the batch is dropped meanwhile."""
+        cuda, counters = _torch.cuda, self.counters_of.get(stream)
+        if counters is None:
+            with cuda.stream(cuda.ExternalStream(stream, self.index)):
+                if cuda.is_current_stream_capturing():    # a fill would be a part of every replay
+                    self.struct.counters_dev, self.stream = self.counters.data_ptr(), None
+                    return
+                counters = _torch.zeros(ATTENTION_COUNTERS, dtype=_torch.int32, device=self.device)
+            self.counters_of[stream] = counters
+        self.struct.counters_dev, self.stream = counters.data_ptr(), stream
 
 
 def rope_frequencies(rot, base=10000.0, scaling="none", factor=1.0, context=4096, beta_fast=32.0, beta_slow=1.0):
@@ -699,7 +719,9 @@ def paged_attention(q, cache, batch, scale=None, window=0, sinks=0, want_lse=Fal
         _need(lse, "lse", _torch.float32, q.device, (tokens, heads))
     elif want_lse:
         lse = _empty((tokens, heads), _torch.float32, i, stream)
-    ref, L = batch.of(tokens), lib()
+    ref, L, handle = batch.of(tokens), lib(), _stream_of(stream, i)
+    if handle != batch.stream:
+        batch.move_to(handle)
     if workspace is None:
         need = L.ocq_attention_workspace_bytes(heads, cache.ref, ref, window, sinks)
         if need:
@@ -710,7 +732,7 @@ def paged_attention(q, cache, batch, scale=None, window=0, sinks=0, want_lse=Fal
     _check(L.ocq_paged_attention(q.data_ptr(), q.stride(0), q.stride(1), heads, cache.ref, ref,
                                  dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
                                  None if lse is None else lse.data_ptr(),
-                                 None if workspace is None else workspace.data_ptr(), need, _stream_of(stream, i)))
+                                 None if workspace is None else workspace.data_ptr(), need, handle))
     return out, lse
 
 

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from quantized_memory_bound_amd import ocq
-from test_gpu_layer import DEV, E4M3, _bf, _check_codes, _gen, make_batch, make_cache
+from test_gpu_layer import DEV, E4M3, _bf, _check_codes, _gen, check_attention, make_batch, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,59 @@ def test_norm_to_tiny_values(size, hidden):
     got = c.view(E4M3).double() * s.double()[:, None]
     tol = y.abs() * (2.0 ** -4 + 2.0 ** -18) + s.double()[:, None] * (2.0 ** -10 + 2.0 ** -18) + 450 * err
     assert torch.all((got - y).abs() <= tol)
+
+
+# ---------------------------------------------------------------- streams
+
+def test_attention_on_a_stream_that_the_batch_was_not_made_on():
+    """The batch is made on a stream that is still busy, in memory that holds other numbers, and dropped while its call
+    is waiting: neither reaches the call's counts."""
+    g = _gen(31)
+    news, kvs = [13, 13], [3000, 2000]
+    first, pages = make_batch(news, kvs, 32, g)
+    cache, q = make_cache(pages, 2, 32, 128, False, g), _bf((26, 8, 128), g)
+    want, lse = check_attention(q, cache, first, news, kvs)
+    home, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(home):
+            spoiled = [torch.full((ocq.ATTENTION_COUNTERS,), 7, dtype=torch.int32, device=DEV) for _ in range(4)]
+            torch.cuda.synchronize()
+            torch.cuda._sleep(20_000_000)                        # about 10 ms
+            del spoiled
+            batch = ocq.TokenBatch(first.q_start, first.kv_lens, first.page_table, 13, 3000)
+        out = ocq.paged_attention(q, cache, batch, want_lse=True, stream=side)
+        side.synchronize()
+        assert torch.equal(out[0], want) and torch.equal(out[1], lse)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        out = ocq.paged_attention(q, cache, batch, want_lse=True, stream=side)
+        del batch
+        with torch.cuda.stream(home):
+            again = [torch.full((ocq.ATTENTION_COUNTERS,), 7, dtype=torch.int32, device=DEV) for _ in range(8)]
+        side.synchronize()
+        assert torch.equal(out[0], want) and torch.equal(out[1], lse)
+        assert all(bool((t == 7).all()) for t in again)
+        torch.cuda.synchronize()
+
+
+def test_one_batch_on_several_streams_and_in_a_graph():
+    g = _gen(32)
+    news, kvs = [5, 5], [2000, 900]
+    batch, pages = make_batch(news, kvs, 64, g)
+    cache, q = make_cache(pages, 2, 64, 128, True, g), _bf((10, 8, 128), g)
+    want, lse = check_attention(q, cache, batch, news, kvs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = ocq.paged_attention(q, cache, batch, want_lse=True)
+    sides = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(4):
+        outs = [ocq.paged_attention(q, cache, batch, want_lse=True, stream=s) for s in sides]   # at the same time
+        captured[0].zero_()
+        graph.replay()
+        outs += [ocq.paged_attention(q, cache, batch, want_lse=True), captured]
+        torch.cuda.synchronize()
+        for a, b in outs:
+            assert torch.equal(a, want) and torch.equal(b, lse)
+    assert not any(bool(c.any()) for c in batch.counters_of.values())

@@ -10,7 +10,9 @@ from quantized_memory_bound_amd import ocq
 @pytest.fixture
 def cpu_handles(monkeypatch):
     """Handles accept CPU tensors, as if those were on the current device."""
-    monkeypatch.setattr(ocq, "_gpu", lambda t, name: 0)
+    monkeypatch.setattr(ocq, "_gpu", lambda t, name: t.get_device())     # -1
+    monkeypatch.setattr(ocq, "_torch", torch)
+    monkeypatch.setattr(ocq, "_raw_stream", lambda i: 11)
 
 
 def _ints(*shape):
@@ -46,3 +48,70 @@ def test_page_table_stride_is_the_tensors_own(cpu_handles, table, stride):
     assert b.struct.table_stride == stride and b.struct.max_pages == table.shape[1]
     last = table.storage_offset() + (len(table) - 1) * stride + table.shape[1] - 1
     assert last < table.untyped_storage().nbytes() // 4
+
+
+# ---------------------------------------------------------------- counters of attention calls
+
+class _Streams:
+    """Stand-ins for torch.cuda's streams and for the library: which counters a call gets, and in whose order tensors
+    were zeroed."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.capturing, self.zeroed_on, self.calls = [11], set(), {}, []
+        zeros = torch.zeros
+
+        def spied(*a, **kw):
+            t = zeros(*a, **kw)
+            self.zeroed_on[t.data_ptr()] = self.now[-1]
+            return t
+
+        class _On:
+            def __init__(this, handle):
+                this.handle = handle
+
+            def __enter__(this):
+                self.now.append(this.handle)
+
+            def __exit__(this, *a):
+                self.now.pop()
+        monkeypatch.setattr(torch, "zeros", spied)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
+        monkeypatch.setattr(torch.cuda, "stream", _On)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.now[-1] in self.capturing)
+        monkeypatch.setattr(ocq, "_raw_stream", lambda i: self.now[-1])
+        monkeypatch.setattr(ocq, "_empty", lambda shape, dtype, index, stream: torch.empty(shape, dtype=dtype))
+        monkeypatch.setattr(ocq, "lib", lambda: self)
+
+    def ocq_attention_workspace_bytes(self, *a):
+        return 0
+
+    def ocq_paged_attention(self, *a):
+        batch = ocq.ctypes.cast(a[5], ocq.ctypes.POINTER(ocq.TokenBatchStruct)).contents
+        self.calls.append((batch.counters_dev, a[-1]))
+        return 0
+
+
+def test_attention_calls_count_in_memory_of_their_own_stream(cpu_handles, monkeypatch):
+    streams = _Streams(monkeypatch)
+    cache = ocq.PagedKVCache(*(torch.zeros(4, 1, 16, 64, dtype=torch.bfloat16) for _ in range(2)))
+    batch, q = _batch(_ints(2, 2)), torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    home = batch.counters.data_ptr()
+    for stream in (None, 22, 22, None, 33, 22):
+        ocq.paged_attention(q, cache, batch, stream=stream)
+    assert [h for _, h in streams.calls] == [11, 22, 22, 11, 33, 22]
+    for counters, handle in streams.calls:
+        assert streams.zeroed_on[counters] == handle
+    assert len({c for c, _ in streams.calls}) == 3
+    assert {t.data_ptr() for t in batch.counters_of.values()} == {c for c, _ in streams.calls}   # kept with the batch
+    # captured calls add no fill to the graph; afterwards the same stream has counters of its own
+    streams.calls.clear()
+    streams.capturing = {44}
+    for _ in range(2):
+        ocq.paged_attention(q, cache, batch, stream=44)
+    assert [c for c, _ in streams.calls] == [home, home]
+    streams.capturing = set()
+    ocq.paged_attention(q, cache, batch, stream=44)
+    assert streams.calls[-1][0] not in (home, None) and streams.zeroed_on[streams.calls[-1][0]] == 44
+    streams.now[0] = 55                                    # the current stream is another one
+    ocq.paged_attention(q, cache, batch)
+    assert streams.zeroed_on[streams.calls[-1][0]] == 55
