@@ -447,7 +447,9 @@ ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_
  * q_dev [tokens, heads, head_dim] with token and head strides; out_dev bf16
  * [tokens, heads, head_dim] contiguous; lse_dev float [tokens, heads] or NULL.
  * scale > 0 and finite, window >= 0 (0: none), sinks >= 0 (0 without a
- * window).  Scores, softmax statistics and sums are fp32; probabilities are
+ * window).  Requests x kv heads x row tiles (of 16 to 128 of the max_new *
+ * heads / kv_heads rows) are one launch of fewer than 2^32 lanes, 64 to 256 a
+ * tile; beyond that: OCQ_ERR_UNSUPPORTED.  Scores, softmax statistics and sums are fp32; probabilities are
  * rounded to bf16 for the second product.
  * Rows that no token of the request sees (past kv_len, behind a window) never
  * reach a result, whatever the pages hold there.  A page outside [0,

@@ -983,6 +983,7 @@ AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads,
     typedef decltype(geo) G;
     AttnPlan p{0, 1, 0, 0, 0};
     const int64_t pairs = (int64_t)requests * kv_heads, tiles = (rows + G::ROWS - 1) / G::ROWS;
+    p.lanes = (double)pairs * (double)tiles * G::THREADS;
     const int64_t key_tiles = (keys + G::TT - 1) / G::TT;
     if (key_tiles <= kMinTiles) return p;
     if (G::EVEN && requests <= kEvenRequests && pairs < 4 * G::RESIDENT && pairs <= OCQ_ATTENTION_COUNTERS &&
@@ -991,12 +992,16 @@ AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads,
       p.slots = G::RESIDENT;
       p.groups = (int)(2 * pairs > p.slots ? p.slots + pairs : p.slots);   // no fewer than there can be pieces
       p.part_rows = (size_t)p.groups * G::ROWS;
+      p.lanes = (double)p.groups * G::THREADS;
       return p;
     }
     const int64_t groups = pairs * tiles, want = (kTargetGroups + groups - 1) / groups, most = key_tiles / kMinTiles;
     const int64_t s = want < most ? want : most;
     p.splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
     p.part_rows = p.splits > 1 ? (size_t)p.splits * tokens * heads : 0;
+    p.lanes *= p.splits;
+    if (p.splits > 1 && (double)tokens * heads * (G::D / 4) + 256 > p.lanes)   // the join's
+      p.lanes = (double)tokens * heads * (G::D / 4) + 256;
     return p;
   });
 }

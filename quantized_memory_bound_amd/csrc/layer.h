@@ -52,6 +52,7 @@ struct RopeArgs {
   uint16_t* q_out;           // [tokens][heads][dim]
   float multiplier;
   int heads, dim, rot, interleaved, e4m3;
+  int first;                 // token of the launch's first workgroup
   BatchArgs b;
   CacheArgs c;
 };
@@ -77,7 +78,12 @@ struct AttnArgs {
 struct AttnPlan {
   int even, splits, groups, slots;
   size_t part_rows;          // rows of partial outputs in the workspace
+  double lanes = 0;          // of the larger launch (a launch holds fewer than 2^32)
 };
+
+// Rows or tokens of one launch of the norm and the append (a launch holds fewer
+// than 2^32 lanes, a row takes up to 1024); more take several.
+constexpr int kRowsAtOnce = 1 << 20;
 
 // each enqueues on `stream` and returns 0 or a hipError_t value
 int launch_norm(const NormArgs& a, void* stream);

@@ -97,12 +97,6 @@ AttnPlan plan_of(int heads, const ocq_kv_cache* c, const ocq_token_batch* b, int
                    sinks, (int64_t)b->max_pages * c->page_size);
 }
 
-// the grid of the attention launch, an upper bound over its row tiles
-bool attn_grid_ok(const ocq_token_batch* b, const ocq_kv_cache* c, int heads, int splits) {
-  const double rows = (double)max_new(b) * (heads / c->kv_heads);
-  return (double)b->requests * c->kv_heads * splits * (std::floor(rows / 16) + 1) < 2147483648.0;
-}
-
 }  // namespace
 
 extern "C" {
@@ -187,7 +181,7 @@ ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_
   const RopeArgs a{(const uint16_t*)q_dev, (const uint16_t*)k_dev, (const uint16_t*)v_dev, q_token_stride,
                    q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
                    (const double*)inv_freq_dev, (const int32_t*)positions_dev, (uint16_t*)q_out_dev, multiplier, heads,
-                   cache->head_dim, rot, interleaved, cache->format == OCQ_CACHE_E4M3, batch_args(batch),
+                   cache->head_dim, rot, interleaved, cache->format == OCQ_CACHE_E4M3, 0, batch_args(batch),
                    cache_args(cache)};
   const int rc = launch_rope(a, stream);
   return rc ? hip_error(rc) : OCQ_OK;
@@ -220,7 +214,7 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
   if (!stride_ok(q_token_stride, 8) || !stride_ok(q_head_stride, 8))
     return invalid("strides must be multiples of 8, not negative");
   const AttnPlan plan = plan_of(heads, cache, batch, window, sinks);
-  if (!attn_grid_ok(batch, cache, heads, plan.splits)) return unsupported("too many row tiles for one launch");
+  if (plan.lanes >= 4294967296.0) return unsupported("too many row tiles for one launch");
   const size_t need = plan.part_rows * (cache->head_dim + 1) * sizeof(float);
   if (workspace_bytes < need)
     return set_error(OCQ_ERR_BUFFER_TOO_SMALL, "workspace_bytes < ocq_attention_workspace_bytes()");

@@ -124,10 +124,7 @@ int run(const NormArgs& a, hipStream_t st) {
   return (int)hipGetLastError();
 }
 
-}  // namespace
-
-int launch_norm(const NormArgs& a, void* stream) {
-  hipStream_t st = (hipStream_t)stream;
+int launch_rows(const NormArgs& a, hipStream_t st) {
   const int waves = (a.hidden / 8 + 63) / 64;   // 64-lane units of a row
   if (waves <= 1) return run<1, 1>(a, st);
   if (waves <= 4) return run<4, 1>(a, st);
@@ -136,6 +133,25 @@ int launch_norm(const NormArgs& a, void* stream) {
   if (waves <= 32) return run<16, 2>(a, st);
   if (waves <= 64) return run<16, 4>(a, st);
   return run<16, 8>(a, st);
+}
+
+}  // namespace
+
+int launch_norm(const NormArgs& a, void* stream) {
+  NormArgs part = a;
+  for (int done = 0; done < a.rows; done += kRowsAtOnce) {
+    part.rows = a.rows - done < kRowsAtOnce ? a.rows - done : kRowsAtOnce;
+    const int rc = launch_rows(part, (hipStream_t)stream);
+    if (rc) return rc;
+    const int64_t out = (int64_t)kRowsAtOnce * a.hidden;
+    part.x += kRowsAtOnce * a.x_stride;
+    if (a.res) part.res += kRowsAtOnce * a.res_stride;
+    if (a.res_out) part.res_out += out;
+    if (a.y) part.y += out;
+    if (a.codes) part.codes += out;
+    if (a.scales) part.scales += kRowsAtOnce;
+  }
+  return 0;
 }
 
 }  // namespace ocq

@@ -48,7 +48,7 @@ template <int DIM, bool E4M3>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
   constexpr int LPH = DIM / 16;   // lanes per head
   __shared__ float s_cos[DIM / 2], s_sin[DIM / 2];
-  const int t = blockIdx.x;
+  const int t = a.first + blockIdx.x;
   const int r = request_of(a.b, t);
   if (r < 0) return;
   const int64_t place = (int64_t)a.b.kv_lens[r] - a.b.q_start[r + 1] + t;
@@ -149,7 +149,8 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
 
 template <int DIM>
 void run(const RopeArgs& a, hipStream_t st) {
-  const dim3 grid(a.b.tokens), block(kRopeThreads);
+  const int left = a.b.tokens - a.first;
+  const dim3 grid(left < kRowsAtOnce ? left : kRowsAtOnce), block(kRopeThreads);
   if (a.e4m3) hipLaunchKernelGGL((k_rope<DIM, true>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((k_rope<DIM, false>), grid, block, 0, st, a);
 }
@@ -158,10 +159,16 @@ void run(const RopeArgs& a, hipStream_t st) {
 
 int launch_rope(const RopeArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  if (a.dim == 64) run<64>(a, st);
-  else if (a.dim == 128) run<128>(a, st);
-  else run<256>(a, st);
-  return (int)hipGetLastError();
+  RopeArgs part = a;
+  for (int64_t first = 0; first < a.b.tokens; first += kRowsAtOnce) {
+    part.first = (int)first;
+    if (a.dim == 64) run<64>(part, st);
+    else if (a.dim == 128) run<128>(part, st);
+    else run<256>(part, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+  }
+  return 0;
 }
 
 }  // namespace ocq

@@ -176,3 +176,37 @@ def test_one_batch_on_several_streams_and_in_a_graph():
         for a, b in outs:
             assert torch.equal(a, want) and torch.equal(b, lse)
     assert not any(bool(c.any()) for c in batch.counters_of.values())
+
+
+# ---------------------------------------------------------------- sizes of launches
+
+def test_norm_of_its_most_rows():
+    """2^24 rows of 256 lanes are 2^32 of them.  Rows overlap in memory (8 elements apart): all differ."""
+    rows, hidden = 1 << 24, 520
+    x = _bf((8 * (rows - 1) + hidden,), _gen(41)).as_strided((rows, hidden), (8, 1))
+    w = _bf((hidden,), _gen(42))
+    scales = torch.full((rows,), -1.0, device=DEV)
+    codes = ocq.add_rmsnorm(x, w, 1e-6, scales=scales)[2]
+    assert bool((scales > 0).all())
+    some = torch.tensor([0, 1, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, 5 << 21, rows - 2, rows - 1], device=DEV)
+    h = x[some].double()
+    y = h / torch.sqrt(h.square().mean(-1, keepdim=True) + 1e-6) * w.double()
+    _check_codes(codes[some], scales[some], y, "codes")
+
+
+def test_append_of_more_tokens_than_one_axis_of_the_grid_holds():
+    tokens, page = (1 << 24) + 5, 1024
+    g = _gen(43)
+    q, k, v = (_bf((8 * (tokens - 1) + 64,), g).as_strided((tokens, 1, 64), (8, 64, 1)) for _ in range(3))
+    pages = -(-tokens // page)
+    cache = ocq.PagedKVCache.allocate(pages, page, 1, 64, device=DEV)
+    table = torch.randperm(pages, device=DEV, generator=g).to(torch.int32)[None]
+    batch = ocq.TokenBatch(torch.tensor([0, tokens], dtype=torch.int32, device=DEV),
+                           torch.tensor([tokens], dtype=torch.int32, device=DEV), table, tokens, tokens)
+    zero = torch.zeros(tokens, dtype=torch.int32, device=DEV)          # position 0: nothing is turned
+    out = ocq.rope_append(q, k, v, ocq.Rope.make(64, device=DEV), cache, batch, positions=zero)
+    at = torch.arange(tokens, device=DEV)
+    for part in at.split(1 << 20):
+        ids, rows = table[0][part // page].long(), part % page
+        assert torch.equal(out[part], q[part])
+        assert torch.equal(cache.k[ids, 0, rows], k[part, 0]) and torch.equal(cache.v[ids, 0, rows], v[part, 0])

@@ -1,6 +1,8 @@
 """The binding's handles of the operators around the block, what runs without a GPU: the numbers that they hand to the C
 ABI, taken from CPU tensors (nothing is launched)."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -86,7 +88,7 @@ class _Streams:
         return 0
 
     def ocq_paged_attention(self, *a):
-        batch = ocq.ctypes.cast(a[5], ocq.ctypes.POINTER(ocq.TokenBatchStruct)).contents
+        batch = ctypes.cast(a[5], ctypes.POINTER(ocq.TokenBatchStruct)).contents
         self.calls.append((batch.counters_dev, a[-1]))
         return 0
 
@@ -115,3 +117,20 @@ def test_attention_calls_count_in_memory_of_their_own_stream(cpu_handles, monkey
     streams.now[0] = 55                                    # the current stream is another one
     ocq.paged_attention(q, cache, batch)
     assert streams.zeroed_on[streams.calls[-1][0]] == 55
+
+
+# ---------------------------------------------------------------- sizes of launches
+
+@pytest.mark.parametrize("requests,tokens,max_new,heads,kv_heads", [
+    (65536, 65536 + 8192, 8192, 8, 8),           # 2^25 workgroups of 256 lanes
+    (4096, 4095 + 32768, 32768, 32, 8),          # one long chunk among many requests
+    (65536, 1 << 17, 1, 4096, 4096)])            # one token each, many heads
+def test_attention_refuses_more_lanes_than_a_launch_holds(requests, tokens, max_new, heads, kv_heads):
+    p = 4096                                     # an aligned address that no refused call reads
+    cache = ocq.KVCacheStruct(k_dev=p, v_dev=p, page_stride=kv_heads * 16 * 64, head_stride=16 * 64, token_stride=64,
+                              num_pages=4, page_size=16, kv_heads=kv_heads, head_dim=64, format=0)
+    batch = ocq.TokenBatchStruct(q_start_dev=p, kv_lens_dev=p, page_table_dev=p, table_stride=4, requests=requests,
+                                 tokens=tokens, max_pages=4, max_new=max_new, max_kv=60, counters_dev=p)
+    status = ocq.lib().ocq_paged_attention(p, heads * 64, 64, heads, ctypes.byref(cache), ctypes.byref(batch), 0.125, 0,
+                                           0, p, None, p, 1 << 50, None)
+    assert status == ocq.ERR_UNSUPPORTED and "launch" in ocq.last_error()
