@@ -150,10 +150,9 @@ def test_attention_on_a_stream_that_the_batch_was_not_made_on():
         del batch
         with torch.cuda.stream(home):
             again = [torch.full((ocq.ATTENTION_COUNTERS,), 7, dtype=torch.int32, device=DEV) for _ in range(8)]
-        side.synchronize()
+        torch.cuda.synchronize()                                 # home's fills too, read on another stream below
         assert torch.equal(out[0], want) and torch.equal(out[1], lse)
         assert all(bool((t == 7).all()) for t in again)
-        torch.cuda.synchronize()
 
 
 def test_one_batch_on_several_streams_and_in_a_graph():
