@@ -32,16 +32,25 @@ __device__ __forceinline__ float max_mag(float m, float v) { return __builtin_el
 // of its values is not finite, so that whoever reads the row sees it.
 __device__ __forceinline__ float e4m3_scale(float m) { return m < __builtin_inff() ? m / 448.0f : __builtin_nanf(""); }
 
-// What e4m3x8_quot takes for a row of scale s: s and its reciprocal (0 for a zero
-// row), of the values times `up`.  up is 1 but for scales below 2^-126: from 2^-128
-// down the reciprocal would overflow, so values and scale grow by 2^64 first,
-// which is exact and leaves the quotients as they are.
+// What e4m3x8_quot takes for the N values of a lane whose row has scale s > 0: s and
+// its reciprocal.  Where that would overflow (s below 2^-128) values and scale
+// grow by 2^64 first, which is exact and leaves the quotients as they are.
 struct Quot {
-  float s, rcp, up;
+  float s, rcp;
 };
-__device__ __forceinline__ Quot e4m3_quot_of(float s) {
-  const float up = s > 0.0f && s < 0x1p-126f ? 0x1p64f : 1.0f;
-  return Quot{s * up, s > 0.0f ? 1.0f / (s * up) : 0.0f, up};
+template <int N>
+__device__ __forceinline__ Quot e4m3_quot_of(float s, float (&v)[N][8]) {
+  Quot q{s, 1.0f / s};
+  if (q.rcp == __builtin_inff() && s > 0.0f) {
+    asm volatile("");   // a branch that is hardly ever taken
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= 0x1p64f;
+    q.s = s * 0x1p64f;
+    q.rcp = 1.0f / q.s;
+  }
+  return q;
 }
 
 }  // namespace ocq

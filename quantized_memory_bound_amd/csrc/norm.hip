@@ -92,15 +92,8 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_norm(NormArgs a) {
   // a row whose squares do not sum to a finite number has no norm: its scale
   // says so, as it does for a y that is not finite
   const float s = ss < __builtin_inff() ? e4m3_scale(amax) : __builtin_nanf("");
-  const Quot qt = e4m3_quot_of(s);
+  const Quot qt = e4m3_quot_of(s, h);
   if (!live) return;
-  if (qt.up > 1.0f) {
-    asm volatile("");   // a branch that is hardly ever taken
-#pragma unroll
-    for (int p = 0; p < PER; ++p)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[p][j] *= qt.up;
-  }
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     const int u = (p * WPR + wr) * 64 + lane;

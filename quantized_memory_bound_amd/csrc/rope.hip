@@ -122,20 +122,15 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
 #pragma unroll
       for (int o = 1; o < LPH; o <<= 1) amax = max_mag(amax, __shfl_xor(amax, o));
       const float s = e4m3_scale(amax);
-      const Quot qt = e4m3_quot_of(s);
-      if (qt.up > 1.0f) {
-        asm volatile("");   // a branch that is hardly ever taken
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] *= qt.up;
-      }
-      float lo[8], hi[8];
+      float y[2][8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        lo[j] = x[j];
-        hi[j] = x[8 + j];
+        y[0][j] = x[j];
+        y[1][j] = x[8 + j];
       }
-      const v2u c0 = s > 0.0f ? e4m3x8_quot(lo, qt.s, qt.rcp) : v2u{0u, 0u};
-      const v2u c1 = s > 0.0f ? e4m3x8_quot(hi, qt.s, qt.rcp) : v2u{0u, 0u};
+      const Quot qt = e4m3_quot_of(s, y);
+      const v2u c0 = s > 0.0f ? e4m3x8_quot(y[0], qt.s, qt.rcp) : v2u{0u, 0u};
+      const v2u c1 = s > 0.0f ? e4m3x8_quot(y[1], qt.s, qt.rcp) : v2u{0u, 0u};
       if (slot) {
         *(v2u*)(pool + d0) = c0;
         *(v2u*)(pool + d1) = c1;
