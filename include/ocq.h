@@ -363,8 +363,8 @@ typedef enum {
  * for k and v: any order of the first three axes.  Strides in elements; in
  * bytes they are multiples of 16, a page's below 2^32 and a head's rows of one
  * page within 2^31.  k_scale_dev, v_scale_dev: float
- * [num_pages, kv_heads, page_size] with strides of their own (E4M3 only; the
- * same bounds, in elements).
+ * [num_pages, kv_heads, page_size] with strides of their own (E4M3 only; a
+ * page's below 2^32 elements, a head's scales of one page within 2^30).
  * page_size: a power of two up to 1024; head_dim 64, 128 or 256. */
 typedef struct {
   void* k_dev;

@@ -209,3 +209,25 @@ def test_append_of_more_tokens_than_one_axis_of_the_grid_holds():
         ids, rows = table[0][part // page].long(), part % page
         assert torch.equal(out[part], q[part])
         assert torch.equal(cache.k[ids, 0, rows], k[part, 0]) and torch.equal(cache.v[ids, 0, rows], v[part, 0])
+
+
+# ---------------------------------------------------------------- scales that lie far apart
+
+def test_scales_of_one_page_as_far_apart_as_may_be():
+    """31 times 2^25 elements are just within 2^30, their offsets in bytes within 2^32 and past 2^31."""
+    g, page, step = _gen(51), 32, 1 << 25
+    news, kvs = [13, 1, 40], [200, 90, 70]
+    batch, pages = make_batch(news, kvs, page, g)
+    room = torch.empty((page - 1) * step + 8 * pages, device=DEV)
+    ks, vs = (room.as_strided((pages, 2, page), (8, 4, step), at) for at in (0, 2))
+    plain = make_cache(pages, 2, page, 128, True, g)
+    ks.copy_(plain.k_scale)
+    vs.copy_(plain.v_scale)
+    cache = ocq.PagedKVCache(plain.k, plain.v, ks, vs)
+    q, k, v = _bf((54, 8, 128), g), _bf((54, 2, 128), g), _bf((54, 2, 128), g)
+    q = ocq.rope_append(q, k, v, ocq.Rope.make(128, device=DEV), cache, batch)
+    check_attention(q, cache, batch, news, kvs)                       # rows of many: 128-row tiles
+    for r, (n, kv) in enumerate(zip(news[:2], kvs[:2])):              # up to 64 rows, up to 16
+        one, _ = make_batch([n], [kv], page, g)
+        one.page_table[0] = batch.page_table[r, : one.page_table.shape[1]]
+        check_attention(q[13 * r: 13 * r + n], cache, one, [n], [kv])

@@ -134,3 +134,24 @@ def test_attention_refuses_more_lanes_than_a_launch_holds(requests, tokens, max_
     status = ocq.lib().ocq_paged_attention(p, heads * 64, 64, heads, ctypes.byref(cache), ctypes.byref(batch), 0.125, 0,
                                            0, p, None, p, 1 << 50, None)
     assert status == ocq.ERR_UNSUPPORTED and "launch" in ocq.last_error()
+
+
+def _e4m3(scale_token_stride, page_size):
+    p = 4096                                     # an aligned address that no refused call reads
+    return ocq.KVCacheStruct(k_dev=p, v_dev=p, k_scale_dev=p, v_scale_dev=p, page_stride=2 * page_size * 64,
+                             head_stride=page_size * 64, token_stride=64, scale_page_stride=8, scale_head_stride=4,
+                             scale_token_stride=scale_token_stride, num_pages=4, page_size=page_size, kv_heads=2,
+                             head_dim=64, format=1)
+
+
+@pytest.mark.parametrize("step,page_size,status", [(1 << 26, 32, ocq.ERR_UNSUPPORTED), (1 << 25, 64, ocq.ERR_UNSUPPORTED),
+                                                   (1 << 30, 2, ocq.ERR_UNSUPPORTED), (1 << 25, 32, ocq.OK),
+                                                   ((1 << 30) - 1, 2, ocq.OK), (1 << 40, 1, ocq.OK)])
+def test_scales_whose_offsets_pass_32_bits_of_bytes_are_refused(step, page_size, status):
+    """Attention would read another row's scale.  (No tokens: an accepted cache has nothing to do.)"""
+    batch = ocq.TokenBatchStruct(requests=0, tokens=0)
+    cache = _e4m3(step, page_size)
+    assert ocq.lib().ocq_paged_attention(None, 64, 64, 4, ctypes.byref(cache), ctypes.byref(batch), 0.125, 0, 0, None,
+                                         None, None, 0, None) == status
+    assert ocq.lib().ocq_rope_append(None, 64, 64, None, 64, 64, None, 64, 64, 4, None, 64, 0, 1.0, None,
+                                     ctypes.byref(cache), ctypes.byref(batch), None, None) == status
