@@ -405,6 +405,8 @@ ATTENTION_COUNTERS = 4096
 ROPE_SCALINGS = ("none", "linear", "ntk", "yarn")
 
 
+_INT_MAX = (1 << 31) - 1
+
 _torch = None
 _raw_stream = None
 _current_device = None
@@ -443,6 +445,14 @@ def _bf16_rows(t, name, index, shape):
         raise OcqError(ERR_INVALID_ARG, "the last axis of %s must be contiguous" % name)
 
 
+def _int32(value, name):
+    """value as an int, which the C ABI takes in 32 bits (ctypes would cut it off silently)."""
+    value = int(value)
+    if not -1 << 31 <= value < 1 << 31:
+        raise OcqError(ERR_INVALID_ARG, "%s is %d, beyond 32 bits" % (name, value))
+    return value
+
+
 def _empty(shape, dtype, index, stream):
     """A new tensor for a call on `stream`: allocated on it, so that its memory is not reused before the call."""
     if stream is None:
@@ -476,6 +486,8 @@ def add_rmsnorm(x, weight, eps=1e-6, residual=None, want_y=False, want_codes=Tru
     if x.dim() != 2:
         raise OcqError(ERR_INVALID_ARG, "x must be [rows, hidden], got %s" % (tuple(x.shape),))
     shape = rows, hidden = x.shape
+    if rows > _INT_MAX or hidden > _INT_MAX:
+        raise OcqError(ERR_INVALID_ARG, "x is [%d, %d], beyond 32 bits" % shape)
     _bf16_rows(x, "x", i, shape)
     _bf16_rows(weight, "weight", i, (hidden,))
     bf16, res, res_stride = _torch.bfloat16, None, 0
@@ -535,6 +547,8 @@ class PagedKVCache:
                     raise OcqError(ERR_INVALID_ARG, "%s must be float32 %s, k_scale and v_scale of one layout" %
                                    (name, tuple(k.shape[:3])))
         self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, dev
+        for n, name in zip(k.shape, ("pages", "kv_heads", "page_size", "head_dim")):
+            _int32(n, name)
         pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         s = k_scale.stride() if e4m3 else (0, 0, 0)
         self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
@@ -590,7 +604,8 @@ class TokenBatch:
         self.stream = _raw_stream(self.index)             # the stream whose counters the struct holds
         self.counters_of = {self.stream: self.counters}
         self.struct = TokenBatchStruct(q_start.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(),
-                                       stride, requests, 0, page_table.shape[1], max_new, max_kv,
+                                       stride, requests, 0, _int32(page_table.shape[1], "max_pages"),
+                                       _int32(max_new, "max_new"), _int32(max_kv, "max_kv"),
                                        self.counters.data_ptr())
         self.ref = ctypes.byref(self.struct)
         if tokens is not None:
@@ -599,7 +614,7 @@ class TokenBatch:
     def of(self, tokens):
         """The batch as an argument for a call over `tokens` rows."""
         if self.tokens is None:
-            self.tokens = self.struct.tokens = int(tokens)
+            self.tokens = self.struct.tokens = _int32(tokens, "tokens")
         elif tokens != self.tokens:
             raise OcqError(ERR_INVALID_ARG, "the batch has %d tokens, the tensor %d" % (self.tokens, tokens))
         return self.ref
@@ -690,7 +705,8 @@ def rope_append(q, k, v, rope, cache, batch, positions=None, q_out=None, stream=
 
 def attention_workspace_bytes(heads, cache, batch, window=0, sinks=0):
     """Workspace of paged_attention for a batch whose tokens are known."""
-    return lib().ocq_attention_workspace_bytes(heads, cache.ref, batch.ref, window, sinks)
+    return lib().ocq_attention_workspace_bytes(_int32(heads, "heads"), cache.ref, batch.ref, _int32(window, "window"),
+                                               _int32(sinks, "sinks"))
 
 
 def paged_attention(q, cache, batch, scale=None, window=0, sinks=0, want_lse=False, out=None, lse=None,
@@ -710,6 +726,8 @@ def paged_attention(q, cache, batch, scale=None, window=0, sinks=0, want_lse=Fal
     if dim != cache.head_dim:
         raise OcqError(ERR_INVALID_ARG, "q has head size %d, the cache %d" % (dim, cache.head_dim))
     _bf16_rows(q, "q", i, shape)
+    if not (0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX):
+        raise OcqError(ERR_INVALID_ARG, "window %d and sinks %d must be in [0, 2^31)" % (window, sinks))
     _on(i, cache, batch)
     if out is None:
         out = _empty_as(q, shape, _torch.bfloat16, i, stream)

@@ -155,3 +155,37 @@ def test_scales_whose_offsets_pass_32_bits_of_bytes_are_refused(step, page_size,
                                          None, None, 0, None) == status
     assert ocq.lib().ocq_rope_append(None, 64, 64, None, 64, 64, None, 64, 64, 4, None, 64, 0, 1.0, None,
                                      ctypes.byref(cache), ctypes.byref(batch), None, None) == status
+
+
+# ---------------------------------------------------------------- numbers beyond 32 bits
+
+BEYOND = [1 << 31, (1 << 32) + 5, -(1 << 32) + 5]
+
+
+@pytest.mark.parametrize("value", BEYOND)
+def test_numbers_beyond_32_bits_are_refused(cpu_handles, monkeypatch, value):
+    """ctypes would pass their low 32 bits: a window of 2^32 + 5 would be one of 5."""
+    cache = ocq.PagedKVCache(*(torch.zeros(4, 1, 16, 64, dtype=torch.bfloat16) for _ in range(2)))
+    batch, q = _batch(_ints(2, 2)), torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    batch.of(2)
+    _Streams(monkeypatch)
+    ints = torch.arange(3, dtype=torch.int32), torch.ones(2, dtype=torch.int32), _ints(2, 2)
+    for call in (lambda: ocq.paged_attention(q, cache, batch, window=value),
+                 lambda: ocq.paged_attention(q, cache, batch, window=8, sinks=value),
+                 lambda: ocq.attention_workspace_bytes(1, cache, batch, value),
+                 lambda: ocq.TokenBatch(*ints, value, 64), lambda: ocq.TokenBatch(*ints, 1, value),
+                 lambda: ocq.TokenBatch(*ints, 1, 64, tokens=value)):
+        with pytest.raises(ocq.OcqError) as e:
+            call()
+        assert e.value.status == ocq.ERR_INVALID_ARG
+
+
+def test_tensors_of_more_rows_than_32_bits_are_refused(cpu_handles):
+    row = torch.zeros(1, 8, dtype=torch.bfloat16)
+    with pytest.raises(ocq.OcqError) as e:
+        ocq.add_rmsnorm(row.expand((1 << 32) + 3, 8), row[0])
+    assert e.value.status == ocq.ERR_INVALID_ARG
+    page = torch.zeros(1, 1, 16, 64, dtype=torch.bfloat16).expand((1 << 32) + 3, 1, 16, 64)
+    with pytest.raises(ocq.OcqError) as e:
+        ocq.PagedKVCache(page, page)
+    assert e.value.status == ocq.ERR_INVALID_ARG
