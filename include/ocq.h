@@ -339,7 +339,11 @@ int ocq_last_requant_in_gateup(void);
  *   y = h / sqrt(mean(h^2) + eps) * weight (fp32, of the unrounded h)
  *   scales = fl32(max|y| / 448), codes = E4M3(fl32(y / scale)); a zero row has
  *   scale 0 and codes 0, a row whose squares do not sum to a finite fp32
- *   number, or with a y that is not finite, has scale NaN and codes 0.
+ *   number, or with a y that is not finite, has scale NaN and codes 0.  (The
+ *   bf16 y of a row whose squares overflow is what the formula gives in fp32:
+ *   0 where h is finite.)
+ * The codes are for 8-bit products of the caller's; the block of this library
+ * takes bf16 and quantizes it itself.
  * x_bf16_dev, residual_bf16_dev: [rows, hidden] with row strides x_stride and
  * residual_stride; weight_bf16_dev [hidden]; residual_out_bf16_dev and
  * y_bf16_dev: [rows, hidden] contiguous, each nullable; codes_dev (uint8
@@ -386,7 +390,8 @@ typedef struct {
  * q_start_dev int32 [requests + 1], kv_lens_dev int32 [requests],
  * page_table_dev int32 [requests, max_pages] with row stride table_stride.
  * max_new, max_kv: host bounds of the new tokens and of kv_lens of any
- * request.  Tokens past max_new of a request are not attended; max_kv only
+ * request.  Tokens past max_new of a request are not attended, nor are tokens
+ * of no request: what out and lse hold for them is not defined.  max_kv only
  * shapes the split of the work.
  * counters_dev: uint32 [OCQ_ATTENTION_COUNTERS] for ocq_paged_attention (not
  * read by the others): zeroed by the caller before the first call in that

@@ -31,12 +31,14 @@
 //   4 requests, one token over 131072 keys, bf16: 268-280 us, 6.3-6.6 TB/s of
 //     the 7.1 that a streaming read reaches: HBM;
 //   16 x 13 tokens over up to 4096 keys, bf16: 49-52 us, 29 of them reading at
-//     the streaming rate: before the first keys are there (5.7 us), writing and
-//     joining the parts (about 9 us) and pieces that end at different times;
-//   64 x 13 over up to 8192, E4M3: 175-188 us (HBM alone 119, products 69):
-//     conversions and softmax on the vector unit, matrix cores 32 % busy;
-//   2048 new tokens over 10007 keys, bf16: 920-945 TFLOP/s (8192 over 12288:
-//     1005; a library product of 8192^3: 1202): vector unit and matrix cores
+//     the streaming rate: the piece, its ids and the first keys (5 us), loops of
+//     11 to 15 stages that end between 22 and 41, writing the parts (3) and
+//     joining them (5);
+//   64 x 13 over up to 8192, E4M3: 176-198 us, more the longer the card has been
+//     busy (HBM alone 119, products 69): conversions and softmax on the vector
+//     unit, matrix cores 32 % busy;
+//   2048 new tokens over 10007 keys, bf16: 898-953 TFLOP/s (8192 over 12288:
+//     951-1005; a library product of 8192^3: 1202): vector unit and matrix cores
 //     together, 45 % of the matrix cores' cycles.
 #include "gemm_core.h"
 #include "layer_dev.h"
@@ -613,6 +615,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
           l += e[i];
           if constexpr (G::KV8) e[i] *= vs[i];
         }
+        // bf16 is what the matrix instruction takes beside bf16 (or converted)
+        // values: an output is off by 0.0023 of its size where its own rounding
+        // is 0.0017.  Two halves of each probability would double the products.
         p[(kt * AN + 4 * i4) / 2] = pack_bf16(e[0], e[1]);
         p[(kt * AN + 4 * i4) / 2 + 1] = pack_bf16(e[2], e[3]);
       }

@@ -9,9 +9,11 @@
 // unit), so x and the residual are read once; two reductions (sum of squares,
 // then max|y|) meet in LDS.  WPR is the smallest that keeps a lane at one or two
 // units (16 waves from 8192 values on), so that a row's loads are in flight at
-// once.  Bound by HBM: 8191 x 4096 rows, both outputs, 52 us (302 MB at 5.8 TB/s;
-// a device copy runs at 4.7); 208 x 4096 rows 5.2 us and one row 2.8 us by
-// latency (load, two reductions, store), against 1.6 us for an empty launch.
+// once.  Bound by HBM: 8191 x 4096 rows, both outputs (302 MB), 52 us by the
+// kernel trace over three inputs in turn, 57 us a pass where neither inputs nor
+// outputs are in the memory-side cache (5.3 TB/s; a device copy runs at 4.7); 208 x
+// 4096 rows 5.4 us and one row 2.8 us by latency (load, two reductions, store),
+// against 1.6 us for an empty launch.
 #include "layer_dev.h"
 
 namespace ocq {
@@ -111,7 +113,8 @@ int run(const NormArgs& a, hipStream_t st) {
   constexpr int threads = WPR < 4 ? 256 : 64 * WPR;
   const dim3 grid((a.rows + RPB - 1) / RPB);
   // Inputs far larger than the L2s pass through them without staying (8191 x 4096
-  // rows: 57 -> 52 us); smaller ones are best kept (2048 x 4096: 15.6 and 15.1).
+  // rows: 55.9 -> 51.8 us by the kernel trace, 61.0 -> 56.5 a pass over cold
+  // memory); smaller ones are best kept (2048 x 4096: 15.6 and 15.1).
   if ((int64_t)a.rows * a.hidden > (1 << 24)) hipLaunchKernelGGL((k_norm<WPR, PER, true>), grid, dim3(threads), 0, st, a);
   else hipLaunchKernelGGL((k_norm<WPR, PER, false>), grid, dim3(threads), 0, st, a);
   return (int)hipGetLastError();

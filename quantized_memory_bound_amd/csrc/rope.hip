@@ -16,8 +16,8 @@
 // One workgroup per token: the token's rot/2 sines and cosines are made once,
 // in LDS, for all heads.  A lane owns 16 elements of a head, both halves of
 // its 8 pairs, so q_out may be q itself.  Bound by HBM: 4672 tokens of 48 heads of
-// 128 elements 24.7 us (115 MB at 4.6 TB/s, a device copy's rate); 208 tokens into
-// an E4M3 cache 5.5 us and one token 2.7 us by latency.
+// 128 elements 25.0 us (115 MB at 4.6 TB/s, a device copy's rate); 208 tokens into
+// an E4M3 cache 5.6 us and one token 2.7 us by latency.
 #include "layer_dev.h"
 #include "layer_index.h"
 
