@@ -338,8 +338,9 @@ int ocq_last_requant_in_gateup(void);
  *   residual_out = bf16(h)
  *   y = h / sqrt(mean(h^2) + eps) * weight (fp32, of the unrounded h)
  *   scales = fl32(max|y| / 448), codes = E4M3(fl32(y / scale)); a zero row has
- *   scale 0 and codes 0, a row whose squares do not sum to a finite fp32
- *   number, or with a y that is not finite, has scale NaN and codes 0.  (The
+ *   scale 0 and codes 0 (with eps 0 too, where y is 0 / 0), any other row whose
+ *   squares do not sum to a finite fp32 number, or with a y that is not finite,
+ *   has scale NaN and codes 0.  (The
  *   bf16 y of a row whose squares overflow is what the formula gives in fp32:
  *   0 where h is finite.)
  * The codes are for 8-bit products of the caller's; the block of this library

@@ -84,6 +84,15 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_norm(NormArgs a) {
           pack8_bf16(h[p]);
   }
   if (!a.codes) return;
+  if (a.eps == 0.0f && ss == 0.0f) {
+    // 0 / 0 in every place of a zero row, whose codes are 0 all the same; what is
+    // not zero here is infinite
+    amax = 0.0f;
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(h[p][j]));
+  }
   amax = wave_max(amax < __builtin_inff() ? amax : __builtin_inff());   // NaN as infinity, which fmaxf keeps
   if constexpr (WPR > 1) {
     if (lane == 0) s_max[slot][wr] = amax;

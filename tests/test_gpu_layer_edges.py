@@ -231,3 +231,26 @@ def test_scales_of_one_page_as_far_apart_as_may_be():
         one, _ = make_batch([n], [kv], page, g)
         one.page_table[0] = batch.page_table[r, : one.page_table.shape[1]]
         check_attention(q[13 * r: 13 * r + n], cache, one, [n], [kv])
+
+
+# ---------------------------------------------------------------- no eps
+
+@pytest.mark.parametrize("hidden", [72, 512, 2048, 4096, 8192, 16384, 32768, 65536])
+def test_norm_without_eps_of_zero_rows_and_of_rows_whose_squares_vanish(hidden):
+    """A zero row has scale 0 and codes 0 whatever its y (0 / 0) is; a row that is not zero but whose squares are 0 in
+    fp32 has no norm: scale NaN, codes 0; the others are as ever."""
+    g = _gen(hidden + 1)
+    x, w = _bf((9, hidden), g), _bf((hidden,), g)
+    w[w == 0] = 1
+    x[[1, 6]] = 0
+    x[3] = 0
+    x[3, hidden // 2] = 1e-30
+    x[4] = 1e-30
+    _, _, c, s = ocq.add_rmsnorm(x, w, 0.0)
+    assert (s[[1, 6]] == 0).all() and not c[[1, 6]].view(torch.uint8).any()
+    assert torch.isnan(s[[3, 4]]).all() and not c[[3, 4]].view(torch.uint8).any()
+    rest = [0, 2, 5, 7, 8]
+    h = x[rest].double()
+    _check_codes(c[rest], s[rest], h / torch.sqrt(h.square().mean(-1, keepdim=True)) * w.double(), "codes")
+    s = ocq.add_rmsnorm(x, w, 1e-6)[3]
+    assert (s[[1, 6]] == 0).all() and (s[[3, 4]] > 0).all()
