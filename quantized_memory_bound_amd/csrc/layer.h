@@ -81,9 +81,9 @@ struct AttnPlan {
   double lanes = 0;          // of the larger launch (a launch holds fewer than 2^32)
 };
 
-// Rows or tokens of one launch of the norm and the append (a launch holds fewer
-// than 2^32 lanes, a row takes up to 1024); more take several.
-constexpr int kRowsAtOnce = 1 << 20;
+// Lanes of one launch of the norm and the append (it holds fewer than 2^32); rows
+// or tokens that take more are several launches.
+constexpr unsigned kLanesAtOnce = 1u << 31;
 
 // each enqueues on `stream` and returns 0 or a hipError_t value
 int launch_norm(const NormArgs& a, void* stream);

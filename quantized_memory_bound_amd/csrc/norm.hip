@@ -117,19 +117,37 @@ __global__ __launch_bounds__(WPR < 4 ? 256 : 64 * WPR) void k_norm(NormArgs a) {
 }
 
 template <int WPR, int PER>
-int run(const NormArgs& a, hipStream_t st) {
+int run(const NormArgs& all, hipStream_t st) {
   constexpr int RPB = WPR < 4 ? 4 / WPR : 1;
   constexpr int threads = WPR < 4 ? 256 : 64 * WPR;
-  const dim3 grid((a.rows + RPB - 1) / RPB);
+  constexpr int at_once = kLanesAtOnce / (64 * WPR);   // a multiple of RPB
   // Inputs far larger than the L2s pass through them without staying (8191 x 4096
   // rows: 55.9 -> 51.8 us by the kernel trace, 61.0 -> 56.5 a pass over cold
   // memory); smaller ones are best kept (2048 x 4096: 15.6 and 15.1).
-  if ((int64_t)a.rows * a.hidden > (1 << 24)) hipLaunchKernelGGL((k_norm<WPR, PER, true>), grid, dim3(threads), 0, st, a);
-  else hipLaunchKernelGGL((k_norm<WPR, PER, false>), grid, dim3(threads), 0, st, a);
-  return (int)hipGetLastError();
+  const bool pass = (int64_t)all.rows * all.hidden > (1 << 24);
+  NormArgs a = all;
+  for (int64_t done = 0; done < all.rows; done += at_once) {
+    a.rows = all.rows - done < at_once ? (int)(all.rows - done) : at_once;
+    const dim3 grid((a.rows + RPB - 1) / RPB);
+    if (pass) hipLaunchKernelGGL((k_norm<WPR, PER, true>), grid, dim3(threads), 0, st, a);
+    else hipLaunchKernelGGL((k_norm<WPR, PER, false>), grid, dim3(threads), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+    const int64_t out = (int64_t)at_once * a.hidden;
+    a.x += at_once * a.x_stride;
+    if (a.res) a.res += at_once * a.res_stride;
+    if (a.res_out) a.res_out += out;
+    if (a.y) a.y += out;
+    if (a.codes) a.codes += out;
+    if (a.scales) a.scales += at_once;
+  }
+  return 0;
 }
 
-int launch_rows(const NormArgs& a, hipStream_t st) {
+}  // namespace
+
+int launch_norm(const NormArgs& a, void* stream) {
+  hipStream_t st = (hipStream_t)stream;
   const int waves = (a.hidden / 8 + 63) / 64;   // 64-lane units of a row
   if (waves <= 1) return run<1, 1>(a, st);
   if (waves <= 4) return run<4, 1>(a, st);
@@ -138,25 +156,6 @@ int launch_rows(const NormArgs& a, hipStream_t st) {
   if (waves <= 32) return run<16, 2>(a, st);
   if (waves <= 64) return run<16, 4>(a, st);
   return run<16, 8>(a, st);
-}
-
-}  // namespace
-
-int launch_norm(const NormArgs& a, void* stream) {
-  NormArgs part = a;
-  for (int done = 0; done < a.rows; done += kRowsAtOnce) {
-    part.rows = a.rows - done < kRowsAtOnce ? a.rows - done : kRowsAtOnce;
-    const int rc = launch_rows(part, (hipStream_t)stream);
-    if (rc) return rc;
-    const int64_t out = (int64_t)kRowsAtOnce * a.hidden;
-    part.x += kRowsAtOnce * a.x_stride;
-    if (a.res) part.res += kRowsAtOnce * a.res_stride;
-    if (a.res_out) part.res_out += out;
-    if (a.y) part.y += out;
-    if (a.codes) part.codes += out;
-    if (a.scales) part.scales += kRowsAtOnce;
-  }
-  return 0;
 }
 
 }  // namespace ocq

@@ -42,7 +42,7 @@ __device__ __forceinline__ int request_of(const BatchArgs& b, int t) {
   return r;
 }
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kAtOnce = kLanesAtOnce / kRopeThreads;   // tokens of a launch
 
 template <int DIM, bool E4M3>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
 template <int DIM>
 void run(const RopeArgs& a, hipStream_t st) {
   const int left = a.b.tokens - a.first;
-  const dim3 grid(left < kRowsAtOnce ? left : kRowsAtOnce), block(kRopeThreads);
+  const dim3 grid(left < kAtOnce ? left : kAtOnce), block(kRopeThreads);
   if (a.e4m3) hipLaunchKernelGGL((k_rope<DIM, true>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((k_rope<DIM, false>), grid, block, 0, st, a);
 }
@@ -155,7 +155,7 @@ void run(const RopeArgs& a, hipStream_t st) {
 int launch_rope(const RopeArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   RopeArgs part = a;
-  for (int64_t first = 0; first < a.b.tokens; first += kRowsAtOnce) {
+  for (int64_t first = 0; first < a.b.tokens; first += kAtOnce) {
     part.first = (int)first;
     if (a.dim == 64) run<64>(part, st);
     else if (a.dim == 128) run<128>(part, st);

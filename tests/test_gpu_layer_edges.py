@@ -187,13 +187,13 @@ def test_norm_of_its_most_rows():
     scales = torch.full((rows,), -1.0, device=DEV)
     codes = ocq.add_rmsnorm(x, w, 1e-6, scales=scales)[2]
     assert bool((scales > 0).all())
-    some = torch.tensor([0, 1, (1 << 20) - 1, 1 << 20, (1 << 20) + 1, 5 << 21, rows - 2, rows - 1], device=DEV)
+    some = torch.tensor([0, 1, 1 << 20, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, rows - 2, rows - 1], device=DEV)
     h = x[some].double()
     y = h / torch.sqrt(h.square().mean(-1, keepdim=True) + 1e-6) * w.double()
     _check_codes(codes[some], scales[some], y, "codes")
 
 
-def test_append_of_more_tokens_than_one_axis_of_the_grid_holds():
+def test_append_of_more_tokens_than_one_launch_holds():
     tokens, page = (1 << 24) + 5, 1024
     g = _gen(43)
     q, k, v = (_bf((8 * (tokens - 1) + 64,), g).as_strided((tokens, 1, 64), (8, 64, 1)) for _ in range(3))
