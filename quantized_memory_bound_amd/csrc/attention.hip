@@ -34,11 +34,11 @@
 //     the streaming rate: the piece, its ids and the first keys (5 us), loops of
 //     11 to 15 stages that end between 22 and 41, writing the parts (3) and
 //     joining them (5);
-//   64 x 13 over up to 8192, E4M3: 176-198 us, more the longer the card has been
+//   64 x 13 over up to 8192, E4M3: 175-198 us, more the longer the card has been
 //     busy (HBM alone 119, products 69): conversions and softmax on the vector
 //     unit, matrix cores 32 % busy;
 //   2048 new tokens over 10007 keys, bf16: 898-953 TFLOP/s (8192 over 12288:
-//     951-1005; a library product of 8192^3: 1202): vector unit and matrix cores
+//     951-1020; a library product of 8192^3: 1202): vector unit and matrix cores
 //     together, 45 % of the matrix cores' cycles.
 #include "gemm_core.h"
 #include "layer_dev.h"
