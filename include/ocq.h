@@ -360,7 +360,8 @@ ocq_status ocq_add_rmsnorm(const void* x_bf16_dev, int64_t x_stride, const void*
 
 typedef enum {
   OCQ_CACHE_BF16 = 0,   /* k, v bf16                                                   */
-  OCQ_CACHE_E4M3 = 1    /* k, v E4M3 codes, one fp32 scale (max / 448) per token and head */
+  OCQ_CACHE_E4M3 = 1,   /* k, v E4M3 codes, one fp32 scale (max / 448) per token and head */
+  OCQ_CACHE_NVFP4 = 2   /* k, v E2M1 codes, one E4M3 scale (max / 6) per 16 elements       */
 } ocq_cache_format;
 
 /* A paged cache of one layer.  k_dev, v_dev: [num_pages, kv_heads, page_size,
@@ -370,6 +371,13 @@ typedef enum {
  * page within 2^31.  k_scale_dev, v_scale_dev: float
  * [num_pages, kv_heads, page_size] with strides of their own (E4M3 only; a
  * page's below 2^32 elements, a head's scales of one page within 2^30).
+ * NVFP4: k_dev, v_dev uint8 [num_pages, kv_heads, page_size, head_dim / 2], element
+ * 2 i of a row in the low half of byte i, and k_scale_dev, v_scale_dev E4M3 bytes
+ * [num_pages, kv_heads, page_size, head_dim / 16]; all strides in bytes, those of
+ * the codes multiples of 16, those of the scales of 4 (their last axis contiguous).
+ * An element is code x scale x unit: k_unit and v_unit, read for NVFP4 only, are
+ * powers of two in [2^-64, 2^64] that move the scales' range (2^-9 to 448) to where
+ * the values are (1 suits values from 0.1 to 2688).
  * page_size: a power of two up to 1024; head_dim 64, 128 or 256. */
 typedef struct {
   void* k_dev;
@@ -380,6 +388,7 @@ typedef struct {
   int64_t scale_page_stride, scale_head_stride, scale_token_stride;
   int num_pages, page_size, kv_heads, head_dim;
   int format;
+  float k_unit, v_unit;
 } ocq_kv_cache;
 
 /* The tokens of one step.  The new tokens of request r are rows q_start[r] ..
@@ -435,7 +444,12 @@ ocq_status ocq_rope_frequencies(int rot, double base, int scaling, double factor
  * itself where that is contiguous.
  * bf16 caches receive bf16(k'), bf16(v); E4M3 caches the codes of the fp32 k'
  * and of v and their scales (a token's head with a value that is not finite:
- * scale NaN, codes 0).  A token whose place is outside [0, max_pages *
+ * scale NaN, codes 0).  NVFP4 caches receive, for each 16 elements of a head, the
+ * scale s = E4M3(fl32(max / 6) / unit) and the codes E2M1(fl32(y / (s unit))) of y =
+ * fl32(k'), which is turned in 64 bits (a code next to a border would hang on the
+ * last bits of an angle in 32), or of v; nearest, ties to even, saturating; a scale
+ * of 0 has codes 0, 16 elements with one that is not finite have scale NaN, codes
+ * 0.  A token whose place is outside [0, max_pages *
  * page_size) or whose page is outside [0, num_pages) is not appended (its q is
  * rotated all the same).  Two new tokens must not share a cache slot. */
 ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, const void* k_dev,
@@ -453,7 +467,8 @@ ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_
  * q_dev [tokens, heads, head_dim] with token and head strides; out_dev bf16
  * [tokens, heads, head_dim] contiguous; lse_dev float [tokens, heads] or NULL.
  * scale > 0 and finite, window >= 0 (0: none), sinks >= 0 (0 without a
- * window).  Requests x kv heads x row tiles (of 16 to 128 of the max_new *
+ * window).  Over NVFP4 caches both products are of fp16 operands: q after a power of
+ * two of each row, the probabilities rounded to fp16.  Requests x kv heads x row tiles (of 16 to 128 of the max_new *
  * heads / kv_heads rows) are one launch of fewer than 2^32 lanes, 64 to 256 a
  * tile; beyond that: OCQ_ERR_UNSUPPORTED.  Scores, softmax statistics and sums are fp32; probabilities are
  * rounded to bf16 for the second product.
@@ -470,6 +485,11 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
                                const ocq_kv_cache* cache, const ocq_token_batch* batch, float scale, int window,
                                int sinks, void* out_dev, void* lse_dev, void* workspace_dev, size_t workspace_bytes,
                                void* stream);
+
+/* The values that an E4M3 or NVFP4 cache stands for, to move it to another format
+ * or to look at it: k_out_dev, v_out_dev bf16 [num_pages, kv_heads, page_size,
+ * head_dim] contiguous (NVFP4 values are exact in bf16, E4M3 ones are rounded). */
+ocq_status ocq_cache_values(const ocq_kv_cache* cache, void* k_out_dev, void* v_out_dev, void* stream);
 
 /* Message for the last failure on this thread ("" if none). */
 const char* ocq_last_error(void);

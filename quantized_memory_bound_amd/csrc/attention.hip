@@ -51,6 +51,7 @@ namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 typedef short v4s __attribute__((ext_vector_type(4)));
+typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __attribute__((address_space(3))) v2i lds_v2i;
 
@@ -58,6 +59,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLow = -3.4028234663852886e38f;   // below every score that is visible
 constexpr float kSlack = 8.0f;                    // see above
+// NVFP4: probabilities are fp16, up to 2^(8 + 7) of its 65504, so that only those
+// below 2^-31 of the largest round as if they were 0
+constexpr float kUp = 7.0f;
 
 constexpr int kTargetGroups = 512, kMinTiles = 4, kMaxSplits = 256;   // see attn_plan
 constexpr int kEvenRequests = 256;                // requests of a batch that is cut into pieces
@@ -74,6 +78,7 @@ __device__ __forceinline__ v8bf e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+constexpr int LG_(int MT) { return 64 / MT; }
 template <int MT> struct Acc;
 template <> struct Acc<16> { typedef v4f T; };
 template <> struct Acc<32> { typedef v16f T; };
@@ -84,25 +89,35 @@ __device__ __forceinline__ v4f mfma(v8bf a, v8bf b, v4f c) {
 __device__ __forceinline__ v16f mfma(v8bf a, v8bf b, v16f c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
+__device__ __forceinline__ v4f mfma(v8h a, v8h b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f mfma(v8h a, v8h b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
 
 // D: head size; KV8: E4M3 cache; MT: rows of a wave; WR x
 // WK waves: over the rows and over the keys; TK: keys of a wave's stage; MINW:
 // waves per SIMD that the registers leave room for.  NST: slots of each ring;
 // two, so that the loop over the stages, unrolled by two, has every LDS address
 // as a register that does not change plus a constant.
-template <int D_, bool KV8_, int MT_, int WR_, int WK_, int TK_, int MINW_>
+template <int D_, int FMT_, int MT_, int WR_, int WK_, int TK_, int MINW_>
 struct Geo {
   static constexpr int MINW = MINW_, NST = 2;
   static constexpr int D = D_, MT = MT_, WR = WR_, WK = WK_, TK = TK_;
-  static constexpr bool KV8 = KV8_;
+  static constexpr bool KV8 = FMT_ == OCQ_CACHE_E4M3, KV4 = FMT_ == OCQ_CACHE_NVFP4;
   static constexpr int NW = WR * WK, THREADS = 64 * NW, ROWS = MT * WR;
-  static constexpr int ESZ = KV8 ? 1 : 2, RB = D * ESZ, CH = RB / 16;   // bytes and chunks of a row
+  static constexpr int RB = KV4 ? D / 2 : KV8 ? D : 2 * D, CH = RB / 16;   // bytes and chunks of a row
   static constexpr int PART = TK * RB;                                  // K (or V) bytes of a key group's stage
-  static constexpr int SCB = KV8 ? 256 : 0;                             // its scales
+  static constexpr int SB = KV4 ? D / 16 : 4;                           // bytes of a key's scales
+  static constexpr int SCB = KV4 ? (TK * SB > 256 ? TK * SB : 256) : KV8 ? 256 : 0;   // the stage's
   static constexpr int KSTG = PART + SCB + 256, VSTG = PART + SCB;      // a stage of K (with 64 page ids) and of V
+  static constexpr int VTAB = KV4 ? TK * SB * 2 : 0;                    // a wave's fp16 scales of V, key by key
   static constexpr int RING = WK * NST * (KSTG + VSTG);
-  static constexpr int QI = PART / 1024 / WR;                           // K (or V) loads per wave and stage
-  static constexpr int PW = 2 * QI + 1 + (KV8 ? 2 : 0);                 // all loads per wave and stage
+  static constexpr int QI = (PART / 1024 + WR - 1) / WR;                // K (or V) loads per wave and stage
+  static constexpr int SI = KV4 ? SCB / 256 : KV8 ? 1 : 0;              // loads of its scales
+  static constexpr int PW = 2 * QI + 1 + 2 * SI;                        // all loads per wave and stage
+  static constexpr int KW = KV4 ? (RB / LG_(MT) >= 16 ? 4 : 2) : KV8 ? 2 : 1;   // steps of S that a read of K serves
   static constexpr int AHEAD = WR > 1 ? NST - 1 : NST;                  // stages on their way, see the ring
   static constexpr int TT = TK * WK;                                    // keys of a tile, all key groups
   static constexpr int NKT = TK / MT;                                   // key tiles of a stage
@@ -111,12 +126,13 @@ struct Geo {
   static constexpr int PS = TK / KS;                                    // steps of O
   static constexpr int SO = D + 4;                                      // floats of a joined row: 16 bytes further per row
   static constexpr int JOIN = WK > 1 ? WK * ROWS * (SO * 4 + 8) + 4 : 0;
-  static constexpr int LDS = RING > JOIN ? RING : JOIN;
+  static constexpr int LDS = RING + NW * VTAB > JOIN ? RING + NW * VTAB : JOIN;
   static constexpr bool EVEN = WK > 1;                                  // may be cut into pieces (layer_index.h)
   static constexpr int PER_CU = 160 * 1024 / (LDS + 1024) < 4 * MINW / NW ? 160 * 1024 / (LDS + 1024) : 4 * MINW / NW;
   static constexpr int RESIDENT = 256 * (PER_CU > 0 ? PER_CU : 1);      // workgroups at once, 256 CUs
-  static_assert(PART % (1024 * WR) == 0 && TK % 32 == 0 && LDS <= 160 * 1024, "");
+  static_assert(PART % 1024 == 0 && (PART % (1024 * WR) == 0 || KV4) && TK % 32 == 0 && LDS <= 160 * 1024, "");
   static_assert(TK <= 64, "one load for the ids, and for the scales");
+  static_assert(!KV4 || TK == 64 || (MT == 32 && TK == 32), "a transposing read of codes takes 64 or 32 keys");
 };
 
 // Chunk swizzle: chunk c of row `row` lies at chunk c ^ swz(row).  What one
@@ -125,13 +141,20 @@ struct Geo {
 //       16 rows, or 16 RB / 256 where a pass holds several rows;
 //   V   half a wave's transposing reads: for bf16 4 rows x 4 chunks (MT 32) or
 //       8 rows x 2 chunks (MT 16) from row 0 or 4 g, for codes 4 + 4 rows KB
-//       apart x 2 chunks, or 8 + 8 rows x 1 chunk.
+//       apart x 2 chunks, or 8 + 8 rows x 1 chunk; for NVFP4 16 rows x 1 chunk
+//       (MT 32), or 32 rows x half a chunk, which takes two passes at least.
 // So the row bits of V's pass go to the chunk bits above those it reads
 // together.  Linear in the bits (swz(a + b) = swz(a) ^ swz(b) without carries).
 template <class G>
 __device__ __forceinline__ constexpr int swz(int row) {
   const int b0 = row & 1, b1 = row >> 1 & 1, b2 = row >> 2 & 1, b3 = row >> 3 & 1, b4 = row >> 4 & 1;
-  if constexpr (!G::KV8) {
+  if constexpr (G::KV4) {
+    const int b5 = row >> 5 & 1;
+    if constexpr (G::MT == 32)
+      return G::CH == 8 ? b1 | b3 << 1 | (b2 ^ b4) << 2 : G::CH == 4 ? (b2 ^ b4) | b3 << 1 : b3;
+    else
+      return G::CH == 8 ? b1 | (b2 ^ b4) << 1 | (b3 ^ b5) << 2 : G::CH == 4 ? (b2 ^ b4) | (b3 ^ b5) << 1 : b3 ^ b4;
+  } else if constexpr (!G::KV8) {
     if constexpr (G::MT == 32)
       return G::CH >= 16 ? b0 << 2 | b1 << 3 | b2 | b3 << 1 : b1 << 2 | b2 | b3 << 1;
     else
@@ -187,6 +210,30 @@ __device__ __forceinline__ void read_tr8(v2i (&x)[4], const uint32_t (&ad)[4]) {
       : "v"(ad[0]), "v"(ad[1]), "v"(ad[2]), "v"(ad[3]), "n"(O0), "n"(O1), "n"(O2), "n"(O3));
 }
 
+// The same of 4-bit codes: 16 keys of one d per lane each.
+template <int O0, int O1, int O2, int O3>
+__device__ __forceinline__ void read_tr4(v2i (&x)[4], const uint32_t (&ad)[4]) {
+  asm volatile(
+      "ds_read_b64_tr_b4 %0, %4 offset:%8\n\tds_read_b64_tr_b4 %1, %5 offset:%9\n\t"
+      "ds_read_b64_tr_b4 %2, %6 offset:%10\n\tds_read_b64_tr_b4 %3, %7 offset:%11\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+      : "v"(ad[0]), "v"(ad[1]), "v"(ad[2]), "v"(ad[3]), "n"(O0), "n"(O1), "n"(O2), "n"(O3));
+}
+
+// eight E2M1 codes (low nibble first) times their own scales in pairs -> fp16, exact
+__device__ __forceinline__ v8h e2m1x8_pairs(uint32_t d, const v2h* s) {
+  const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 0) * s[0];
+  const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 1) * s[1];
+  const v2h c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 2) * s[2];
+  const v2h e = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(d, 1.0f, 3) * s[3];
+  return v8h{a[0], a[1], b[0], b[1], c[0], c[1], e[0], e[1]};
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {   // nearest even
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{a, b}), v2h));
+}
+
 template <int N, class F>
 __device__ __forceinline__ void unrolled(F f) {   // f(0) .. f(N - 1) with compile-time arguments
   if constexpr (N > 0) {
@@ -198,8 +245,7 @@ __device__ __forceinline__ void unrolled(F f) {   // f(0) .. f(N - 1) with compi
 // d of element j = 0 of a lane's operand in step s of S
 template <class G>
 __device__ __forceinline__ int q_dim(int s, int g) {
-  if constexpr (G::KV8) return 2 * G::KS * (s >> 1) + 16 * g + 8 * (s & 1);   // one 16-byte read serves two steps
-  else return G::KS * s + 8 * g;
+  return G::KW * (G::KS * (s / G::KW) + 8 * g) + 8 * (s % G::KW);   // one read of K serves KW steps
 }
 
 // Inclusive sums over the lanes: within rows of 16 (DPP row_shr 1, 2, 4, 8),
@@ -251,7 +297,7 @@ __device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int piece
     // mean shares and more are cut (pieces of half a share: 64 x 13 rows over
     // 8192 keys in E4M3 221 us instead of 203)
     per = (float)(total / 2 * 3 / a.slots + 1);
-    if (a.e4m3 && a.b.requests <= 64) {
+    if (a.format != OCQ_CACHE_BF16 && a.b.requests <= 64) {
       // The longest first, so that a CU's second workgroup is a short one: E4M3
       // keys are bound by the CUs' vector units (64 x 13 rows over 8192: 189 ->
       // 181 us), bf16 keys by HBM (40 x 13 rows over 4096: 99 -> 102).
@@ -415,14 +461,37 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   const int tok = live ? row / a.group : 0, head = kvh * a.group + (live ? row % a.group : 0);
   const int place = live ? base + tok : -1;
   const size_t at = (size_t)(t0 + tok) * a.heads + head;
-  v8bf q[G::QS];
+  typedef std::conditional_t<G::KV4, v8h, v8bf> operand;
+  operand q[G::QS];
   const uint16_t* qp = a.q + (t0 + tok) * a.q_token + head * a.q_head;
+  float c = a.scale * kLog2e;
+  if constexpr (G::KV4) {
+    // Codes times their scales are exact in fp16, not all in bf16 with one
+    // instruction less; q goes to fp16 after a power of two that brings the row's
+    // largest value to 2^14 .. 2^15, which is exact down to 2^-28 of it (and off by
+    // at most 2^-40 of it below).
+    float f[G::QS][8], top = 0.0f;
 #pragma unroll
-  for (int s = 0; s < G::QS; ++s) {
-    const v4i u = live ? *(const v4i*)(qp + q_dim<G>(s, g)) : v4i{0, 0, 0, 0};
-    q[s] = __builtin_bit_cast(v8bf, u);
+    for (int s = 0; s < G::QS; ++s) {
+      unpack8_bf16(live ? *(const v4i*)(qp + q_dim<G>(s, g)) : v4i{0, 0, 0, 0}, f[s]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[s][j]));
+    }
+#pragma unroll
+    for (int x = G::MT; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+    const int up = top > 0.0f && top < __builtin_inff() ? 15 - __builtin_amdgcn_frexp_expf(top) : 0;
+#pragma unroll
+    for (int s = 0; s < G::QS; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[s][j] = (_Float16)__builtin_ldexpf(f[s][j], up);
+    c = __builtin_ldexpf(c * a.c.k_unit, -up);
+  } else {
+#pragma unroll
+    for (int s = 0; s < G::QS; ++s) {
+      const v4i u = live ? *(const v4i*)(qp + q_dim<G>(s, g)) : v4i{0, 0, 0, 0};
+      q[s] = __builtin_bit_cast(v8bf, u);
+    }
   }
-  const float c = a.scale * kLog2e;
 
   // ---- loads: rows of this wave's part of its key group's stage.  V of a stage
   // goes after K of it, with the same offsets.
@@ -432,70 +501,82 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   const int32_t* const table = a.b.table + pc.req * a.b.table_stride;
   const int page_mask = (1 << a.c.page_shift) - 1;
   const uint64_t k_head = (uint64_t)a.c.k + kvh * a.c.head, v_less_k = (uint64_t)a.c.v - (uint64_t)a.c.k;
-  const uint64_t ks_head = (uint64_t)(a.c.k_scale + (G::KV8 ? kvh * a.c.s_head : 0));
+  constexpr int SE = G::KV4 ? 1 : 4;                     // bytes that strides of the scales count
+  const uint64_t ks_head = (uint64_t)a.c.k_scale + (G::SI ? kvh * a.c.s_head * SE : 0);
   const uint64_t vs_less_ks = (uint64_t)a.c.v_scale - (uint64_t)a.c.k_scale;
   // first key of the wave's key group in stage st: a multiple of TK, so that a
   // row's place in its page is that of the first key plus a part of its own
   auto tile_key = [&](int st) { return tile_of(pc.tiles, pc.s0 + st) * G::TT + wk * G::TK; };
-  auto q_row = [&](int i) {   // row of load i of K and V, or (i = QI) of the scales
-    return i < G::QI ? ((i * G::WR + wr) * 64 + lane) / G::CH : lane % G::TK;
+  // load i of the stage's PART / 1024 (where waves outnumber them, some come twice)
+  auto nth = [&](int i) { return (i * G::WR + wr) % (G::PART / 1024); };
+  auto q_row = [&](int i) {   // row of load i of K and V, or (from i = QI) of the scales
+    if (i < G::QI) return (nth(i) * 64 + lane) / G::CH;
+    return G::KV4 ? ((i - G::QI) * 64 + lane) / (G::SB / 4) % G::TK : lane % G::TK;
   };
-  uint32_t part[G::QI];
+  uint32_t part[G::QI], s_part[G::SI + 1];
 #pragma unroll
   for (int i = 0; i < G::QI; ++i) {
-    const int rw = q_row(i), lin = ((i * G::WR + wr) * 64 + lane) % G::CH;
+    const int rw = q_row(i), lin = (nth(i) * 64 + lane) % G::CH;
     part[i] = (rw & page_mask) * a.c.token + ((lin ^ swz<G>(rw)) << 4);
   }
-  const uint32_t s_part = (lane % G::TK & page_mask) * a.c.s_token * 4;
+#pragma unroll
+  for (int i = 0; i < G::SI; ++i)
+    s_part[i] = (q_row(G::QI + i) & page_mask) * a.c.s_token * SE + (G::KV4 ? lane % (G::SB / 4) * 4 : 0);
   const uint64_t zero = (uint64_t)g_zero;
   const KeyRange range = key_range(p_lo, p_hi, a.window, a.sinks);
-  uint64_t src[G::QI], s_src = 0;   // rows of the last K stage issued
-  bool there[G::QI], s_there = false;
+  uint64_t src[G::QI], s_src[G::SI + 1];   // rows of the last K stage issued
+  bool there[G::QI], s_there[G::SI + 1];
   // Page ids come with the K stage AHEAD before the one that they are for: a
   // load into registers would have to be waited for together with every
   // earlier load of the wave.
   auto entry = [&](int st, int row) { return table + table_entry(tile_key(st) + row, kv, a.c.page_shift); };
   auto issue_k = [&](int st, int slot, auto id_of) {
     const int key0 = tile_key(st);
-    int ids[G::QI], sid = 0;
+    int ids[G::QI], sid[G::SI + 1];
 #pragma unroll
     for (int i = 0; i < G::QI; ++i) ids[i] = id_of(i);
-    if constexpr (G::KV8) sid = id_of(G::QI);
+#pragma unroll
+    for (int i = 0; i < G::SI; ++i) sid[i] = id_of(G::QI + i);
     if constexpr (G::WR == 1) {
       // The next ids go where these lay: they have to be read, not only asked
       // for, before (waves that share a stage read them from the other slot).
 #pragma unroll
       for (int i = 0; i < G::QI; ++i) asm volatile("" : "+v"(ids[i]) : : "memory");
-      if constexpr (G::KV8) asm volatile("" : "+v"(sid) : : "memory");
+#pragma unroll
+      for (int i = 0; i < G::SI; ++i) asm volatile("" : "+v"(sid[i]) : : "memory");
     }
     uint8_t* const to = ring + slot;
     dma4((uint64_t)entry(st + G::AHEAD < ns ? st + G::AHEAD : st, lane % G::TK), to + G::PART + G::SCB);
     const uint64_t first = k_head + (uint32_t)(key0 & page_mask) * a.c.token;
 #pragma unroll
     for (int i = 0; i < G::QI; ++i) there[i] = page_there(ids[i], a.c.num_pages);
-    if constexpr (G::KV8) s_there = page_there(sid, a.c.num_pages);
+#pragma unroll
+    for (int i = 0; i < G::SI; ++i) s_there[i] = page_there(sid[i], a.c.num_pages);
     if (key0 + G::TK - 1 > range.to || key0 <= range.from) {   // a stage at the edge of what the rows see
       asm volatile("");
 #pragma unroll
       for (int i = 0; i < G::QI; ++i) there[i] = there[i] && key_in(key0 + q_row(i), range);
-      if constexpr (G::KV8) s_there = s_there && key_in(key0 + lane % G::TK, range);
+#pragma unroll
+      for (int i = 0; i < G::SI; ++i) s_there[i] = s_there[i] && key_in(key0 + q_row(G::QI + i), range);
     }
 #pragma unroll
     for (int i = 0; i < G::QI; ++i) {
       src[i] = first + (uint64_t)(uint32_t)ids[i] * a.c.page + part[i];
-      dma16<G::EVEN>(there[i] ? src[i] : zero, to + (i * G::WR + wr) * 1024);
+      dma16<G::EVEN>(there[i] ? src[i] : zero, to + nth(i) * 1024);
     }
-    if constexpr (G::KV8) {
-      s_src = ks_head + (uint64_t)(uint32_t)(key0 & page_mask) * a.c.s_token * 4 +
-              (uint64_t)(uint32_t)sid * a.c.s_page * 4 + s_part;
-      dma4(s_there ? s_src : zero, to + G::PART);
+#pragma unroll
+    for (int i = 0; i < G::SI; ++i) {
+      s_src[i] = ks_head + (uint64_t)(uint32_t)(key0 & page_mask) * a.c.s_token * SE +
+                 (uint64_t)(uint32_t)sid[i] * a.c.s_page * SE + s_part[i];
+      dma4(s_there[i] ? s_src[i] : zero, to + G::PART + i * 256);
     }
   };
   auto issue_v = [&](int slot) {
     uint8_t* const to = ring + slot;
 #pragma unroll
-    for (int i = 0; i < G::QI; ++i) dma16<G::EVEN>(there[i] ? src[i] + v_less_k : zero, to + (i * G::WR + wr) * 1024);
-    if constexpr (G::KV8) dma4(s_there ? s_src + vs_less_ks : zero, to + G::PART);
+    for (int i = 0; i < G::QI; ++i) dma16<G::EVEN>(there[i] ? src[i] + v_less_k : zero, to + nth(i) * 1024);
+#pragma unroll
+    for (int i = 0; i < G::SI; ++i) dma4(s_there[i] ? s_src[i] + vs_less_ks : zero, to + G::PART + i * 256);
   };
 
   acc_t o[G::DT];
@@ -507,14 +588,19 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
 
   // where the lane's part of a V^T fragment lies in a stage: tile d of the
   // output, keys kb + 4 g + {0..3} (first half) and kb + KB + 4 g + {0..3}
-  uint32_t v_off[G::DT][G::KV8 ? 1 : 2];
+  uint32_t v_off[G::DT][G::KV8 || G::KV4 ? 1 : 2];
   {
     constexpr int KB = G::MT == 16 ? 16 : 8;
     const int i16 = lane & 15, dh = G::MT == 32 ? ((lane >> 4) & 1) * 16 : 0;
 #pragma unroll
     for (int d = 0; d < G::DT; ++d)
 #pragma unroll
-      for (int h = 0; h < (G::KV8 ? 1 : 2); ++h) {
+      for (int h = 0; h < (G::KV8 || G::KV4 ? 1 : 2); ++h) {
+        if constexpr (G::KV4) {   // codes: a lane names the 16 of one key, keys KB apart four at a time
+          const int key = (i16 >> 2) * KB + 4 * g + (i16 & 3), blk = (d * G::MT + dh) / 16;
+          v_off[d][h] = (uint32_t)(uintptr_t)(lds_void*)ring + key * G::RB + (((blk >> 1) ^ swz<G>(key)) << 4) + 8 * (blk & 1);
+          continue;
+        }
         const int key = G::KV8 ? (i16 >> 3) * KB + 4 * g + ((i16 >> 1) & 3) : h * KB + 4 * g + (i16 >> 2);
         const int ch = G::KV8 ? (d * G::MT + dh) / 16 : (d * G::MT + dh) / 8 + ((i16 >> 1) & 1);
         v_off[d][h] = (uint32_t)(uintptr_t)(lds_void*)ring + key * G::RB + ((ch ^ swz<G>(key)) << 4) + 8 * (i16 & 1);
@@ -523,10 +609,14 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
 
   // ---- one stage: S^T = K Q^T
   typedef acc_t scores[G::NKT];
-  uint32_t k_off[G::KV8 ? G::QS / 2 : G::QS];   // the lane's part of the K fragments, key tile 0
+  uint32_t k_off[G::QS / G::KW];   // the lane's part of the K fragments, key tile 0
 #pragma unroll
-  for (int x = 0; x < (G::KV8 ? G::QS / 2 : G::QS); ++x)
-    k_off[x] = r * G::RB + (((x * G::LG + g) ^ swz<G>(r)) << 4);
+  for (int x = 0; x < G::QS / G::KW; ++x) {
+    if constexpr (G::KV4 && G::KW == 2)
+      k_off[x] = r * G::RB + ((((x * G::LG + g) >> 1) ^ swz<G>(r)) << 4) + 8 * (g & 1);
+    else
+      k_off[x] = r * G::RB + (((x * G::LG + g) ^ swz<G>(r)) << 4);
+  }
   auto products = [&](auto slot_c, scores& s) {
     constexpr int slot = decltype(slot_c)::value;
 #pragma unroll
@@ -535,7 +625,26 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
       for (int i = 0; i < AN; ++i) s[kt][i] = 0.0f;
       // (swz of the tile's first row is not 0 in the E4M3 layouts of 16-row tiles)
       const int at = slot + kt * G::MT * G::RB, f = swz<G>(kt * G::MT) << 4;
-      if constexpr (!G::KV8) {
+      if constexpr (G::KV4) {
+#pragma unroll
+        for (int x = 0; x < G::QS; x += G::KW) {
+          // the read's codes, 16 to a scale
+          const uint8_t* const sc = ring + slot + G::PART + (kt * G::MT + r) * G::SB + (x / G::KW * G::LG + g) * (G::KW / 2);
+          v2h s0, s1;
+          uint32_t u[4];
+          if constexpr (G::KW == 4) {
+            e4m3x2_scales(*(const uint16_t*)sc, s0, s1);
+            const v4i w = *(const v4i*)(ring + at + (k_off[x / 4] ^ f));
+            for (int j = 0; j < 4; ++j) u[j] = w[j];
+          } else {
+            e4m3x2_scales(*sc, s0, s1);
+            const v2i w = *(const v2i*)(ring + at + (k_off[x / 2] ^ f));
+            for (int j = 0; j < 2; ++j) u[j] = w[j];
+          }
+#pragma unroll
+          for (int j = 0; j < G::KW; ++j) s[kt] = mfma(e2m1x8_to_f16(u[j], j < 2 ? s0 : s1), q[x + j], s[kt]);
+        }
+      } else if constexpr (!G::KV8) {
 #pragma unroll
         for (int x = 0; x < G::QS; ++x) {
           const v8bf ka = *(const v8bf*)(ring + at + (k_off[x] ^ f));
@@ -599,8 +708,22 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
 #pragma unroll
         for (int i = 0; i < AN; ++i) o[d][i] *= f;
     }
+    _Float16* const v_tab = (_Float16*)(lds + G::RING + wave * G::VTAB);   // [D / 16][TK]
+    if constexpr (G::KV4) {
+      // the stage's scales of V in fp16, so that a lane finds those of four keys
+      // side by side: its part of a V^T fragment has a scale for every key
+      constexpr int HALF = G::TK == 64 ? G::SB : G::SB / 2;                // scales of a key that one lane takes
+      const uint8_t* const from = ring + decltype(v_at)::value + G::PART + lane % G::TK * G::SB + lane / G::TK * HALF;
+#pragma unroll
+      for (int j = 0; j < HALF; j += 2) {
+        const v2h two = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)*(const uint16_t*)(from + j), 1.0f, false);
+        v_tab[(lane / G::TK * HALF + j) * G::TK + lane % G::TK] = two[0];
+        v_tab[(lane / G::TK * HALF + j + 1) * G::TK + lane % G::TK] = two[1];
+      }
+    }
     products(k_next, sb);
     const float* sc = (const float*)(ring + decltype(v_at)::value + G::PART);
+    const float from = G::KV4 ? kUp - m : -m;
     uint32_t p[G::NKT * AN / 2];
 #pragma unroll
     for (int kt = 0; kt < G::NKT; ++kt)
@@ -611,18 +734,51 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
         float e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sa[kt][4 * i4 + i], c, -m));
+          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sa[kt][4 * i4 + i], c, from));
           l += e[i];
           if constexpr (G::KV8) e[i] *= vs[i];
         }
         // bf16 is what the matrix instruction takes beside bf16 (or converted)
         // values: an output is off by 0.0023 of its size where its own rounding
         // is 0.0017.  Two halves of each probability would double the products.
-        p[(kt * AN + 4 * i4) / 2] = pack_bf16(e[0], e[1]);
-        p[(kt * AN + 4 * i4) / 2 + 1] = pack_bf16(e[2], e[3]);
+        p[(kt * AN + 4 * i4) / 2] = G::KV4 ? pack_f16(e[0], e[1]) : pack_bf16(e[0], e[1]);
+        p[(kt * AN + 4 * i4) / 2 + 1] = G::KV4 ? pack_f16(e[2], e[3]) : pack_bf16(e[2], e[3]);
       }
+    if constexpr (G::KV4) {
+      // four reads at a time (keys of steps 2 x and 2 x + 1, tile d of the output)
+      const int dh = G::MT == 32 ? (lane >> 4) & 1 : 0;
+      unrolled<G::PS / 2 * G::DT / 4>([&](auto blk) {
+        constexpr int F0 = 4 * decltype(blk)::value;
+        auto at_key = [](int f) constexpr { return decltype(v_at)::value + f / G::DT * 2 * G::KS * G::RB; };
+        uint32_t ad[4];
+        v2i x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ad[j] = v_off[(F0 + j) % G::DT][0];
+        read_tr4<at_key(F0), at_key(F0 + 1), at_key(F0 + 2), at_key(F0 + 3)>(x, ad);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          constexpr int DT = G::DT, KB = G::MT == 16 ? 16 : 8;
+          const int y = (F0 + j) / DT, d = (F0 + j) % DT;
+          v2h vs[8];   // the scales of the lane's 16 keys
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const v4h w = *(const v4h*)(v_tab + (d * G::MT / 16 + dh) * G::TK + y * 2 * G::KS + k4 * KB + 4 * g);
+            vs[2 * k4] = __builtin_shufflevector(w, w, 0, 1);
+            vs[2 * k4 + 1] = __builtin_shufflevector(w, w, 2, 3);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int st2 = 2 * y + h;
+            const v8h pb = __builtin_bit_cast(
+                v8h, (v4i{(int)p[4 * st2], (int)p[4 * st2 + 1], (int)p[4 * st2 + 2], (int)p[4 * st2 + 3]}));
+            o[d] = mfma(e2m1x8_pairs((uint32_t)x[j][h], vs + 4 * h), pb, o[d]);
+          }
+        }
+      });
+      return;
+    }
     // O^T += V^T P^T, four fragments (step x of the keys, tile d of the output) at a time
-    unrolled<G::PS * G::DT / 4>([&](auto blk) {
+    if constexpr (!G::KV4) unrolled<G::PS * G::DT / 4>([&](auto blk) {
       constexpr int F0 = 4 * decltype(blk)::value;
       auto at_key = [](int f) constexpr { return decltype(v_at)::value + f / G::DT * G::KS * G::RB; };
       v8bf va[4];
@@ -668,11 +824,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
     };
     // the first stages' ids before any of their loads: a wait for an id is one
     // for every load before it
-    int first_ids[G::NST][G::QI + 1];
+    int first_ids[G::NST][G::QI + G::SI];
 #pragma unroll
     for (int st = 0; st < G::NST; ++st)
 #pragma unroll
-      for (int i = 0; i < G::QI + G::KV8; ++i) first_ids[st][i] = *entry(st < ns ? st : 0, q_row(i));
+      for (int i = 0; i < G::QI + G::SI; ++i) first_ids[st][i] = *entry(st < ns ? st : 0, q_row(i));
 #pragma unroll
     for (int st = 0; st < G::NST; ++st)
       if (st < ns) {
@@ -722,12 +878,13 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   }
 
   // ---- join the lane groups' sums and the key groups' parts, and write
+  const float v_unit = G::KV4 ? a.c.v_unit : 1.0f, up2 = G::KV4 ? kUp : 0.0f;
 #pragma unroll
   for (int x = G::MT; x < 64; x <<= 1) l += __shfl_xor(l, x);
   if constexpr (G::WK == 1) {
     if (!live) return;
-    const float inv = l > 0.0f ? 1.0f / l : l;   // l: 0, or NaN kept
-    const float lse2 = l == 0.0f ? -__builtin_inff() : m + __builtin_amdgcn_logf(l);
+    const float inv = (l > 0.0f ? 1.0f / l : l) * v_unit;   // l: 0, or NaN kept
+    const float lse2 = l == 0.0f ? -__builtin_inff() : m - up2 + __builtin_amdgcn_logf(l);
     const size_t ps = pc.part + at;
 #pragma unroll
     for (int d = 0; d < G::DT; ++d)
@@ -774,8 +931,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
 #pragma unroll
         for (int i = 0; i < 4; ++i) ov[i] += y[i] * f;
       }
-      const float inv = ll > 0.0f ? 1.0f / ll : ll;
-      const float lse2 = ll == 0.0f ? -__builtin_inff() : mm + __builtin_amdgcn_logf(ll);
+      const float inv = (ll > 0.0f ? 1.0f / ll : ll) * v_unit;
+      const float lse2 = ll == 0.0f ? -__builtin_inff() : mm - up2 + __builtin_amdgcn_logf(ll);
       const size_t ar = a.even && !pc.direct ? 0 : (size_t)(t0 + rg / a.group) * a.heads + kvh * a.group + rg % a.group;
       if (pc.direct) {
         *(v2i*)(a.out + ar * G::D + d) = v2i{(int)pack_bf16(ov[0] * inv, ov[1] * inv),
@@ -951,19 +1108,32 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
 // and two workgroups a CU allow them (E4M3 at 128: 198 -> 189; bf16 would leave
 // one workgroup a CU: 40 x 13 rows over 4096 keys 99 -> 131).  Three waves a SIMD
 // at head size 64 for many rows (309 against 348), two for up to 64 (20.5, 22.8).
-template <int D, bool KV8, class F>
+template <int D, int FMT, class F>
 auto visit_rows(int64_t rows, F f) {
-  if (rows <= 16) return f(Geo<D, KV8, 16, 1, D == 256 && !KV8 ? 2 : 4, 32, D == 256 ? 1 : 2>{});
+  constexpr bool KV8 = FMT == OCQ_CACHE_E4M3;
+  if constexpr (FMT == OCQ_CACHE_NVFP4) {
+    if (rows <= 16) return f(Geo<D, FMT, 16, 1, D == 256 ? 2 : 4, 64, D == 256 ? 1 : 2>{});
+    if constexpr (D < 256)
+      if (rows <= 32) return f(Geo<D, FMT, 32, 1, 4, 64, 2>{});
+    if (rows <= 64) return f(Geo<D, FMT, 32, 2, 2, 64, D == 256 ? 1 : 2>{});
+    return f(Geo<D, FMT, 32, 4, 1, D == 256 ? 32 : 64, D == 256 ? 1 : 2>{});
+  } else {
+  if (rows <= 16) return f(Geo<D, FMT, 16, 1, D == 256 && !KV8 ? 2 : 4, 32, D == 256 ? 1 : 2>{});
   if constexpr (D < 256)
-    if (rows <= 32) return f(Geo<D, KV8, 32, 1, 4, 32, 2>{});
-  if (rows <= 64) return f(Geo<D, KV8, 32, 2, 2, KV8 && D == 128 ? 64 : 32, D == 256 ? 1 : 2>{});
-  return f(Geo<D, KV8, 32, 4, 1, D == 256 ? 32 : 64, D == 256 ? 1 : D == 64 ? 3 : 2>{});
+    if (rows <= 32) return f(Geo<D, FMT, 32, 1, 4, 32, 2>{});
+  if (rows <= 64) return f(Geo<D, FMT, 32, 2, 2, KV8 && D == 128 ? 64 : 32, D == 256 ? 1 : 2>{});
+  return f(Geo<D, FMT, 32, 4, 1, D == 256 ? 32 : 64, D == 256 ? 1 : D == 64 ? 3 : 2>{});
+  }
+}
+template <int D, class F>
+auto visit_format(int format, int64_t rows, F f) {
+  return format == OCQ_CACHE_BF16 ? visit_rows<D, OCQ_CACHE_BF16>(rows, f)
+         : format == OCQ_CACHE_E4M3 ? visit_rows<D, OCQ_CACHE_E4M3>(rows, f) : visit_rows<D, OCQ_CACHE_NVFP4>(rows, f);
 }
 template <class F>
-auto visit(int dim, bool e4m3, int64_t rows, F f) {
-  if (dim == 64) return e4m3 ? visit_rows<64, true>(rows, f) : visit_rows<64, false>(rows, f);
-  if (dim == 128) return e4m3 ? visit_rows<128, true>(rows, f) : visit_rows<128, false>(rows, f);
-  return e4m3 ? visit_rows<256, true>(rows, f) : visit_rows<256, false>(rows, f);
+auto visit(int dim, int format, int64_t rows, F f) {
+  return dim == 64 ? visit_format<64>(format, rows, f) : dim == 128 ? visit_format<128>(format, rows, f)
+                                                                    : visit_format<256>(format, rows, f);
 }
 
 }  // namespace
@@ -979,12 +1149,12 @@ auto visit(int dim, bool e4m3, int64_t rows, F f) {
 //  * Else one workgroup per row tile, all its keys: enough of them to fill the
 //    GPU by themselves, or at most four key tiles (a join takes longer than
 //    those: 257 keys 8.7 us in all).
-AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads, int kv_heads, int dim, int e4m3,
+AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads, int kv_heads, int dim, int format,
                    int window, int sinks, int64_t cap) {
   const int64_t rows = (int64_t)max_new * (heads / kv_heads);
   int64_t keys = max_kv;
   if (window > 0 && (int64_t)window + sinks + max_new < keys) keys = (int64_t)window + sinks + max_new;
-  return visit(dim, e4m3 != 0, rows, [&](auto geo) {
+  return visit(dim, format, rows, [&](auto geo) {
     typedef decltype(geo) G;
     AttnPlan p{0, 1, 0, 0, 0};
     const int64_t pairs = (int64_t)requests * kv_heads, tiles = (rows + G::ROWS - 1) / G::ROWS;
@@ -1013,7 +1183,7 @@ AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads,
 
 int launch_attn(const AttnArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
-  return (int)visit(a.dim, a.e4m3 != 0, (int64_t)a.max_new * a.group,
+  return (int)visit(a.dim, a.format, (int64_t)a.max_new * a.group,
                     [&](auto geo) { return run<decltype(geo)>(a, st); });
 }
 

@@ -35,11 +35,12 @@ struct BatchArgs {
 struct CacheArgs {
   uint8_t* k;
   uint8_t* v;
-  float* k_scale;            // E4M3 only
+  float* k_scale;            // E4M3: one a row; NVFP4: E4M3 bytes, one per 16 values of a row
   float* v_scale;
-  int64_t head, s_head;            // strides: of k and v in bytes, of the scales in elements
+  int64_t head, s_head;            // strides: of k and v in bytes, of the scales in elements (NVFP4: bytes)
   uint32_t page, token, s_page, s_token;
   int num_pages, page_shift, kv_heads;
+  float k_unit, v_unit;      // NVFP4: what every scale is a multiple of
 };
 
 struct RopeArgs {
@@ -51,7 +52,7 @@ struct RopeArgs {
   const int32_t* positions;  // nullable: place in the request
   uint16_t* q_out;           // [tokens][heads][dim]
   float multiplier;
-  int heads, dim, rot, interleaved, e4m3;
+  int heads, dim, rot, interleaved, format;
   int first;                 // token of the launch's first workgroup
   BatchArgs b;
   CacheArgs c;
@@ -63,7 +64,7 @@ struct AttnArgs {
   uint16_t* out;             // [tokens][heads][dim]
   float* lse;                // nullable, [tokens][heads]
   float scale;
-  int heads, group, dim, window, sinks, e4m3;
+  int heads, group, dim, window, sinks, format;
   int max_new;
   BatchArgs b;
   CacheArgs c;
@@ -73,6 +74,15 @@ struct AttnArgs {
   float* part_o;             // [part_rows][dim]
   float* part_lse;           // [part_rows]
   uint32_t* counters;        // [OCQ_ATTENTION_COUNTERS], 0 between calls
+};
+
+// The values that an E4M3 or NVFP4 cache stands for, [pages][kv_heads][page_size][dim] bf16.
+struct ValuesArgs {
+  uint16_t* k;
+  uint16_t* v;
+  int64_t rows;              // pages x kv_heads x page_size
+  int dim, format;
+  CacheArgs c;
 };
 
 struct AttnPlan {
@@ -89,8 +99,9 @@ constexpr unsigned kLanesAtOnce = 1u << 31;
 int launch_norm(const NormArgs& a, void* stream);
 int launch_rope(const RopeArgs& a, void* stream);
 int launch_attn(const AttnArgs& a, void* stream);
+int launch_values(const ValuesArgs& a, void* stream);
 // layout of a call of this shape (host numbers only; cap: keys that a request's row of the page table can name)
-AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads, int kv_heads, int dim, int e4m3,
+AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads, int kv_heads, int dim, int format,
                    int window, int sinks, int64_t cap);
 
 }  // namespace ocq

@@ -1,96 +1,12 @@
 // C-ABI entry points of the operators around the MLP block: argument checks,
 // rotary frequencies, launches.
-#include <hip/hip_runtime.h>
-
 #include <cmath>
-#include <cstdio>
 
-#include "layer.h"
-#include "ocq_internal.h"
+#include "layer_check.h"
 
 using namespace ocq;
 
 namespace {
-
-ocq_status hip_error(int rc) {
-  char buf[256];
-  std::snprintf(buf, sizeof(buf), "kernel launch: %s (%d)", hipGetErrorString((hipError_t)rc), rc);
-  return set_error(OCQ_ERR_DEVICE, buf);
-}
-
-ocq_status invalid(const char* msg) { return set_error(OCQ_ERR_INVALID_ARG, msg); }
-ocq_status unsupported(const char* msg) { return set_error(OCQ_ERR_UNSUPPORTED, msg); }
-
-bool aligned(const void* p, uintptr_t n = 16) { return ((uintptr_t)p & (n - 1)) == 0; }
-
-// strides that keep every byte offset far from 2^63, and 16-byte aligned in units of `per16` elements
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
-constexpr int64_t kMaxPage = 0xFFFFFFFFll, kMaxInPage = 0x7FFFFFFFll, kMaxScaleInPage = 0x3FFFFFFFll;
-bool stride_ok(int64_t s, int per16) { return s >= 0 && s <= kMaxStride && s % per16 == 0; }
-
-ocq_status check_cache(const ocq_kv_cache* c) {
-  if (!c) return invalid("cache is null");
-  if (c->format != OCQ_CACHE_BF16 && c->format != OCQ_CACHE_E4M3) return invalid("cache format must be 0 or 1");
-  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
-    return unsupported("head_dim must be 64, 128 or 256");
-  if (c->page_size < 1 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
-    return unsupported("page_size must be a power of two in [1, 1024]");
-  if (c->num_pages < 1 || c->kv_heads < 1 || c->kv_heads > 4096)
-    return invalid("num_pages and kv_heads (up to 4096) must be positive");
-  if (!c->k_dev || !c->v_dev) return invalid("null cache pointer");
-  if (!aligned(c->k_dev) || !aligned(c->v_dev)) return invalid("cache pointers must be 16-byte aligned");
-  const int per16 = c->format == OCQ_CACHE_E4M3 ? 16 : 8;
-  if (!stride_ok(c->page_stride, per16) || !stride_ok(c->head_stride, per16) || !stride_ok(c->token_stride, per16))
-    return invalid("cache strides must be multiples of 16 bytes, not negative");
-  const int64_t esz = 16 / per16;
-  if (c->page_stride * esz > kMaxPage || (c->page_size - 1) * c->token_stride * esz > kMaxInPage)
-    return unsupported("page strides must be below 2^32 bytes, a page's rows within 2^31");
-  if (c->format == OCQ_CACHE_E4M3) {
-    if (!c->k_scale_dev || !c->v_scale_dev) return invalid("an E4M3 cache needs scales");
-    if (!aligned(c->k_scale_dev, 4) || !aligned(c->v_scale_dev, 4)) return invalid("misaligned scale pointer");
-    if (!stride_ok(c->scale_page_stride, 1) || !stride_ok(c->scale_head_stride, 1) ||
-        !stride_ok(c->scale_token_stride, 1))
-      return invalid("scale strides must not be negative");
-    // (attention holds a scale's byte offset in its page in 32 bits; in 64 a verify
-    // pass of 16 x 13 tokens over 512 E4M3 keys takes 18.0 us instead of 17.6)
-    if (c->scale_page_stride > kMaxPage || (c->page_size - 1) * c->scale_token_stride > kMaxScaleInPage)
-      return unsupported("scale page strides must be below 2^32, a page's rows within 2^30");
-  }
-  return OCQ_OK;
-}
-
-ocq_status check_batch(const ocq_token_batch* b, const ocq_kv_cache* c, int heads) {
-  if (!b) return invalid("batch is null");
-  if (b->requests < 0 || b->tokens < 0) return invalid("requests and tokens must not be negative");
-  if (heads < 1 || heads > 65536 || heads % c->kv_heads) return invalid("heads must be a multiple of kv_heads, up to 65536");
-  if ((int64_t)b->tokens * heads >= (int64_t)1 << 31) return unsupported("tokens * heads must be below 2^31");
-  if (b->requests == 0 || b->tokens == 0) return OCQ_OK;
-  if (b->requests > 65536) return unsupported("at most 65536 requests");
-  if (b->max_pages < 1 || (int64_t)b->max_pages * c->page_size >= (int64_t)1 << 31)
-    return unsupported("max_pages * page_size must be in [1, 2^31)");
-  if (b->max_new < 1 || b->max_kv < 0) return invalid("max_new must be positive, max_kv not negative");
-  if (!stride_ok(b->table_stride, 1) || b->table_stride < b->max_pages)
-    return invalid("table_stride must be at least max_pages");
-  if (!b->q_start_dev || !b->kv_lens_dev || !b->page_table_dev) return invalid("null batch pointer");
-  if (!aligned(b->q_start_dev, 4) || !aligned(b->kv_lens_dev, 4) || !aligned(b->page_table_dev, 4))
-    return invalid("misaligned batch pointer");
-  return OCQ_OK;
-}
-
-BatchArgs batch_args(const ocq_token_batch* b) {
-  return BatchArgs{(const int32_t*)b->q_start_dev, (const int32_t*)b->kv_lens_dev, (const int32_t*)b->page_table_dev,
-                   b->table_stride, b->requests, b->tokens, b->max_pages};
-}
-
-CacheArgs cache_args(const ocq_kv_cache* c) {
-  const int64_t esz = c->format == OCQ_CACHE_E4M3 ? 1 : 2;
-  int shift = 0;
-  while ((1 << shift) < c->page_size) ++shift;
-  return CacheArgs{(uint8_t*)c->k_dev, (uint8_t*)c->v_dev, (float*)c->k_scale_dev, (float*)c->v_scale_dev,
-                   c->head_stride * esz, c->scale_head_stride, (uint32_t)(c->page_stride * esz),
-                   (uint32_t)(c->token_stride * esz), (uint32_t)c->scale_page_stride, (uint32_t)c->scale_token_stride,
-                   c->num_pages, shift, c->kv_heads};
-}
 
 int max_new(const ocq_token_batch* b) { return b->max_new < b->tokens ? b->max_new : b->tokens; }
 
@@ -183,7 +99,7 @@ ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_
   const RopeArgs a{(const uint16_t*)q_dev, (const uint16_t*)k_dev, (const uint16_t*)v_dev, q_token_stride,
                    q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
                    (const double*)inv_freq_dev, (const int32_t*)positions_dev, (uint16_t*)q_out_dev, multiplier, heads,
-                   cache->head_dim, rot, interleaved, cache->format == OCQ_CACHE_E4M3, 0, batch_args(batch),
+                   cache->head_dim, rot, interleaved, cache->format, 0, batch_args(batch),
                    cache_args(cache)};
   const int rc = launch_rope(a, stream);
   return rc ? hip_error(rc) : OCQ_OK;
@@ -233,7 +149,7 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
   a.dim = cache->head_dim;
   a.window = window;
   a.sinks = sinks;
-  a.e4m3 = cache->format == OCQ_CACHE_E4M3;
+  a.format = cache->format;
   a.max_new = max_new(batch);
   a.b = batch_args(batch);
   a.c = cache_args(cache);

@@ -42,12 +42,44 @@ __device__ __forceinline__ int request_of(const BatchArgs& b, int t) {
   return r;
 }
 
+// The 16 values of a block of an NVFP4 row: its scale's code, then the codes.  The
+// scale's E4M3 rounding decides first; the quotients are of the rounded scale.
+struct Block4 {
+  uint32_t scale;
+  v2u codes;
+};
+__device__ __forceinline__ Block4 nvfp4_block(const float (&y)[16], float unit) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) amax = max_mag(amax, y[j]);
+  Block4 b{0x7Fu, v2u{0u, 0u}};                    // E4M3's NaN
+  if (!(amax < __builtin_inff())) return b;
+  b.scale = enc_e4m3(amax / 6.0f / unit);
+  if (b.scale == 0) return b;
+  const float s = (float)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b.scale, 1.0f, false)[0] * unit;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t c = 0;
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_fmed3f(y[8 * h + j] / s, -6.0f, 6.0f);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[0], q[1], 1.0f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[2], q[3], 1.0f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[4], q[5], 1.0f, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, q[6], q[7], 1.0f, 3);
+    b.codes[h] = c;
+  }
+  return b;
+}
+
 constexpr int kRopeThreads = 256, kAtOnce = kLanesAtOnce / kRopeThreads;   // tokens of a launch
 
-template <int DIM, bool E4M3>
+template <int DIM, int FMT>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
+  constexpr bool E4M3 = FMT == OCQ_CACHE_E4M3, NVFP4 = FMT == OCQ_CACHE_NVFP4;
   constexpr int LPH = DIM / 16;   // lanes per head
   __shared__ float s_cos[DIM / 2], s_sin[DIM / 2];
+  __shared__ double d_cos[NVFP4 ? DIM / 2 : 1], d_sin[NVFP4 ? DIM / 2 : 1];
   const int t = a.first + blockIdx.x;
   const int r = request_of(a.b, t);
   if (r < 0) return;
@@ -55,6 +87,15 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
   const int64_t pos = a.positions ? a.positions[t] : place;
   const int half = a.rot / 2;
   for (int j = threadIdx.x; j < half; j += kRopeThreads) {
+    if constexpr (NVFP4) {
+      double sn, cs;
+      sincos((double)pos * a.inv_freq[j], &sn, &cs);
+      d_cos[j] = cs * a.multiplier;
+      d_sin[j] = sn * a.multiplier;
+      s_cos[j] = (float)d_cos[j];
+      s_sin[j] = (float)d_sin[j];
+      continue;
+    }
     double turns = (double)pos * a.inv_freq[j] * 0.15915494309189533577;   // 1 / (2 pi)
     turns -= __builtin_rint(turns);
     float sn, cs;
@@ -79,6 +120,50 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeArgs a) {
     const uint16_t* src = which == 0 ? a.q + t * a.q_token + head * a.q_head
                         : which == 1 ? a.k + t * a.k_token + head * a.k_head
                                      : a.v + t * a.v_token + head * a.v_head;
+    if constexpr (NVFP4) {
+      if (which > 0) {
+        // a lane's 16 elements are one block; of their pairs' other halves it reads
+        // what it needs: eight elements are all first or all second ones
+        float y[16];
+        load8(src + 16 * i, y);
+        load8(src + 16 * i + 8, y + 8);
+        if (which == 1 && 16 * i < a.rot) {
+          if (a.interleaved) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const double c = d_cos[8 * i + j], s = d_sin[8 * i + j], u = y[2 * j], v = y[2 * j + 1];
+              y[2 * j] = (float)(u * c - v * s);
+              y[2 * j + 1] = (float)(v * c + u * s);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int e = 16 * i + 8 * h;
+              const bool first = e < half;
+              float o[8];
+              load8(src + (first ? e + half : e - half), o);
+              const double* const cs = d_cos + (first ? e : e - half);
+              const double* const sn = d_sin + (first ? e : e - half);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const double x = (double)y[8 * h + j] * cs[j], z = (double)o[j] * sn[j];
+                y[8 * h + j] = (float)(first ? x - z : x + z);
+              }
+            }
+          }
+        }
+        const Block4 b = nvfp4_block(y, which == 1 ? a.c.k_unit : a.c.v_unit);
+        if (slot) {
+          uint8_t* const pool = (which == 1 ? a.c.k : a.c.v) + head * a.c.head +
+                                row_offset(key, page, a.c.page_shift, a.c.page, a.c.token);
+          uint8_t* const sc = (uint8_t*)(which == 1 ? a.c.k_scale : a.c.v_scale) + head * a.c.s_head +
+                              row_offset(key, page, a.c.page_shift, a.c.s_page, a.c.s_token);
+          *(v2u*)(pool + 8 * i) = b.codes;
+          sc[i] = (uint8_t)b.scale;
+        }
+        continue;
+      }
+    }
     const bool turn = i * 16 < a.rot;
     const bool split = turn && !a.interleaved;
     const int d0 = split ? 8 * i : 16 * i, d1 = split ? half + 8 * i : 16 * i + 8;
@@ -146,11 +231,69 @@ template <int DIM>
 void run(const RopeArgs& a, hipStream_t st) {
   const int left = a.b.tokens - a.first;
   const dim3 grid(left < kAtOnce ? left : kAtOnce), block(kRopeThreads);
-  if (a.e4m3) hipLaunchKernelGGL((k_rope<DIM, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_rope<DIM, false>), grid, block, 0, st, a);
+  if (a.format == OCQ_CACHE_NVFP4) hipLaunchKernelGGL((k_rope<DIM, OCQ_CACHE_NVFP4>), grid, block, 0, st, a);
+  else if (a.format == OCQ_CACHE_E4M3) hipLaunchKernelGGL((k_rope<DIM, OCQ_CACHE_E4M3>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_rope<DIM, OCQ_CACHE_BF16>), grid, block, 0, st, a);
+}
+
+// The values of a pool of codes: a lane makes 16 of one row, of k, then of v.
+template <bool NVFP4>
+__global__ __launch_bounds__(256) void k_values(ValuesArgs a, int64_t first) {
+  const int lanes = a.dim / 16;
+  const int64_t it = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = it / lanes;
+  if (row >= a.rows) return;
+  const int i = (int)(it % lanes), key = (int)(row & ((1 << a.c.page_shift) - 1));
+  const int64_t up = row >> a.c.page_shift;
+  const int head = (int)(up % a.c.kv_heads), page = (int)(up / a.c.kv_heads);
+  const uint64_t at = row_offset(key, page, a.c.page_shift, a.c.page, a.c.token) + head * a.c.head;
+  const uint64_t s_at = row_offset(key, page, a.c.page_shift, a.c.s_page, a.c.s_token) + head * a.c.s_head;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint8_t* const pool = (kv ? a.c.v : a.c.k) + at;
+    float y[16];
+    if constexpr (NVFP4) {
+      const v2u c = *(const v2u*)(pool + 8 * i);
+      const uint32_t sc = ((const uint8_t*)(kv ? a.c.v_scale : a.c.k_scale))[s_at + i];
+      const float unit = kv ? a.c.v_unit : a.c.k_unit;
+      v2h s0, s1;
+      e4m3x2_scales(sc, s0, s1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v8h v = e2m1x8_to_f16(c[h], s0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[8 * h + j] = (float)v[j] * unit;
+      }
+    } else {
+      const v4i c = *(const v4i*)(pool + 16 * i);
+      const float s = (kv ? a.c.v_scale : a.c.k_scale)[s_at];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v8h v = e4m3x8_to_f16((uint32_t)c[2 * h], (uint32_t)c[2 * h + 1]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[8 * h + j] = (float)v[j] * s;
+      }
+    }
+    uint16_t* const to = (kv ? a.v : a.k) + row * a.dim + 16 * i;
+    store8(to, y);
+    store8(to + 8, y + 8);
+  }
 }
 
 }  // namespace
+
+int launch_values(const ValuesArgs& a, void* stream) {
+  const int64_t items = a.rows * (a.dim / 16);
+  for (int64_t first = 0; first < items; first += kLanesAtOnce) {
+    const int64_t left = items - first, now = left < kLanesAtOnce ? left : kLanesAtOnce;
+    const dim3 grid((unsigned)((now + 255) / 256)), block(256);
+    if (a.format == OCQ_CACHE_NVFP4) hipLaunchKernelGGL((k_values<true>), grid, block, 0, (hipStream_t)stream, a, first);
+    else hipLaunchKernelGGL((k_values<false>), grid, block, 0, (hipStream_t)stream, a, first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+  }
+  return 0;
+}
 
 int launch_rope(const RopeArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;

@@ -34,7 +34,7 @@ EXPORTS = ("ocq_version", "ocq_packed_bytes", "ocq_pack_weights_host", "ocq_pack
            "ocq_diag_stream_read", "ocq_diag_window_read", "ocq_diag_mfma_rate", "ocq_diag_empty", "ocq_diag_mfma_dot", "ocq_diag_phase_stamps", "ocq_noalloc_scratch_bytes",
            "ocq_mlp_forward_noalloc", "ocq_set_fused_requant", "ocq_last_requant_in_gateup",
            "ocq_add_rmsnorm", "ocq_rope_frequencies", "ocq_rope_append", "ocq_attention_workspace_bytes",
-           "ocq_paged_attention")
+           "ocq_paged_attention", "ocq_cache_values")
 
 
 class OcqError(RuntimeError):
@@ -52,7 +52,8 @@ class KVCacheStruct(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("k_dev", "v_dev", "k_scale_dev", "v_scale_dev")] +
                 [(n, ctypes.c_int64) for n in ("page_stride", "head_stride", "token_stride", "scale_page_stride",
                                                "scale_head_stride", "scale_token_stride")] +
-                [(n, ctypes.c_int) for n in ("num_pages", "page_size", "kv_heads", "head_dim", "format")])
+                [(n, ctypes.c_int) for n in ("num_pages", "page_size", "kv_heads", "head_dim", "format")] +
+                [(n, ctypes.c_float) for n in ("k_unit", "v_unit")])
 
 
 class TokenBatchStruct(ctypes.Structure):
@@ -120,6 +121,7 @@ def lib():
     L.ocq_attention_workspace_bytes.argtypes, L.ocq_attention_workspace_bytes.restype = [i, cp, bp, i, i], sz
     L.ocq_paged_attention.argtypes = [vp, i64, i64, i, cp, bp, f, i, i, vp, vp, vp, sz, vp]
     L.ocq_paged_attention.restype = i
+    L.ocq_cache_values.argtypes, L.ocq_cache_values.restype = [cp, vp, vp, vp], i
     _lib = L
     return L
 
@@ -524,14 +526,23 @@ class PagedKVCache:
     k, v: [num_pages, kv_heads, page_size, head_dim] CUDA tensors, bf16, or float8_e4m3fn (or uint8) codes with
     k_scale, v_scale float32 [num_pages, kv_heads, page_size].  Any order of the first three axes in memory (a
     permuted view of a pool of another layout is fine), the same for k and v.
+
+    An NVFP4 cache has k, v uint8 (or float4_e2m1fn_x2) [num_pages, kv_heads, page_size, head_dim / 2], element 2 i in
+    the low half of byte i, with k_scale, v_scale float8_e4m3fn (or uint8) [num_pages, kv_heads, page_size, head_dim /
+    16]; k_unit and v_unit, powers of two, move the scales' range: an element is code x scale x unit.
     """
 
-    def __init__(self, k, v, k_scale=None, v_scale=None):
+    def __init__(self, k, v, k_scale=None, v_scale=None, k_unit=1.0, v_unit=1.0):
         import torch
         self.index = _gpu(k, "k")
         dev = k.device
-        if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
+        nvfp4 = hasattr(k_scale, "dim") and k_scale.dim() == 4
+        if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8) and not nvfp4:
             raise OcqError(ERR_INVALID_ARG, "k must be [pages, kv_heads, page_size, head_dim], bf16 or E4M3 codes")
+        if nvfp4 and k.dtype not in (torch.uint8, torch.float4_e2m1fn_x2):
+            raise OcqError(ERR_INVALID_ARG, "the codes of an NVFP4 cache are uint8 or float4_e2m1fn_x2, two a byte")
+        if not nvfp4 and (k_unit != 1.0 or v_unit != 1.0):
+            raise OcqError(ERR_INVALID_ARG, "k_unit and v_unit are of NVFP4 caches")
         if v is None or not hasattr(v, "data_ptr") or v.device != dev or v.dtype != k.dtype or v.shape != k.shape or \
                 v.stride() != k.stride():
             raise OcqError(ERR_INVALID_ARG, "v must have k's device, dtype, shape and strides")
@@ -540,7 +551,14 @@ class PagedKVCache:
         e4m3 = k.dtype != torch.bfloat16
         if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
             raise OcqError(ERR_INVALID_ARG, "E4M3 caches have scales, bf16 caches none")
-        if e4m3:
+        if nvfp4:
+            want = k.shape[:3] + (k.shape[3] // 8,)
+            for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if not hasattr(t, "device") or t.device != dev or t.dtype not in (torch.float8_e4m3fn, torch.uint8) or \
+                        t.shape != want or t.stride() != k_scale.stride() or t.stride(3) != 1:
+                    raise OcqError(ERR_INVALID_ARG, "%s must be float8_e4m3fn or uint8 %s, its last axis contiguous, "
+                                   "k_scale and v_scale of one layout" % (name, tuple(want)))
+        elif e4m3:
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
                 if t.device != dev or t.dtype != torch.float32 or t.shape != k.shape[:3] or \
                         t.stride() != k_scale.stride():
@@ -550,17 +568,28 @@ class PagedKVCache:
         for n, name in zip(k.shape, ("pages", "kv_heads", "page_size", "head_dim")):
             _int32(n, name)
         pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        if nvfp4:
+            self.head_dim *= 2
+        self.k_unit, self.v_unit = float(k_unit), float(v_unit)
         s = k_scale.stride() if e4m3 else (0, 0, 0)
         self.struct = KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if e4m3 else None,
                                     v_scale.data_ptr() if e4m3 else None, k.stride(0), k.stride(1), k.stride(2), s[0],
-                                    s[1], s[2], pages, self.page_size, self.kv_heads, self.head_dim, int(e4m3))
+                                    s[1], s[2], pages, self.page_size, self.kv_heads, self.head_dim,
+                                    2 if nvfp4 else int(e4m3), self.k_unit, self.v_unit)
         self.ref = ctypes.byref(self.struct)
 
     @classmethod
-    def allocate(cls, num_pages, page_size, kv_heads, head_dim, e4m3=False, device="cuda"):
+    def allocate(cls, num_pages, page_size, kv_heads, head_dim, e4m3=False, device="cuda", nvfp4=False, k_unit=1.0,
+                 v_unit=1.0):
         """A zeroed cache whose pages hold each head's rows side by side."""
         import torch
         shape = (num_pages, kv_heads, page_size, head_dim)
+        if nvfp4:
+            if e4m3:
+                raise OcqError(ERR_INVALID_ARG, "a cache is E4M3 or NVFP4, not both")
+            kv = [torch.zeros(shape[:3] + (n,), dtype=torch.uint8, device=device)
+                  for n in (head_dim // 2, head_dim // 2, head_dim // 16, head_dim // 16)]
+            return cls(kv[0], kv[1], *(t.view(torch.float8_e4m3fn) for t in kv[2:]), k_unit, v_unit)
         if not e4m3:
             return cls(*(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
         kv = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
@@ -752,6 +781,22 @@ def paged_attention(q, cache, batch, scale=None, window=0, sinks=0, want_lse=Fal
                                  None if lse is None else lse.data_ptr(),
                                  None if workspace is None else workspace.data_ptr(), need, handle))
     return out, lse
+
+
+def cache_values(cache, k=None, v=None, stream=None):
+    """The values that an E4M3 or NVFP4 cache stands for: (k, v), bf16 [num_pages, kv_heads, page_size, head_dim]
+    (allocated if not given; NVFP4 values are exact in bf16, E4M3 ones are rounded)."""
+    i = _gpu(cache.k, "the cache")
+    shape = cache.k.shape[:3] + (cache.head_dim,)
+    out = []
+    for t, name in ((k, "k"), (v, "v")):
+        if t is None:
+            t = _empty(shape, _torch.bfloat16, i, stream)
+        else:
+            _need(t, name, _torch.bfloat16, cache.device, shape)
+        out.append(t)
+    _check(lib().ocq_cache_values(cache.ref, out[0].data_ptr(), out[1].data_ptr(), _stream_of(stream, i)))
+    return tuple(out)
 
 
 # ---------------------------------------------------------------- measurement helpers

@@ -1,0 +1,483 @@
+"""NVFP4 caches on the GPU: the append, the values, and attention over them, against plain 64-bit implementations
+written here (codes and scales from the oracle's tables).
+
+Tolerances, fixed before the first run.  Codes and scales are whole: the rotated k is rounded to 32 bits out of 64 on
+both sides, which differ by less than 2^-50, so that a code could differ once in 2^20 or more of these elements; equal is
+asked for.  Attention: q, k and v are exact in the products, probabilities are rounded to fp16, 2^-11 relative, scores
+are fp32 sums of exact products, 2^-20 of their size (at most 2^5 here but where a test says more), which the exponential
+turns into a relative 2^-15 of each weight: |out - ref| <= 2^-8 |ref| (the output's own rounding) + (2^-11 + 2^-14) sum_j
+w_j |v_j|.  Below fp16's normal range a rounding is absolute, 2^-25, of probabilities whose largest is 2^7 at least: 2^-32
+sum_j |v_j| more over the keys that a token sees.  The log-sum-exp as for the other formats.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import formats as F
+from quantized_memory_bound_amd import ocq
+from test_gpu_layer import BATCHES, _bf, _gen, make_batch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+E4M3 = torch.float8_e4m3fn
+GRID = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64)
+
+
+def decoded(codes, scale, unit=1.0):
+    """64-bit values of packed codes [..., n / 2] and scales [..., n / 16]."""
+    c = torch.stack([codes.view(torch.uint8) & 15, codes.view(torch.uint8) >> 4], -1).flatten(-2).long()
+    v = GRID.to(codes.device)[c & 7] * (1 - 2 * (c >> 3)).double()
+    return v * scale.view(E4M3).double().repeat_interleave(16, -1) * unit
+
+
+def quantized(y, unit=1.0):
+    """Codes (one a byte) and scale codes of fp32 rows, on the host from the oracle's tables."""
+    y = y.cpu().numpy().astype(np.float32).reshape(*y.shape[:-1], -1, 16)
+    scale = F.enc_e4m3((np.abs(y).max(-1) / np.float32(6)) / np.float32(unit))
+    s = F.dec_e4m3(scale).astype(np.float32) * np.float32(unit)
+    q = np.divide(y, s[..., None], out=np.zeros_like(y), where=s[..., None] > 0)
+    return F.enc_e2m1(q).reshape(*y.shape[:-2], -1), scale
+
+
+def make_cache(pages, kv_heads, page_size, dim, gen, order="heads", units=(1.0, 1.0)):
+    """A cache of random codes whose values are of order one, axes [pages, heads, tokens] or [pages, tokens, heads]."""
+    def pool(n, low, high):
+        s = (pages, kv_heads, page_size, n) if order == "heads" else (pages, page_size, kv_heads, n)
+        x = torch.randint(low, high, s, dtype=torch.uint8, device=DEV, generator=gen)
+        return x if order == "heads" else x.transpose(1, 2)
+    k, v = pool(dim // 2, 0, 256), pool(dim // 2, 0, 256)
+    ks, vs = pool(dim // 16, 0x20, 0x38), pool(dim // 16, 0x20, 0x38)      # 2^-3 .. 1
+    return ocq.PagedKVCache(k, v, ks.view(E4M3), vs.view(E4M3), k_unit=units[0], v_unit=units[1])
+
+
+def rows_of(cache, which, table, j):
+    """The values of places j of a request, [places, kv_heads, dim] in 64 bits; zeros where there is no page."""
+    codes, scale = (cache.k, cache.k_scale) if which == "k" else (cache.v, cache.v_scale)
+    unit = cache.k_unit if which == "k" else cache.v_unit
+    ids = table[j // cache.page_size].long()
+    ok = (ids >= 0) & (ids < codes.shape[0])
+    ids = ids.clamp(0, codes.shape[0] - 1)
+    x = decoded(codes[ids, :, j % cache.page_size], scale.view(torch.uint8)[ids, :, j % cache.page_size], unit)
+    return torch.where(ok[:, None, None], x, torch.zeros_like(x))
+
+
+def attention_ref(q, cache, batch, news, kvs, scale, window, sinks):
+    out, lse, mag, at = [], [], [], 0
+    group = q.shape[1] // cache.kv_heads
+    for r, (n, kv) in enumerate(zip(news, kvs)):
+        if n == 0:
+            continue
+        qq = q[at: at + n].double()
+        at += n
+        j = torch.arange(kv, device=DEV)
+        p = torch.arange(kv - n, kv, device=DEV)
+        k, v = (rows_of(cache, w, batch.page_table[r], j) for w in ("k", "v"))
+        seen = j[None] <= p[:, None]
+        if window:
+            seen = seen & ((j[None] > p[:, None] - window) | (j[None] < sinks))
+        kh, vh = (x.repeat_interleave(group, 1).permute(1, 0, 2).contiguous() for x in (k, v))
+        s = torch.matmul(qq.transpose(0, 1).contiguous(), kh.transpose(1, 2).contiguous()) * scale
+        s = s.masked_fill(~seen[None], -math.inf)
+        w = torch.softmax(s, -1) if kv else s
+        w = torch.where(seen[None].any(-1, keepdim=True), w, torch.zeros_like(w))
+        out.append(torch.matmul(w, vh).transpose(0, 1))
+        seen = seen[None].expand(len(w), -1, -1).double()
+        mag.append(torch.stack([torch.matmul(x, vh.abs()) for x in (w, seen)]).transpose(1, 2))
+        lse.append((torch.logsumexp(s, -1) if kv else
+                    torch.full(s.shape[:2], -math.inf, device=DEV, dtype=torch.float64)).transpose(0, 1))
+    return torch.cat(out), torch.cat(lse), torch.cat(mag, 1)
+
+
+def check_attention(q, cache, batch, news, kvs, scale=None, window=0, sinks=0, score=2.0 ** 5, **kw):
+    out, lse = ocq.paged_attention(q, cache, batch, scale=scale, window=window, sinks=sinks, want_lse=True, **kw)
+    torch.cuda.synchronize()
+    sc = q.shape[2] ** -0.5 if scale is None else scale
+    ref, rl, mag = attention_ref(q, cache, batch, news, kvs, sc, window, sinks)
+    empty = torch.isinf(rl)
+    assert torch.equal(torch.isinf(lse), empty) and not out[empty].float().any()
+    d = (lse.double() - rl)[~empty].abs()
+    assert not d.numel() or d.max() <= 2.0 ** -18 + rl[~empty].abs().max() * 2.0 ** -18
+    tol = ref.abs() * 2.0 ** -8 + mag[0] * (2.0 ** -11 + score * 2.0 ** -19) + mag[1] * 2.0 ** -32 + 1e-30
+    bad = ~((out.double() - ref).abs() <= tol)
+    assert not bad.any(), "%d of %d off, worst %.3g" % (int(bad.sum()), bad.numel(), float((out.double() - ref).abs().max()))
+    return out, lse
+
+
+# ---------------------------------------------------------------- append and values
+
+@pytest.mark.parametrize("dim,rot", [(64, 64), (64, 16), (128, 128), (128, 48), (128, 64), (256, 256), (256, 112)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("order,page", [("heads", 16), ("tokens", 1), ("tokens", 64)])
+def test_append(dim, rot, interleaved, order, page):
+    g = _gen(dim + rot + page)
+    news, kvs, heads, kv_heads = [3, 1, 0, 40], [70, 1, 9, 61], 6, 3
+    units = (2.0 ** -3, 4.0)
+    batch, pages = make_batch(news, kvs, page, g)
+    cache = make_cache(pages, kv_heads, page, dim, g, order, units)
+    rope = ocq.Rope.make(rot, interleaved=interleaved, device=DEV, scaling="yarn", factor=4.0)
+    qkv = _bf((sum(news), heads + 2 * kv_heads, dim), g, 2.0)
+    q, k, v = qkv.split([heads, kv_heads, kv_heads], 1)
+    v[0, 0, :16] = 0
+    v[1, 1] *= 1e-3
+    v[2, 2] *= 3e4                                                        # past 6 x 448 x 4: saturates
+    positions = torch.randint(0, 1 << 21, (sum(news),), dtype=torch.int32, device=DEV, generator=g)
+    before = [t.clone() for t in (cache.k, cache.v, cache.k_scale.view(torch.uint8), cache.v_scale.view(torch.uint8))]
+    got = ocq.rope_append(q, k, v, rope, cache, batch, positions=positions)
+    torch.cuda.synchronize()
+    # in 64 bits
+    ang = positions.double()[:, None] * rope.inv_freq
+    c, s = (torch.cos(ang) * rope.multiplier)[:, None], (torch.sin(ang) * rope.multiplier)[:, None]
+
+    def turn(x):
+        x = x.double()
+        a, b = (x[..., 0:rot:2], x[..., 1:rot:2]) if interleaved else (x[..., :rot // 2], x[..., rot // 2:rot])
+        a, b = a * c - b * s, b * c + a * s
+        t = torch.stack([a, b], -1).flatten(-2) if interleaved else torch.cat([a, b], -1)
+        return torch.cat([t, x[..., rot:]], -1)
+    ref = turn(q)
+    # sines and cosines in 32 bits, two products and a sum: 2^-22 of the pair's size; then half a step of bf16
+    size = ref.abs().amax() * 2.0 ** -21
+    assert torch.all((got.double() - ref).abs() <= ref.abs() * 2.0 ** -8 + size)
+    at = 0
+    for r, (n, kv) in enumerate(zip(news, kvs)):
+        for i in range(n):
+            place = kv - n + i
+            p, row = int(batch.page_table[r, place // page]), place % page
+            for pool, sc, old, old_s, y, unit in ((cache.k, cache.k_scale, before[0], before[2], turn(k)[at], units[0]),
+                                                  (cache.v, cache.v_scale, before[1], before[3], v[at].double(), units[1])):
+                codes, scales = quantized(y.float(), unit)
+                packed = pool[p, :, row].cpu().numpy()
+                mine = np.stack([packed & 15, packed >> 4], -1).reshape(codes.shape)
+                # (-0 and 0 are one value)
+                assert np.array_equal(np.where(mine == 8, 0, mine), np.where(codes == 8, 0, codes)), (r, i)
+                assert np.array_equal(sc.view(torch.uint8)[p, :, row].cpu().numpy(), scales), (r, i)
+                old[p, :, row], old_s[p, :, row] = pool[p, :, row], sc.view(torch.uint8)[p, :, row]
+            at += 1
+    for t, old in zip((cache.k, cache.v, cache.k_scale.view(torch.uint8), cache.v_scale.view(torch.uint8)), before):
+        assert torch.equal(t, old)                                        # nothing else was written
+
+
+def test_append_codes_at_every_border():
+    """Blocks whose scale is known (their largest value is 6 s) with values on, just below and just above every
+    border between two codes, of both signs and many scales."""
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 0.0])
+    rows = []
+    for e in range(-9, 9):
+        for m in (1.0, 1.25, 1.75):
+            s = 2.0 ** e * m
+            if s > 448 or not float(torch.tensor(s).to(E4M3)) == s:
+                continue
+            for sign in (1, -1):
+                for step in (-1, 0, 1):
+                    x = (mids * s * sign).to(torch.bfloat16)
+                    x = (x.view(torch.int16) + (step if step == 0 else step * (x != 0).to(torch.int16))).view(torch.bfloat16)
+                    rows.append(torch.cat([torch.tensor([6 * s, -6 * s]).to(torch.bfloat16), x]))
+    rows = torch.stack(rows)
+    rows = rows[: len(rows) // 4 * 4].reshape(-1, 1, 64).to(DEV)
+    n = len(rows)
+    batch, pages = make_batch([n], [n], 64, _gen(1))
+    cache = ocq.PagedKVCache.allocate(pages, 64, 1, 64, nvfp4=True, device=DEV)
+    rope = ocq.Rope(torch.zeros(32, dtype=torch.float64, device=DEV))     # no turn: k' = k
+    ocq.rope_append(rows, rows, rows, rope, cache, batch)
+    j = torch.arange(n, device=DEV)
+    codes, scales = quantized(rows[:, 0].float())
+    for pool, sc in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        packed = pool[batch.page_table[0][j // 64].long(), 0, j % 64].cpu().numpy()
+        mine = np.stack([packed & 15, packed >> 4], -1).reshape(codes.shape)
+        assert np.array_equal(np.where(mine == 8, 0, mine), np.where(codes == 8, 0, codes))
+        assert np.array_equal(sc.view(torch.uint8)[batch.page_table[0][j // 64].long(), 0, j % 64].cpu().numpy(), scales)
+
+
+def test_append_of_values_that_are_not_finite():
+    """Their 16 elements get scale NaN and codes 0, which the values and attention show; the others are as ever."""
+    g = _gen(3)
+    batch, pages = make_batch([4], [4], 16, g)
+    cache = ocq.PagedKVCache.allocate(pages, 16, 1, 64, nvfp4=True, device=DEV)
+    rope = ocq.Rope(torch.zeros(32, dtype=torch.float64, device=DEV))
+    x = _bf((4, 1, 64), g)
+    k, v = x.clone(), x.clone()
+    v[1, 0, 20], v[2, 0, 63], k[3, 0, 0] = float("nan"), float("inf"), float("-inf")
+    ocq.rope_append(x, k, v, rope, cache, batch)
+    kk, vv = (t[int(batch.page_table[0, 0]), 0, :4].float() for t in ocq.cache_values(cache))
+    want = torch.zeros((4, 64), dtype=torch.bool, device=DEV)
+    want[1, 16:32], want[2, 48:] = True, True
+    assert torch.equal(torch.isnan(vv), want)
+    # (without a turn the other half of the pair is inf * 0: both blocks)
+    assert torch.isnan(kk[3, :16]).all() and torch.isfinite(kk[:3]).all() and torch.isfinite(kk[3, 48:]).all()
+    # tokens that see such values show them; one that does not may too (0 x NaN), in those elements alone
+    out, _ = ocq.paged_attention(x, cache, batch)
+    assert torch.isnan(out[1:, 0, 16:32].float()).all() and torch.isfinite(out[:3, 0, :16].float()).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("order", ["heads", "tokens"])
+def test_values(dim, order):
+    g = _gen(dim)
+    cache = make_cache(5, 3, 16, dim, g, order, (2.0 ** -7, 8.0))
+    cache.k_scale.view(torch.uint8)[1, 0, 0, 0] = 0x7F
+    k, v = ocq.cache_values(cache)
+    ref = decoded(cache.k, cache.k_scale.view(torch.uint8), 2.0 ** -7)
+    assert torch.equal(torch.isnan(k.double()), torch.isnan(ref))
+    ok = ~torch.isnan(ref)
+    assert torch.equal(k.double()[ok], ref[ok])
+    assert torch.equal(v.double(), decoded(cache.v, cache.v_scale.view(torch.uint8), 8.0))
+    out = torch.empty((2, 5, 3, 16, dim), dtype=torch.bfloat16, device=DEV)
+    a, b = ocq.cache_values(cache, k=out[0], v=out[1])
+    assert a.data_ptr() == out.data_ptr() and torch.equal(b, v)
+    codes = [(torch.randn((5, 3, 16, dim), device=DEV, generator=g) * 100).to(E4M3) for _ in range(2)]
+    scales = [torch.rand((5, 3, 16), device=DEV, generator=g) for _ in range(2)]
+    for got, c, s in zip(ocq.cache_values(ocq.PagedKVCache(*codes, *scales)), codes, scales):
+        ref = c.float() * s[..., None]                                    # one product, rounded twice
+        assert torch.equal(torch.isnan(got), torch.isnan(ref))            # codes past 448 are NaN
+        assert torch.equal(got.nan_to_num(), ref.to(torch.bfloat16).nan_to_num())
+
+
+# ---------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,kv_heads", [(1, 3), (4, 2), (5, 1), (16, 1)])
+@pytest.mark.parametrize("news,kvs", BATCHES)
+def test_attention(dim, group, kv_heads, news, kvs):
+    g = _gen(dim * group + len(news))
+    page = {64: 16, 128: 32, 256: 1}[dim]
+    batch, pages = make_batch(news, kvs, page, g, table_pad=1)
+    cache = make_cache(pages, kv_heads, page, dim, g, "heads" if group % 2 else "tokens", (0.5, 2.0 ** 9))
+    q = _bf((sum(news), group * kv_heads, dim), g)
+    check_attention(q, cache, batch, news, kvs)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (16, 0), (100, 1), (100, 130), (333, 4), (5000, 8)])
+def test_attention_window_and_sinks(window, sinks):
+    g = _gen(window + sinks)
+    news, kvs = [1, 13, 90, 300], [2500, 1313, 1000, 300]
+    for dim, page in ((64, 64), (128, 16)):
+        batch, pages = make_batch(news, kvs, page, g)
+        cache = make_cache(pages, 2, page, dim, g)
+        check_attention(_bf((sum(news), 8, dim), g), cache, batch, news, kvs, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dim,news,kvs", [(128, [1, 1], [40001, 777]), (64, [13, 13], [20011, 31]), (256, [2], [9001]),
+                                          (128, [700], [4099]), (64, [513, 1], [513, 5001]), (256, [129], [3001])])
+def test_attention_long(dim, news, kvs):
+    g = _gen(kvs[0])
+    batch, pages = make_batch(news, kvs, 64, g)
+    cache = make_cache(pages, 2, 64, dim, g)
+    check_attention(_bf((sum(news), 8, dim), g), cache, batch, news, kvs)
+
+
+@pytest.mark.parametrize("n,group", [(1, 4), (5, 5), (13, 4), (3, 40)])
+@pytest.mark.parametrize("kv", [511, 512, 513, 640, 1024, 1025, 4097])
+def test_attention_cut_contexts(n, group, kv):
+    """Contexts around whole numbers of tiles and pieces, for each kernel by the rows of a request."""
+    g = _gen(kv + n)
+    news, kvs = [n, n, n], [kv, kv // 3 + n, n]
+    for dim in (64, 128):
+        batch, pages = make_batch(news, kvs, 32, g)
+        cache = make_cache(pages, 1, 32, dim, g)
+        check_attention(_bf((sum(news), group, dim), g), cache, batch, news, kvs)
+        assert not batch.counters.any()
+
+
+@pytest.mark.parametrize("requests,new", [(64, 13), (65, 1), (300, 5)])
+def test_attention_many_requests(requests, new):
+    rng = np.random.default_rng(requests + new)
+    news = [int(x) for x in rng.integers(0, new + 1, requests)]
+    news[0] = new
+    kvs = [n + int(x) for n, x in zip(news, rng.integers(0, 90, requests))]
+    kvs[1], kvs[-1] = news[1] + 3000, news[-1] + 5000
+    g = _gen(requests)
+    batch, pages = make_batch(news, kvs, 16, g)
+    cache = make_cache(pages, 2, 16, 64, g)
+    check_attention(_bf((sum(news), 8, 64), g), cache, batch, news, kvs)
+
+
+def test_attention_over_many_pages_call_after_call():
+    """Many pieces and stages over one workspace: every further call the same bits."""
+    g = _gen(9)
+    news, kvs = [13] * 8, [6000 - 37 * r for r in range(8)]
+    batch, pages = make_batch(news, kvs, 32, g)
+    cache = make_cache(pages, 4, 32, 128, g)
+    q = _bf((13 * 8, 16, 128), g)
+    out, lse = check_attention(q, cache, batch, news, kvs)
+    for _ in range(40):
+        a, b = ocq.paged_attention(q, cache, batch, want_lse=True)
+        assert torch.equal(a, out) and torch.equal(b, lse)
+
+
+def test_attention_rows_that_see_nothing():
+    g = _gen(18)
+    for news, kvs in (([3, 5, 1, 2], [0, 2, 0, 900]), ([70, 9], [64, 0]), ([13, 13], [6, 2000])):
+        batch, pages = make_batch(news, kvs, 16, g)
+        cache = make_cache(pages, 2, 16, 128, g)
+        out, lse = check_attention(_bf((sum(news), 8, 128), g), cache, batch, news, kvs)
+        assert torch.isinf(lse).any()
+
+
+@pytest.mark.parametrize("n", [1, 13, 70])
+def test_attention_scores_and_rows_of_every_size(n):
+    """Large scores, a moving maximum, scores far below zero, equal keys; rows of q far from one, with values 2^60 apart
+    and rows of zeros."""
+    g = _gen(n)
+    kv = 900
+    batch, pages = make_batch([n], [kv], 16, g)
+    cache = make_cache(pages, 1, 16, 64, g)
+    q = _bf((n, 4, 64), g)
+    for scale in (1e-4, 1.0, 8.0):
+        check_attention(q, cache, batch, [n], [kv], scale=scale, score=2.0 ** 5 * max(1.0, 8 * scale))
+    wide = q.clone()
+    wide[:, 0] *= 2.0 ** 40
+    wide[:, 1] *= 2.0 ** -100
+    wide[:, 2, ::3] *= 2.0 ** -60
+    wide[:, 3] = 0
+    check_attention(wide[:, 1:], ocq.PagedKVCache(cache.k, cache.v, cache.k_scale, cache.v_scale), batch, [n], [kv])
+    small = wide.clone()
+    check_attention(small[:, :1], cache, batch, [n], [kv], scale=2.0 ** -43)
+    # every key's score below or above the one after it
+    places = torch.arange(kv, device=DEV)
+    ids = batch.page_table[0][places // 16].long()
+    q[:] = 1
+    cache.k[:] = 0x22                                                      # ones
+    step = (places // 64 + 1).float().to(E4M3).view(torch.uint8)          # scales 1 .. 15
+    for order in (step, step.flip(0)):
+        cache.k_scale.view(torch.uint8)[ids, 0, places % 16] = order[:, None].expand(-1, 4)
+        for sign in (1, -1):
+            check_attention(q * sign, cache, batch, [n], [kv], scale=0.25, score=2.0 ** 8)
+
+
+def test_attention_what_no_token_sees_does_not_reach_it():
+    """NaN scales past the context in used pages and in unused pages, and behind a window, where pages are gone too."""
+    g = _gen(11)
+    for n in (1, 13, 40):
+        news, kvs = [n, n], [n + 37, n + 5]
+        batch, pages = make_batch(news, kvs, 64, g)
+        cache = make_cache(pages, 2, 64, 128, g)
+        used = torch.zeros((pages, 64), dtype=torch.bool, device=DEV)
+        for r, kv in enumerate(kvs):
+            p = torch.arange(kv, device=DEV)
+            used[batch.page_table[r][p // 64].long(), p % 64] = True
+        spoil = ~used[:, None, :].expand(-1, 2, -1)
+        cache.k_scale.view(torch.uint8)[spoil] = 0x7F
+        cache.v_scale.view(torch.uint8)[spoil] = 0x7F
+        check_attention(_bf((2 * n, 8, 128), g), cache, batch, news, kvs)
+    for n, kv, window, sinks in ((1, 1000, 100, 3), (13, 700, 64, 0), (3, 2000, 333, 17), (1, 90, 7, 70)):
+        batch, pages = make_batch([n], [kv], 16, g)
+        cache = make_cache(pages, 2, 16, 128, g)
+        p = torch.arange(sinks, kv - n - window + 1, device=DEV)
+        ids = batch.page_table[0][p // 16].long()
+        cache.k_scale.view(torch.uint8)[ids, :, p % 16] = 0x7F
+        cache.v_scale.view(torch.uint8)[ids, :, p % 16] = 0x7F
+        full = torch.arange(max(1, -(-sinks // 16)), (kv - n - window + 1) // 16, device=DEV)
+        q = _bf((n, 8, 128), g)
+        out, lse = ocq.paged_attention(q, cache, batch, window=window, sinks=sinks, want_lse=True)
+        batch.page_table[0, full] = -1
+        again = ocq.paged_attention(q, cache, batch, window=window, sinks=sinks, want_lse=True)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+        cache.k_scale.view(torch.uint8)[ids, :, p % 16] = 0
+        cache.v_scale.view(torch.uint8)[ids, :, p % 16] = 0
+        a, b = check_attention(q, cache, batch, [n], [kv], window=window, sinks=sinks)
+        assert torch.equal(out, a) and torch.equal(lse, b)
+
+
+def test_attention_pages_that_are_none_read_as_zeros():
+    g = _gen(12)
+    news, kvs = [3, 20], [200, 300]
+    for dim in (64, 128, 256):
+        batch, pages = make_batch(news, kvs, 16, g)
+        cache = make_cache(pages, 2, 16, dim, g)
+        batch.page_table[0, 2], batch.page_table[1, 0], batch.page_table[1, 7] = -1, pages, 2 ** 31 - 1
+        check_attention(_bf((23, 4, dim), g), cache, batch, news, kvs)
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 bytes of codes whose used pages lie at its end."""
+    g = _gen(14)
+    pages = (1 << 32) // (64 * 128) + 40
+    k = torch.zeros((pages, 1, 64, 128), dtype=torch.uint8, device=DEV)
+    ks = torch.zeros((pages, 1, 64, 16), dtype=torch.uint8, device=DEV)
+    tail = make_cache(20, 1, 64, 256, g)
+    k[-20:], ks[-20:] = tail.k, tail.k_scale.view(torch.uint8)
+    cache = ocq.PagedKVCache(k, k.clone(), ks.view(E4M3), ks.clone().view(E4M3))
+    kvs = [1200]
+    table = (pages - 1 - torch.arange(19, device=DEV)).to(torch.int32)[None]
+    batch = ocq.TokenBatch(torch.tensor([0, 2], dtype=torch.int32, device=DEV),
+                           torch.tensor(kvs, dtype=torch.int32, device=DEV), table, 2, 1200)
+    q, nk, nv = _bf((2, 4, 256), g), _bf((2, 1, 256), g), _bf((2, 1, 256), g)
+    q = ocq.rope_append(q, nk, nv, ocq.Rope.make(256, device=DEV), cache, batch)
+    codes, _ = quantized(nv[:, 0].float())
+    packed = cache.v[int(table[0, 18]), 0, 1198 % 64: 1200 % 64].cpu().numpy()
+    assert np.array_equal(np.stack([packed & 15, packed >> 4], -1).reshape(codes.shape) & 7, codes & 7)
+    check_attention(q, cache, batch, [2], kvs)
+
+
+def test_views_streams_and_given_outputs():
+    g = _gen(13)
+    news, kvs = [13, 2], [500, 90]
+    batch, pages = make_batch(news, kvs, 32, g)
+    cache = make_cache(pages, 2, 32, 128, g, "tokens")
+    q = _bf((15, 8 + 4, 128), g)[:, 2:10]
+    want, wl = check_attention(q, cache, batch, news, kvs)
+    ws = torch.full((max(ocq.attention_workspace_bytes(8, cache, batch), 16),), 0xFF, dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        a, b = ocq.paged_attention(q, cache, batch, want_lse=True, workspace=ws, stream=side)
+        side.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, wl)
+    k, v = ocq.cache_values(cache, stream=side)
+    side.synchronize()
+    a, b = ocq.cache_values(cache)
+    assert torch.equal(a, k) and torch.equal(b, v)
+
+
+def test_captured_step_replays():
+    """The append, attention and the values in a graph: the device arrays change between replays."""
+    g = _gen(15)
+    n, heads = 5, 8
+    batch, pages = make_batch([n, n], [2000, 900], 64, g)
+    cache = make_cache(pages, 2, 64, 128, g)
+    rope = ocq.Rope.make(128, device=DEV)
+    q, k, v = _bf((2 * n, heads, 128), g), _bf((2 * n, 2, 128), g), _bf((2 * n, 2, 128), g)
+
+    def step():
+        r = ocq.rope_append(q, k, v, rope, cache, batch)
+        return ocq.paged_attention(r, cache, batch, want_lse=True) + ocq.cache_values(cache)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for i in range(4):
+        q.copy_(_bf(q.shape, g))
+        k.copy_(_bf(k.shape, g))
+        batch.kv_lens.copy_(torch.tensor([1500 + i, 600 + 7 * i], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in outs]
+        for a, b in zip(got, step()):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_binding_refusals():
+    g = _gen(16)
+    c = make_cache(4, 2, 16, 64, g)
+    ks, vs = c.k_scale, c.v_scale
+    wide = torch.zeros((4, 2, 16, 6), dtype=torch.uint8, device=DEV)
+    for call in (lambda: ocq.PagedKVCache(c.k, c.v, ks), lambda: ocq.PagedKVCache(c.k, c.v, ks, vs[:, :, :, :2]),
+                 lambda: ocq.PagedKVCache(c.k, c.v, ks.float(), vs.float()), lambda: ocq.PagedKVCache(c.k, c.v[:2], ks, vs),
+                 lambda: ocq.PagedKVCache(c.k.view(torch.int8), c.v.view(torch.int8), ks, vs),
+                 lambda: ocq.PagedKVCache.allocate(4, 16, 2, 64, e4m3=True, nvfp4=True),
+                 lambda: ocq.PagedKVCache(_bf((4, 2, 16, 64), g), _bf((4, 2, 16, 64), g), k_unit=2.0),
+                 lambda: ocq.cache_values(ocq.PagedKVCache.allocate(4, 16, 2, 64)),
+                 lambda: ocq.cache_values(c, k=torch.empty((4, 2, 16, 32), dtype=torch.bfloat16, device=DEV)),
+                 lambda: ocq.cache_values(ocq.PagedKVCache(c.k, c.v, ks, vs, k_unit=3.0)),
+                 lambda: ocq.cache_values(ocq.PagedKVCache(c.k, c.v, wide[..., 1:5], wide[..., 1:5])),
+                 lambda: ocq.cache_values(ocq.PagedKVCache(c.k, c.v, ks, vs, v_unit=0.0))):
+        with pytest.raises(ocq.OcqError) as e:
+            call()
+        assert e.value.status in (ocq.ERR_INVALID_ARG, ocq.ERR_UNSUPPORTED)
