@@ -491,6 +491,88 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
  * head_dim] contiguous (NVFP4 values are exact in bf16, E4M3 ones are rounded). */
 ocq_status ocq_cache_values(const ocq_kv_cache* cache, void* k_out_dev, void* v_out_dev, void* stream);
 
+/* Which drafted tokens of a verify pass stay, and the token that follows them
+ * ("Generate more tokens per target pass" in the post: the target checks every
+ * draft at once and keeps those that it accepts).
+ * Request r of the batch has rows t0 = q_start[r] .. q_start[r + 1] - 1, n of them:
+ * tokens[t0] and its n - 1 drafts; row t of the target is the distribution p of the
+ * token after tokens[t]: logits l with p = softmax(l / T) (T = 0: 1 at the largest
+ * logit, the first of several), or with probabilities 1 p itself.  Draft i is
+ * tokens[t0 + i + 1], drawn from q, row i of the request's draft rows (n - 1 a
+ * request, side by side in the order of the requests); draft_dev NULL: q is 1 at
+ * the draft (found by lookup or greedily).  The draft stays while
+ *   u_accept[t0 + i] q(x) < p(x)
+ * and all before it do.  At the first that does not, the next token is drawn from w
+ * = max(p - q, 0) (p where that is 0 throughout), after the last one from w = p: the
+ * lowest j with sum_{i <= j} w_i > u_next[r] sum_i w_i.  Sums and exponentials of
+ * that row are 64-bit; the normalization of an acceptance's p is within 2^-20.
+ *   accepted[r]            drafts that stay (0 for a request without tokens)
+ *   out[t0 .. t0 + n - 1]  those drafts, the next token, then -1; -1 too in rows
+ *                          behind the last request
+ * A next token of -1 says that the row has none: no weight above 0, or values that
+ * are not numbers (at T > 0 also +inf).  Logits of -inf rule tokens out.  A draft
+ * outside [0, vocab) is not accepted.
+ * target_dev: fp32 (target_bf16 0) or bf16 [tokens, vocab], rows target_stride
+ * elements apart, at any alignment of the type, vocab in [1, 2^24]; draft_dev
+ * likewise, draft_rows rows.  tokens_dev int32 [tokens], u_accept_dev float
+ * [tokens] and u_next_dev float [requests], numbers in [0, 1); temperature_dev float
+ * [requests], or NULL: temperature for all (neither is read with probabilities 1).
+ * accepted_dev int32 [requests], out_dev int32 [tokens].  Of the batch q_start,
+ * requests (up to OCQ_ATTENTION_COUNTERS), tokens (up to 2^20) and the counters are
+ * used, the counters as attention uses them.
+ * workspace_dev: ocq_verify_drafts_workspace_bytes(...) bytes, contents need not be
+ * initialized; calls that share it must be ordered on one stream. */
+size_t ocq_verify_drafts_workspace_bytes(const ocq_token_batch* batch, int vocab, int probabilities);
+ocq_status ocq_verify_drafts(const void* target_dev, int64_t target_stride, int target_bf16, int probabilities,
+                             const void* draft_dev, int64_t draft_stride, int64_t draft_rows, int draft_bf16,
+                             const void* tokens_dev, const void* u_accept_dev, const void* u_next_dev,
+                             const void* temperature_dev, float temperature, int vocab, const ocq_token_batch* batch,
+                             void* accepted_dev, void* out_dev, void* workspace_dev, size_t workspace_bytes,
+                             void* stream);
+
+/* What a server keeps of its requests between steps, on the GPU: the arrays of an
+ * ocq_token_batch, the pages that each request holds, and the free pages.
+ * q_start_dev int32 [requests + 1], kv_lens_dev int32 [requests], page_table_dev
+ * int32 [requests, max_pages] with row stride table_stride as in a batch; held_dev
+ * int32 [requests]: the entries of a request's row that are its pages; ring_dev
+ * int32 [ring_size]: page ids, free ones at places counts[0] .. counts[1] - 1 modulo
+ * ring_size; counts_dev int64 [2]: entries ever taken out and put in.  ring_size is
+ * at least the number of pages in all.  page_size a power of two up to 1024,
+ * max_pages * page_size below 2^31, up to 65536 requests. */
+typedef struct {
+  void* q_start_dev;
+  void* kv_lens_dev;
+  void* held_dev;
+  void* counts_dev;
+  void* page_table_dev;
+  void* ring_dev;
+  int64_t table_stride;
+  int requests, max_pages, ring_size, page_size;
+} ocq_page_tables;
+
+/* The tables of the next step.  Of request r's n tokens of the step before (its
+ * share of before's q_start) 1 + accepted[r] stay, at most n (accepted_dev NULL:
+ * all), and news[r] tokens come (news[r] < 0: the request has ended, keeps nothing
+ * and brings nothing):
+ *   kv_lens' = kv_lens - n + min(n, 1 + accepted) + news;  q_start' sums news
+ *   held' = ceil(kv_lens' / page_size): what it lacks comes from the ring, in the
+ *     order of the requests, what it no longer needs goes back there (and can be
+ *     taken in the next call; its entries stay in the table, unused)
+ * Where the ring has too few pages, or max_pages is too small, missing[0] counts
+ * those that lack, their entries in the table are -1 and held' counts the others:
+ * appended tokens without a page are dropped, and the next call tries again.
+ * Per new token, in the order of the token axis (tokens rows, at least the sum of
+ * news; -1 in rows behind it): slots int64 (page * page_size + row in the page, -1
+ * without a page), positions int32 (its place in the request), requests int32; each
+ * and missing nullable.
+ * before and after may be the same; they share the page table and the ring, which
+ * are changed in place.  No output may overlap news or accepted. */
+size_t ocq_step_tables_workspace_bytes(int requests, int tokens);
+ocq_status ocq_step_tables(const ocq_page_tables* before, const ocq_page_tables* after, const void* news_dev,
+                           const void* accepted_dev, int tokens, void* slots_dev, void* positions_dev,
+                           void* requests_dev, void* missing_dev, void* workspace_dev, size_t workspace_bytes,
+                           void* stream);
+
 /* Message for the last failure on this thread ("" if none). */
 const char* ocq_last_error(void);
 

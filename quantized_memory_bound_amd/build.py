@@ -26,7 +26,8 @@ BUILD_PHASES = os.path.join(HERE, "_build_phases")
 LIB_PHASES = os.path.join(HERE, "libocq_phases.so")
 
 SOURCES = ["api.cpp", "pack.cpp", "kernels.hip", "gemm_gateup.hip", "gemm_down.hip", "gemm_large.hip", "diag.hip",
-           "noalloc.hip", "layer_api.cpp", "step_api.cpp", "norm.hip", "rope.hip", "attention.hip"]
+           "noalloc.hip", "layer_api.cpp", "step_api.cpp", "norm.hip", "rope.hip", "attention.hip",
+           "drafts.hip", "tables.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

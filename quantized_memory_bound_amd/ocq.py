@@ -34,7 +34,8 @@ EXPORTS = ("ocq_version", "ocq_packed_bytes", "ocq_pack_weights_host", "ocq_pack
            "ocq_diag_stream_read", "ocq_diag_window_read", "ocq_diag_mfma_rate", "ocq_diag_empty", "ocq_diag_mfma_dot", "ocq_diag_phase_stamps", "ocq_noalloc_scratch_bytes",
            "ocq_mlp_forward_noalloc", "ocq_set_fused_requant", "ocq_last_requant_in_gateup",
            "ocq_add_rmsnorm", "ocq_rope_frequencies", "ocq_rope_append", "ocq_attention_workspace_bytes",
-           "ocq_paged_attention", "ocq_cache_values")
+           "ocq_paged_attention", "ocq_cache_values", "ocq_verify_drafts_workspace_bytes", "ocq_verify_drafts",
+           "ocq_step_tables_workspace_bytes", "ocq_step_tables")
 
 
 class OcqError(RuntimeError):
@@ -61,6 +62,13 @@ class TokenBatchStruct(ctypes.Structure):
                 [("table_stride", ctypes.c_int64)] +
                 [(n, ctypes.c_int) for n in ("requests", "tokens", "max_pages", "max_new", "max_kv")] +
                 [("counters_dev", ctypes.c_void_p)])
+
+
+class PageTablesStruct(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q_start_dev", "kv_lens_dev", "held_dev", "counts_dev",
+                                                "page_table_dev", "ring_dev")] +
+                [("table_stride", ctypes.c_int64)] +
+                [(n, ctypes.c_int) for n in ("requests", "max_pages", "ring_size", "page_size")])
 
 
 _lib = None
@@ -122,6 +130,12 @@ def lib():
     L.ocq_paged_attention.argtypes = [vp, i64, i64, i, cp, bp, f, i, i, vp, vp, vp, sz, vp]
     L.ocq_paged_attention.restype = i
     L.ocq_cache_values.argtypes, L.ocq_cache_values.restype = [cp, vp, vp, vp], i
+    L.ocq_verify_drafts_workspace_bytes.argtypes, L.ocq_verify_drafts_workspace_bytes.restype = [bp, i, i], sz
+    L.ocq_verify_drafts.argtypes = [vp, i64, i, i, vp, i64, i64, i, vp, vp, vp, vp, f, i, bp, vp, vp, vp, sz, vp]
+    L.ocq_verify_drafts.restype = i
+    tp = ctypes.POINTER(PageTablesStruct)
+    L.ocq_step_tables_workspace_bytes.argtypes, L.ocq_step_tables_workspace_bytes.restype = [i, i], sz
+    L.ocq_step_tables.argtypes, L.ocq_step_tables.restype = [tp, tp, vp, vp, i, vp, vp, vp, vp, vp, sz, vp], i
     _lib = L
     return L
 
@@ -797,6 +811,164 @@ def cache_values(cache, k=None, v=None, stream=None):
         out.append(t)
     _check(lib().ocq_cache_values(cache.ref, out[0].data_ptr(), out[1].data_ptr(), _stream_of(stream, i)))
     return tuple(out)
+
+
+# ---------------------------------------------------------------- between two verify steps
+
+def _row_matrix(t, name, index, rows, cols):
+    """(pointer, row stride, is bf16) of a float32 or bf16 matrix with `rows` rows or more, its last axis contiguous."""
+    if t is None or not hasattr(t, "get_device") or t.get_device() != index or t.dim() != 2 or \
+            t.dtype not in (_torch.float32, _torch.bfloat16):
+        raise OcqError(ERR_INVALID_ARG, "%s must be a float32 or bfloat16 matrix on cuda:%d" % (name, index))
+    if t.shape[0] < rows or t.shape[1] != cols or (t.stride(1) != 1 and cols > 1):
+        raise OcqError(ERR_INVALID_ARG, "%s must be [%d, %d], its last axis contiguous, got %s with strides %s" %
+                       (name, rows, cols, tuple(t.shape), t.stride()))
+    return t.data_ptr(), t.stride(0), int(t.dtype == _torch.bfloat16)
+
+
+def verify_drafts(target, tokens, batch, u_accept, u_next, draft_probs=None, temperature=1.0, probabilities=False,
+                  accepted=None, out=None, workspace=None, stream=None):
+    """Which drafted tokens of a verify pass stay and the token that follows them: (accepted int32 [requests], out int32
+    [tokens]), out holding each request's accepted drafts, the next token and -1 (see ocq_verify_drafts).
+
+    target: float32 or bf16 [tokens, vocab], the logits after each of the batch's tokens, or with probabilities=True
+    their probabilities; tokens: int32 [tokens], each request's last token and its drafts; u_accept float32 [tokens],
+    u_next float32 [requests]: random numbers in [0, 1).  draft_probs: float32 or bf16 [drafts, vocab], what each draft
+    was drawn from, in the order of the requests (tokens - requests rows where each has one); None where drafts were
+    not drawn.  temperature: a number or float32 [requests], 0 for greedy requests.  A next token of -1: the row has
+    no token to draw.
+    """
+    i = _gpu(target, "target")
+    if target.dim() != 2:
+        raise OcqError(ERR_INVALID_ARG, "target must be [tokens, vocab], got %s" % (tuple(target.shape),))
+    rows, vocab = target.shape
+    ref, L, handle = batch.of(rows), lib(), _stream_of(stream, i)
+    _on(i, batch)
+    if vocab > _INT_MAX:
+        raise OcqError(ERR_INVALID_ARG, "vocab is %d, beyond 32 bits" % vocab)
+    requests, dev = batch.requests, target.device
+    t, t_stride, t_bf16 = _row_matrix(target, "target", i, rows, vocab)
+    d = d_stride = d_rows = d_bf16 = 0
+    if draft_probs is not None:
+        d, d_stride, d_bf16 = _row_matrix(draft_probs, "draft_probs", i, max(0, rows - requests), vocab)
+        d_rows = draft_probs.shape[0]
+        if d_rows == 0:
+            d = t                                   # no drafts: not read, but not a missing q either
+    _need(tokens, "tokens", _torch.int32, dev, (rows,))
+    _need(u_accept, "u_accept", _torch.float32, dev, (rows,))
+    _need(u_next, "u_next", _torch.float32, dev, (requests,))
+    temps, temp = None, 1.0
+    if hasattr(temperature, "data_ptr"):
+        _need(temperature, "temperature", _torch.float32, dev, (requests,))
+        temps = temperature.data_ptr()
+    else:
+        temp = float(temperature)
+    if accepted is None:
+        accepted = _empty(requests, _torch.int32, i, stream)
+    else:
+        _need(accepted, "accepted", _torch.int32, dev, (requests,))
+    if out is None:
+        out = _empty(rows, _torch.int32, i, stream)
+    else:
+        _need(out, "out", _torch.int32, dev, (rows,))
+    if handle != batch.stream:
+        batch.move_to(handle)
+    if workspace is None:
+        need = L.ocq_verify_drafts_workspace_bytes(ref, vocab, int(bool(probabilities)))
+        workspace = _empty(max(need, 16), _torch.uint8, i, stream)
+    else:
+        _need(workspace, "workspace", _torch.uint8, dev)
+    _check(L.ocq_verify_drafts(t, t_stride, t_bf16, int(bool(probabilities)), d or None, d_stride, d_rows, d_bf16,
+                               tokens.data_ptr(), u_accept.data_ptr(), u_next.data_ptr(), temps, temp, vocab, ref,
+                               accepted.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.numel(), handle))
+    return accepted, out
+
+
+class PageTables:
+    """What a server keeps of its requests between steps: q_start int32 [requests + 1], kv_lens and held int32
+    [requests] (cached tokens, pages in hand), page_table int32 [requests, max_pages], and the free pages: ring int32
+    [at least the number of pages], whose entries counts[0] .. counts[1] - 1 (int64 [2], modulo its size) are free.
+
+    CUDA tensors; a TokenBatch over q_start, kv_lens and page_table sees each step's tables.
+    """
+
+    def __init__(self, q_start, kv_lens, held, counts, page_table, ring, page_size):
+        import torch
+        self.index = _gpu(kv_lens, "kv_lens")
+        dev = kv_lens.device
+        requests = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+        _need(kv_lens, "kv_lens", torch.int32, dev, shape=(requests,))
+        _need(q_start, "q_start", torch.int32, dev, shape=(requests + 1,))
+        _need(held, "held", torch.int32, dev, shape=(requests,))
+        _need(counts, "counts", torch.int64, dev, shape=(2,))
+        _need(ring, "ring", torch.int32, dev, min_numel=1)
+        if not hasattr(page_table, "data_ptr") or page_table.dtype != torch.int32 or page_table.device != dev or \
+                page_table.dim() != 2 or page_table.shape[0] != requests or \
+                (page_table.shape[1] > 1 and page_table.stride(1) != 1) or \
+                (requests > 1 and page_table.stride(0) < page_table.shape[1]):
+            raise OcqError(ERR_INVALID_ARG, "page_table must be int32 [%d, max_pages], its rows contiguous and apart" %
+                           requests)
+        self.q_start, self.kv_lens, self.held, self.counts = q_start, kv_lens, held, counts
+        self.page_table, self.ring, self.page_size, self.device = page_table, ring, int(page_size), dev
+        self.requests = requests
+        stride = page_table.stride(0) if requests > 1 else max(page_table.stride(0), page_table.shape[1])
+        self.struct = PageTablesStruct(q_start.data_ptr(), kv_lens.data_ptr(), held.data_ptr(), counts.data_ptr(),
+                                       page_table.data_ptr(), ring.data_ptr(), stride, _int32(requests, "requests"),
+                                       _int32(page_table.shape[1], "max_pages"), _int32(ring.numel(), "ring"),
+                                       _int32(page_size, "page_size"))
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def allocate(cls, requests, max_pages, num_pages, page_size, device="cuda"):
+        """Empty requests, all of num_pages pages free."""
+        import torch
+        ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(ints(requests + 1), ints(requests), ints(requests),
+                   torch.tensor([0, num_pages], dtype=torch.int64, device=device), ints(requests, max_pages) - 1,
+                   torch.arange(num_pages, dtype=torch.int32, device=device), page_size)
+
+
+def step_tables(tables, news, tokens, accepted=None, out=None, slots=None, positions=None, requests=None, missing=None,
+                workspace=None, stream=None):
+    """The tables of the next step, on the GPU: (slots int64 [tokens], positions int32 [tokens], requests int32
+    [tokens], missing int32 [1]) (see ocq_step_tables).
+
+    Of each request's tokens of the step before 1 + accepted (int32 [requests], as verify_drafts gives it; None: all)
+    stay, and news (int32 [requests]; -1: the request has ended) come.  tokens: a host number, at least the sum of
+    news.  The arrays of `tables` are changed in place, or those of `out`, a PageTables over the same page table and
+    ring with small arrays of its own.  missing: the pages that the ring or the table lacked.
+    """
+    i = _gpu(news, "news")
+    after = tables if out is None else out
+    _on(i, tables, after)
+    n, dev = tables.requests, tables.device
+    tokens = _int32(tokens, "tokens")
+    if tokens < 0:
+        raise OcqError(ERR_INVALID_ARG, "tokens is %d" % tokens)
+    _need(news, "news", _torch.int32, dev, (n,))
+    if accepted is not None:
+        _need(accepted, "accepted", _torch.int32, dev, (n,))
+    given = []
+    for t, name, dtype, size in ((slots, "slots", _torch.int64, tokens), (positions, "positions", _torch.int32, tokens),
+                                 (requests, "requests", _torch.int32, tokens), (missing, "missing", _torch.int32, 1)):
+        if t is None:
+            t = _empty(size, dtype, i, stream)
+        else:
+            _need(t, name, dtype, dev, (size,))
+        given.append(t)
+    L = lib()
+    if workspace is None:
+        need = L.ocq_step_tables_workspace_bytes(n, tokens)
+        if need:
+            workspace = _empty(need, _torch.uint8, i, stream)
+    else:
+        _need(workspace, "workspace", _torch.uint8, dev)
+        need = workspace.numel()
+    _check(L.ocq_step_tables(tables.ref, after.ref, news.data_ptr(), None if accepted is None else accepted.data_ptr(),
+                             tokens, given[0].data_ptr(), given[1].data_ptr(), given[2].data_ptr(),
+                             given[3].data_ptr(), None if workspace is None else workspace.data_ptr(), need,
+                             _stream_of(stream, i)))
+    return tuple(given)
 
 
 # ---------------------------------------------------------------- measurement helpers
