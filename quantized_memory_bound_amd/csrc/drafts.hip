@@ -9,25 +9,50 @@
 // (without q: from p without x), after the last one from w = p of its row: the
 // lowest j with sum_{i <= j} w_i > u sum w.
 //
-// Three launches.  A reads all logits once: each row's maximum and sum in 32 bits.
-// The acceptances compare 64-bit exponentials with that sum, whose relative error
-// is below 2^-22.  B sums the drawn row's exponentials in 64 bits (its weights
-// subtract q from p, and the place that a random number falls on hangs on every
-// weight before it), C its weights, in chunks; the workgroup that ends a request's
-// last chunk finds the chunk and the place in it.  Without q the weights need no Z
-// and B falls away; with given probabilities A does too.
+// Two launches.  A reads all logits once: each row's maximum and sum in 32 bits; the
+// workgroup that ends a request's last row compares its drafts (64-bit exponentials
+// with that sum Z', off by less than 2^-20) and leaves what drawing needs.  B sums the
+// drawn row's weights in 64 bits, in chunks; the workgroup that ends a request's
+// last chunk finds the chunk and the place in it.  (With given probabilities there
+// is no A: B's workgroups compare the drafts themselves.)
+//
+// The place that a random number falls on hangs on every weight before it, so Z' is
+// not enough for w = max(e_j / Z - q_j, 0), and Z is known only when all chunks are.
+// With S the j where e_j / Z' > q_j a chunk leaves sum e, sum_S e and sum_S q: its
+// weights are sum_S e / Z - sum_S q but for those j that lie between Z' and Z, each of
+// which is off by at most d e_j / Z, d = |Z' / Z - 1|.  It leaves the sum of e_j / Z'
+// over all j within 2^-16 of the border as well; where d is larger or d times that
+// sum is over 10^-10 of the weights (q is p but for roundings) the chunks are summed
+// again with Z, by one workgroup.  Against a launch for Z before the weights': 3.9
+// us.  What one workgroup leaves for another of its launch goes through
+// device-scope stores and loads, past the L2s.
 #include "kcommon.h"
 #include "layer_index.h"
 #include "step.h"
 
 namespace ocq {
 
-// A part of a row: its maximum, where it first stands, sum of exp((l - max) / T);
-// where not every logit is a number, the sum is NaN.
+// A part of a row: its maximum and where it first stands; the sum of exp((l - max) /
+// T), NaN where not every logit is a number.
 struct RowStat {
-  float top;
-  int at;
+  uint64_t top_at;   // float, int
   double sum;
+};
+
+// The draft after a row: its logit and id (-1: none), u q of it.
+struct RowDraft {
+  uint64_t logit_id;
+  double uq;
+};
+
+// What a request draws its next token from.
+struct Choice {
+  double top, inv_t, z;      // of the drawn row (logits), z as A has it
+  int64_t q_row;             // the draft's row that is subtracted, -1: none
+  int t0, n, count;          // first row, rows, accepted drafts
+  int draw;                  // 0: the next token is `next` (-1: none)
+  int next;
+  int without;               // the id that is left out, -1: none
 };
 
 namespace {
@@ -65,6 +90,9 @@ __device__ __forceinline__ void load_row(const T* row, int j, int end, float non
   }
 }
 
+// elements of a row's part where `ways` workgroups share it
+__device__ __forceinline__ int part_size(int vocab, int ways) { return ((vocab + ways - 1) / ways + kVec - 1) / kVec * kVec; }
+
 // The request of token t, or -1 (64 of them at a time).
 __device__ __forceinline__ int request_of(const DraftArgs& a, int t) {
   const int lane = threadIdx.x & 63;
@@ -88,67 +116,337 @@ __device__ __forceinline__ void best(float& v, int& at, float v2, int at2) {
   at = take ? at2 : at;
 }
 
+template <class V>
+__device__ __forceinline__ V load_agent(const V* p) {
+  return __builtin_bit_cast(V, __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+template <class V>
+__device__ __forceinline__ void store_agent(V* p, V v) {
+  __hip_atomic_store((uint64_t*)p, __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// A request's counter: 128 requests' lie 128 bytes apart.  (Arrivals at one cache
+// line follow each other 20 ns apart: side by side, 2080 of them took 30 us.)
+__device__ __forceinline__ uint32_t* counter_of(const DraftArgs& a, int r) {
+  static_assert(OCQ_ATTENTION_COUNTERS == 128 * 32, "");
+  return a.counters + (r & 127) * 32 + (r >> 7);
+}
+// Whether this workgroup is the last of `all` to come here with this counter, for
+// all its threads; what the others' first wave stored before is then visible to
+// device-scope loads.  The counter is 0 again afterwards.
+__device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t all, int* shared) {
+  if (threadIdx.x == 0) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const uint32_t before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *shared = before + 1 == all;
+    if (*shared) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return *shared != 0;
+}
+
+// A double of another lane (0 where there is none): DPP, no LDS round trip.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane64(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane) << 32 |
+                                        (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane));
+}
+// Sums over the lanes before and with this one: within rows of 16 (row_shr 1, 2, 4,
+// 8), then each row's last into the next rows (row_bcast 15 and 31).
+__device__ __forceinline__ double scan64(double v) {
+  v += dpp64<0x111, 0xF>(v);
+  v += dpp64<0x112, 0xF>(v);
+  v += dpp64<0x114, 0xF>(v);
+  v += dpp64<0x118, 0xF>(v);
+  v += dpp64<0x142, 0xA>(v);
+  v += dpp64<0x143, 0xC>(v);
+  return v;
+}
+__device__ __forceinline__ double sum64(double v) { return lane64(scan64(v), 63); }
+
+// e^y for y <= 0: 2^n times the series of e^g, g = (y log2 e - n) ln 2 within ln 2 /
+// 2, up to g^11 / 11! (the next term is below 2^-47); 0 from 2^-1075 down, NaN kept.
+__device__ __forceinline__ double exp64(double y) {
+  double x = y * kLog2e;
+  x = x < -1100.0 ? -1100.0 : x;
+  const double n = __builtin_rint(x), g = (x - n) * 0.69314718055994530942;
+  double p = 1.0 / 39916800.0;
+  p = __builtin_fma(p, g, 1.0 / 3628800.0);
+  p = __builtin_fma(p, g, 1.0 / 362880.0);
+  p = __builtin_fma(p, g, 1.0 / 40320.0);
+  p = __builtin_fma(p, g, 1.0 / 5040.0);
+  p = __builtin_fma(p, g, 1.0 / 720.0);
+  p = __builtin_fma(p, g, 1.0 / 120.0);
+  p = __builtin_fma(p, g, 1.0 / 24.0);
+  p = __builtin_fma(p, g, 1.0 / 6.0);
+  p = __builtin_fma(p, g, 0.5);
+  p = __builtin_fma(p, g, 1.0);
+  p = __builtin_fma(p, g, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+
+// ---------------------------------------------------------------- which drafts stay
+
+struct ChooseShared {
+  double z[64];
+  float top[64];
+  int at[64], id[64], first;
+};
+
+// The draft's rows before request r's: one less than its tokens for each request
+// (by whole waves).
+__device__ __forceinline__ int64_t draft_rows_before(const DraftArgs& a, int r, int t0) {
+  int idle = 0;
+  const int lane = threadIdx.x & 63;
+  for (int base = 0; base < r; base += 64)
+    idle += __popcll(__ballot(base + lane < r && token_span(a.q_start, base + lane, a.tokens).n <= 0));
+  return t0 - (r - idle);
+}
+
+// The draft after row t = t0 + i of a request with n rows.
+struct Draft {
+  int x;
+  float l;
+  double uq;
+};
+template <class T, class Q>
+__device__ __forceinline__ Draft draft_of(const DraftArgs& a, int t, int i, int n, int64_t before) {
+  Draft d{-1, 0.0f, 0.0};
+  if (i < n - 1) {
+    const int x = a.ids[t + 1];
+    if (x >= 0 && x < a.vocab) {
+      const float q = !a.draft ? 1.0f : before + i >= 0 && before + i < a.draft_rows
+                      ? load1((const Q*)a.draft + (before + i) * a.d_stride + x) : __builtin_nanf("");
+      d = Draft{x, load1((const T*)a.target + t * a.t_stride + x), (double)a.u_accept[t] * (double)q};
+    }
+  }
+  return d;
+}
+
+// By all threads of a workgroup; four lanes share a row's parts, 64 rows at a time.
+template <class T, class Q, bool PROBS>
+__device__ __forceinline__ Choice choose(const DraftArgs& a, int r, const Span& sp, int64_t before, float temp,
+                                         ChooseShared& sh) {
+  const int n = sp.n < 0 ? 0 : sp.n;
+  const double inv_t = 1.0 / (double)temp;
+  Choice c{0.0, inv_t, 0.0, -1, sp.t0, n, 0, 1, -1, -1};
+  for (int i0 = 0; i0 < n; i0 += 64) {
+    const int row = threadIdx.x >> 2, i = i0 + row, t = sp.t0 + (i < n ? i : 0);
+    Draft d;
+    if constexpr (PROBS) {
+      d = draft_of<T, Q>(a, t, i, n, before);
+    } else {
+      const uint64_t li = load_agent(&a.row_drafts[t].logit_id);
+      d = Draft{i < n ? (int)(li >> 32) : -1, __uint_as_float((uint32_t)li), load_agent(&a.row_drafts[t].uq)};
+    }
+    float top = -__builtin_inff();
+    int at = 0x7FFFFFFF;
+    double z = 0.0;
+    if constexpr (!PROBS) {
+      const RowStat* const st = a.stats + (size_t)t * a.splits;
+#pragma unroll 4
+      for (int k = threadIdx.x & 3; k < a.splits; k += 4) {
+        const uint64_t ta = load_agent(&st[k].top_at);
+        best(top, at, __uint_as_float((uint32_t)ta), (int)(ta >> 32));
+      }
+#pragma unroll
+      for (int b = 1; b < 4; b <<= 1) best(top, at, __shfl_xor(top, b), __shfl_xor(at, b));
+#pragma unroll 2
+      for (int k = threadIdx.x & 3; k < a.splits; k += 4) {
+        const float v = __uint_as_float((uint32_t)load_agent(&st[k].top_at));
+        const double s = load_agent(&st[k].sum);
+        z += temp == 0.0f || s == 0.0 ? s : s * exp64(((double)v - (double)top) * inv_t);
+      }
+#pragma unroll
+      for (int b = 1; b < 4; b <<= 1) z += __shfl_xor(z, b);
+    }
+    bool keep = false;
+    if (d.x >= 0) {
+      if (PROBS) keep = d.uq < (double)d.l;
+      else if (temp == 0.0f) keep = z == 0.0 && d.uq < (d.x == at ? 1.0 : 0.0);
+      else keep = d.uq * z < exp64(((double)d.l - (double)top) * inv_t);
+    }
+    if (threadIdx.x == 0) sh.first = 0x7FFFFFFF;
+    __syncthreads();
+    if (i < n && !keep && (threadIdx.x & 3) == 0) atomicMin(&sh.first, i);
+    if ((threadIdx.x & 3) == 0) {
+      sh.z[row] = z;
+      sh.top[row] = top;
+      sh.at[row] = at;
+      sh.id[row] = d.x;
+    }
+    __syncthreads();
+    const int first = sh.first;
+    if (first != 0x7FFFFFFF) {       // (the row after the last draft keeps none)
+      c.count = first;
+      c.top = (double)sh.top[first - i0];
+      c.z = sh.z[first - i0];
+      if (first < n - 1) {
+        if (a.draft) c.q_row = before + first >= 0 && before + first < a.draft_rows ? before + first : -1;
+        else c.without = sh.id[first - i0];
+      }
+      if (!PROBS && temp == 0.0f) {
+        c.draw = 0;
+        c.next = sh.z[first - i0] == 0.0 && sh.at[first - i0] != 0x7FFFFFFF ? sh.at[first - i0] : -1;
+      }
+      break;
+    }
+    __syncthreads();
+  }
+  if (n == 0) c.draw = 0;
+  return c;
+}
+
+// A request's rows: the accepted drafts, the next token if it is known, -1.
+__device__ __forceinline__ void put_rows(const DraftArgs& a, const Choice& c, int r) {
+  for (int i = threadIdx.x; i < c.n; i += kThreads)
+    if (i != c.count || !c.draw) a.out[c.t0 + i] = i < c.count ? a.ids[c.t0 + i + 1] : i == c.count ? c.next : -1;
+  if (threadIdx.x == 0) a.accepted[r] = c.count;
+}
+
 // ---------------------------------------------------------------- A: statistics of every row
 
+// A lane's vector as it lies in memory, and the one that changes nothing.
 template <class T>
+struct Raw {
+  static constexpr int W = kVec * sizeof(T) / 4;
+  uint32_t w[W];
+};
+__device__ __forceinline__ void unpack(const Raw<float>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) f[i] = __uint_as_float(r.w[i]);
+}
+__device__ __forceinline__ void unpack(const Raw<uint16_t>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < kVec / 2; ++i) {
+    f[2 * i] = __uint_as_float(r.w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+  }
+}
+
+// The statistics of one row's part.  UNR vectors of a lane are summed while the
+// next UNR are on their way.
+template <class T, class Q>
 __global__ __launch_bounds__(kThreads) void k_stats(DraftArgs a) {
+  constexpr int UNR = sizeof(T) == 2 ? 4 : 2, STEP = kThreads * kVec, TILE = UNR * STEP;
+  __shared__ ChooseShared sh;
+  __shared__ float s_top[4];
+  __shared__ int s_at[4], s_last;
+  __shared__ double s_sum[4];
   const int t = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int r = request_of(a, t);
-  if (r < 0) return;
-  const float temp = temperature(a, r);
-  const int per = ((a.vocab + a.splits - 1) / a.splits + kVec - 1) / kVec * kVec;
+  const int per = part_size(a.vocab, a.splits);
   const int from = split * per, end = from + per < a.vocab ? from + per : a.vocab;
   const T* const row = (const T*)a.target + t * a.t_stride;
-  float top = -__builtin_inff();
-  int at = 0x7FFFFFFF;
-  double sum = 0.0;
-  bool bad = false;
-  if (temp == 0.0f) {
-    for (int j = from + threadIdx.x * kVec; j < end; j += kThreads * kVec) {
-      float f[kVec];
-      load_row(row, j, end, -__builtin_inff(), f);
+  Raw<T> raw[UNR];
+  auto load = [&](int j) {       // whole vectors; those that the row's end cuts come last
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        bad |= f[i] != f[i];
-        if (f[i] > top) {
-          top = f[i];
-          at = j + i;
+    for (int k = 0; k < UNR; ++k) {
+      if (j + k * STEP + kVec <= end) {
+        __builtin_memcpy(raw[k].w, row + j + k * STEP, sizeof(raw[k].w));
+      } else {
+#pragma unroll
+        for (int i = 0; i < Raw<T>::W; ++i) raw[k].w[i] = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;   // -inf
+      }
+    }
+  };
+  const int j0 = from + threadIdx.x * kVec;
+  load(j0);
+  const int cut = end - end % kVec + threadIdx.x;
+  const float rest = (int)threadIdx.x < end % kVec ? load1(row + cut) : -__builtin_inff();
+  const int r = request_of(a, t);
+  if (r < 0) {
+    if (threadIdx.x == 0 && split == 0) a.out[t] = -1;
+    return;
+  }
+  const float temp = temperature(a, r);
+  const Span sp = token_span(a.q_start, r, a.tokens);
+  // what the request's comparisons take of this row's draft, on its way early
+  const int64_t before = a.draft ? draft_rows_before(a, r, sp.t0) : 0;
+  Draft d{-1, 0.0f, 0.0};
+  if (split == 0 && threadIdx.x == 0) d = draft_of<T, Q>(a, t, t - sp.t0, sp.n, before);
+  float top = rest;
+  int at = (int)threadIdx.x < end % kVec && rest > -__builtin_inff() ? cut : 0x7FFFFFFF;
+  double sum = 0.0;
+  if (temp == 0.0f) {
+    bool bad = rest != rest;
+    if (bad) top = -__builtin_inff();
+    for (int j = j0; j < end; j += TILE) {
+      Raw<T> now[UNR];
+#pragma unroll
+      for (int k = 0; k < UNR; ++k) now[k] = raw[k];
+      if (j + TILE < end) load(j + TILE);
+#pragma unroll
+      for (int k = 0; k < UNR; ++k) {
+        // the vector's maximum first: its place only where it is a new one
+        float f[kVec], m;
+        unpack(now[k], f);
+        m = f[0];
+        bool nan = f[0] != f[0];
+#pragma unroll
+        for (int i = 1; i < kVec; ++i) {
+          m = fmaxf(m, f[i]);
+          nan |= f[i] != f[i];
+        }
+        bad |= nan;
+        if (m > top || (m == top && j + k * STEP < at)) {
+          top = m;
+#pragma unroll
+          for (int i = kVec - 1; i >= 0; --i)
+            if (f[i] == m) at = j + k * STEP + i;
         }
       }
     }
+    if (top == -__builtin_inff()) at = 0x7FFFFFFF;
+    if (bad) sum = __builtin_nan("");
   } else {
     const float c = (float)(kLog2e / (double)temp);
-    float s = 0.0f;
-    for (int j = from + threadIdx.x * kVec; j < end; j += kThreads * kVec) {
-      float f[kVec], m = top;
-      load_row(row, j, end, -__builtin_inff(), f);
+    float s = rest == -__builtin_inff() ? 0.0f : 1.0f + 0.0f * rest;   // e^0; NaN and inf are none
+    if (rest != rest) top = -__builtin_inff();
+    for (int j = j0; j < end; j += TILE) {
+      float f[UNR][kVec], m = top;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) m = fmaxf(m, f[i]);
+      for (int k = 0; k < UNR; ++k) unpack(raw[k], f[k]);
+      if (j + TILE < end) load(j + TILE);
+#pragma unroll
+      for (int k = 0; k < UNR; ++k)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) m = fmaxf(m, f[k][i]);
       if (m > top) {
         s = top == -__builtin_inff() ? s : s * __builtin_amdgcn_exp2f((top - m) * c);
         top = m;
       }
       const float base = top == -__builtin_inff() ? 0.0f : top;
-      float e = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) e += __builtin_amdgcn_exp2f((f[i] - base) * c);
-      s += e;
+      for (int k = 0; k < UNR; ++k) {
+        float e = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) e += __builtin_amdgcn_exp2f((f[k][i] - base) * c);
+        s += e;
+      }
     }
     sum = s;
   }
   // over the workgroup
-  __shared__ float s_top[4];
-  __shared__ int s_at[4];
-  __shared__ double s_sum[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float mine = top;
-  if (bad) sum = __builtin_nan("");
+  top = wave_max(top);
+  if (temp == 0.0f) {
+    at = mine == top ? at : 0x7FFFFFFF;
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) best(top, at, __shfl_xor(top, x), __shfl_xor(at, x));
-  if (temp != 0.0f && mine != top)
-    sum = mine == -__builtin_inff() ? sum : sum * (double)__builtin_amdgcn_exp2f((mine - top) * (float)(kLog2e / temp));
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+    for (int x = 1; x < 64; x <<= 1) {
+      const int other = __shfl_xor(at, x);
+      at = other < at ? other : at;
+    }
+  } else if (mine != top && mine != -__builtin_inff()) {
+    sum *= (double)__builtin_amdgcn_exp2f((mine - top) * (float)(kLog2e / (double)temp));
+  }
+  sum = sum64(sum);
   if (lane == 0) {
     s_top[wave] = top;
     s_at[wave] = at;
@@ -160,133 +458,64 @@ __global__ __launch_bounds__(kThreads) void k_stats(DraftArgs a) {
     sum = 0.0;
     for (int w = 0; w < 4; ++w)
       sum += s_top[w] == top || s_top[w] == -__builtin_inff() || temp == 0.0f
-                 ? s_sum[w] : s_sum[w] * exp(((double)s_top[w] - (double)top) / (double)temp);
-    a.stats[(size_t)t * a.splits + split] = RowStat{top, at, sum};
+                 ? s_sum[w] : s_sum[w] * exp64(((double)s_top[w] - (double)top) / (double)temp);
+    RowStat* const st = a.stats + (size_t)t * a.splits + split;
+    store_agent(&st->top_at, (uint64_t)(uint32_t)at << 32 | __float_as_uint(top));
+    store_agent(&st->sum, sum);
+    if (split == 0) {
+      store_agent(&a.row_drafts[t].logit_id, (uint64_t)(uint32_t)d.x << 32 | __float_as_uint(d.l));
+      store_agent(&a.row_drafts[t].uq, d.uq);
+    }
   }
+  if (!last_of(counter_of(a, r), (uint32_t)(sp.n * a.splits), &s_last)) return;
+  const Choice c = choose<T, Q, false>(a, r, sp, before, temp, sh);
+  if (threadIdx.x == 0) a.choices[r] = c;
+  put_rows(a, c, r);
 }
 
-// ---------------------------------------------------------------- B, C: the row that is drawn from
-
-// What every workgroup of a request finds out by itself.
-struct Choice {
-  int t0, n, count;          // first row, rows, accepted drafts
-  int greedy, at;            // T = 0: the next token (-1: none)
-  double top, inv_t, z;      // of the drawn row (logits)
-  int64_t q_row;             // the draft's row that is subtracted, -1: none
-  int without;               // the id that is left out, -1: none
-};
-
-template <class T, class Q>
-__device__ __forceinline__ void choose(const DraftArgs& a, int r, Choice* sh) {
-  const Span sp = token_span(a.q_start, r, a.tokens);
-  const int n = sp.n < 0 ? 0 : sp.n, lane = threadIdx.x & 63;
-  if (threadIdx.x >= 64) return;
-  // rows of the draft's before this request's: one less than its tokens each
-  int64_t before = 0;
-  if (a.draft) {
-    int idle = 0;
-    for (int base = 0; base < r; base += 64)
-      idle += __popcll(__ballot(base + lane < r && token_span(a.q_start, base + lane, a.tokens).n <= 0));
-    before = sp.t0 - (r - idle);
-  }
-  const float temp = a.probs ? 1.0f : temperature(a, r);
-  const double inv_t = 1.0 / (double)temp;
-  int count = n - 1;
-  Choice c{sp.t0, n, 0, 0, -1, 0.0, inv_t, 1.0, -1, -1};
-  // a lane's row t: what it says about its draft, and what drawing from it takes
-  for (int i0 = 0; i0 < n; i0 += 64) {
-    const int i = i0 + lane, t = sp.t0 + (i < n ? i : 0);
-    float top = -__builtin_inff();
-    int at = 0x7FFFFFFF;
-    double z = 0.0;
-    if (!a.probs) {
-      const RowStat* const st = a.stats + (size_t)t * a.splits;
-      for (int k = 0; k < a.splits; ++k) best(top, at, st[k].top, st[k].at);
-      for (int k = 0; k < a.splits; ++k)
-        z += st[k].top == top || st[k].top == -__builtin_inff() || temp == 0.0f
-                 ? st[k].sum : st[k].sum * exp(((double)st[k].top - (double)top) * inv_t);
-    }
-    bool keep = false;
-    if (i < n - 1) {
-      const int x = a.ids[t + 1];
-      if (x >= 0 && x < a.vocab) {
-        double q = 1.0;
-        if (a.draft) q = before + i >= 0 && before + i < a.draft_rows
-                             ? (double)load1((const Q*)a.draft + (before + i) * a.d_stride + x) : __builtin_nan("");
-        const double l = (double)load1((const T*)a.target + t * a.t_stride + x);
-        const double u = (double)a.u_accept[t];
-        if (a.probs) keep = u * q < l;
-        else if (temp == 0.0f) keep = z == 0.0 && u * q < (x == at ? 1.0 : 0.0);
-        else keep = u * q * z < exp((l - (double)top) * inv_t);
-      }
-    }
-    const uint64_t out = ~__ballot(keep);
-    const int first = i0 + __builtin_ctzll(out);   // (a row past the last draft keeps nothing)
-    if (out != 0 && first < n) {
-      const int l = first - i0;
-      count = first;
-      c.top = (double)__shfl(top, l);
-      c.z = __shfl(z, l);
-      c.at = __shfl(at, l);
-      break;
-    }
-  }
-  if (lane != 0) return;
-  c.count = n > 0 ? count : 0;
-  c.greedy = !a.probs && temp == 0.0f;
-  if (!c.greedy || c.at == 0x7FFFFFFF || c.z != 0.0) c.at = -1;
-  if (n > 0 && count < n - 1) {
-    const int x = a.ids[sp.t0 + count + 1];
-    if (a.draft) c.q_row = before + count >= 0 && before + count < a.draft_rows ? before + count : -1;
-    else if (x >= 0 && x < a.vocab) c.without = x;
-  }
-  *sh = c;
-}
+// ---------------------------------------------------------------- B: the row that is drawn from
 
 // eight weights from j on; 0 past the end
 template <class T, class Q, bool PROBS>
 __device__ __forceinline__ void weights(const DraftArgs& a, const Choice& c, int j, double inv_z, bool plain, double* w) {
   float f[kVec];
   load_row((const T*)a.target + (int64_t)(c.t0 + c.count) * a.t_stride, j, a.vocab, PROBS ? 0.0f : -__builtin_inff(), f);
+  float q[kVec];
+  const bool less = !plain && c.q_row >= 0;
+  if (less) load_row((const Q*)a.draft + c.q_row * a.d_stride, j, a.vocab, 0.0f, q);
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) w[i] = PROBS ? (double)f[i] : exp(((double)f[i] - c.top) * c.inv_t) * inv_z;
-  if (plain) return;
-  if (c.q_row >= 0) {
-    float q[kVec];
-    load_row((const Q*)a.draft + c.q_row * a.d_stride, j, a.vocab, 0.0f, q);
+  for (int i = 0; i < kVec; ++i) w[i] = PROBS ? (double)f[i] : exp64(((double)f[i] - c.top) * c.inv_t) * inv_z;
+  if (less) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const double d = w[i] - (double)q[i];
       w[i] = d > 0.0 ? d : d == d ? 0.0 : d;      // NaN stays
     }
   }
-  if (c.without >= j && c.without < j + kVec)
+  if (!plain && c.without >= j && c.without < j + kVec)
 #pragma unroll
     for (int i = 0; i < kVec; ++i) w[i] = j + i == c.without ? 0.0 : w[i];
 }
 
-// Sums over the lanes before and with this one.
-__device__ __forceinline__ double scan64(double v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) {
-    const double o = __shfl_up(v, x);
-    if (lane >= x) v += o;
-  }
-  return v;
-}
-
 __device__ __forceinline__ double block_sum(double v, double* s) {
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) v += __shfl_xor(v, x);
+  v = sum64(v);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
   return s[0] + s[1] + s[2] + s[3];
 }
 
-__device__ __forceinline__ int chunk_size(const DraftArgs& a) {
-  return ((a.vocab + a.chunks - 1) / a.chunks + kVec - 1) / kVec * kVec;
+template <class T, class Q, bool PROBS>
+__device__ __forceinline__ double chunk_sum(const DraftArgs& a, const Choice& c, int g, double inv_z, bool plain, double* s) {
+  const int per = part_size(a.vocab, a.chunks), from = g * per, end = from + per < a.vocab ? from + per : a.vocab;
+  double sum = 0.0;
+  for (int j = from + threadIdx.x * kVec; j < end; j += kThreads * kVec) {
+    double w[kVec];
+    weights<T, Q, PROBS>(a, c, j, inv_z, plain, w);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) sum += j + i < end ? w[i] : 0.0;
+  }
+  return block_sum(sum, s);
 }
 
 // The place in chunk `g` where the sum that starts at `before` passes t, or the
@@ -294,7 +523,7 @@ __device__ __forceinline__ int chunk_size(const DraftArgs& a) {
 template <class T, class Q, bool PROBS>
 __device__ __forceinline__ int place_in(const DraftArgs& a, const Choice& c, int g, double before, double t, double inv_z,
                                         bool plain, double* s, int* s_at) {
-  const int per = chunk_size(a), from = g * per, end = from + per < a.vocab ? from + per : a.vocab;
+  const int per = part_size(a.vocab, a.chunks), from = g * per, end = from + per < a.vocab ? from + per : a.vocab;
   const int wave = threadIdx.x >> 6;
   int last = -1;
   for (int base = from; base < end; base += kThreads * kVec) {
@@ -332,135 +561,154 @@ __device__ __forceinline__ int place_in(const DraftArgs& a, const Choice& c, int
   return last;
 }
 
-// Z: sums of the exponentials (a launch of its own before the weights'); else the
-// sums of the weights, and the next token.
-template <class T, class Q, bool PROBS, bool Z>
-__global__ __launch_bounds__(kThreads) void k_next(DraftArgs a) {
-  __shared__ Choice sh;
-  __shared__ double s[4], s_part[64];
-  __shared__ int s_at[2], s_last;
-  const int r = blockIdx.x / a.chunks, g = blockIdx.x % a.chunks;
-  choose<T, Q>(a, r, &sh);
-  __syncthreads();
-  const Choice c = sh;
-  const size_t pairs = (size_t)a.requests * a.chunks;
-  double* const parts = a.parts + (Z ? 0 : pairs) + (size_t)r * a.chunks;
-  int next = c.at;
-  if (c.n > 0 && !c.greedy) {
-    const int per = chunk_size(a), from = g * per, end = from + per < a.vocab ? from + per : a.vocab;
-    double z = 1.0;
-    if (!Z && !PROBS && c.q_row >= 0) {
-      z = 0.0;
-      for (int k = 0; k < a.chunks; ++k) z += a.parts[(size_t)r * a.chunks + k];
-    }
-    const double inv_z = 1.0 / z;
-    double sum = 0.0;
-    if (!Z || c.q_row >= 0)
-      for (int j = from + threadIdx.x * kVec; j < end; j += kThreads * kVec) {
-        double w[kVec];
-        weights<T, Q, PROBS>(a, c, j, inv_z, Z, w);
+// The chunk where the sum of the chunks' (one a lane; every wave finds it) passes u
+// times all, and the sum before it; -1: nowhere.
+struct Found {
+  int chunk;
+  double before, t;
+};
+__device__ __forceinline__ Found find_chunk(double mine, float u, bool& none) {
+  const double upto = scan64(mine), total = lane64(upto, 63);
+  Found f{-1, 0.0, (double)u * total};
+  none = total == 0.0;
+  if (!(total > 0.0 && total < __builtin_inf())) return f;
+  const uint64_t past = __ballot(upto > f.t), some = __ballot(mine > 0.0);
+  f.chunk = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);    // u of 1 or more: the last weight
+  f.before = f.chunk ? lane64(upto, f.chunk - 1) : 0.0;
+  return f;
+}
+
+// What a chunk leaves of a row from which q is subtracted.
+struct Sums {
+  double e, e_s, q_s, near;
+};
+constexpr double kNear = 1.0 / 65536, kOff = 1e-10;
+
+template <class T, class Q>
+__device__ __forceinline__ Sums chunk_sums(const DraftArgs& a, const Choice& c, int g, double inv_z, double (&s)[4][4]) {
+  const int per = part_size(a.vocab, a.chunks), from = g * per, end = from + per < a.vocab ? from + per : a.vocab;
+  double v[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int j = from + threadIdx.x * kVec; j < end; j += kThreads * kVec) {
+    float f[kVec], q[kVec];
+    load_row((const T*)a.target + (int64_t)(c.t0 + c.count) * a.t_stride, j, end, -__builtin_inff(), f);
+    load_row((const Q*)a.draft + c.q_row * a.d_stride, j, end, 0.0f, q);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sum += j + i < end ? w[i] : 0.0;
-      }
-    sum = block_sum(sum, s);
-    if (threadIdx.x == 0) {
-      if (Z) parts[g] = sum;
-      else __hip_atomic_store((uint64_t*)parts + g, __builtin_bit_cast(uint64_t, sum), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = 0; i < kVec; ++i) {
+      const double e = exp64(((double)f[i] - c.top) * c.inv_t), p = e * inv_z, d = p - (double)q[i];
+      v[0] += e;
+      v[1] += d > 0.0 ? e : 0.0;
+      v[2] += d > 0.0 ? (double)q[i] : d == d ? 0.0 : d;     // NaN stays
+      v[3] += __builtin_fabs(d) <= kNear * p ? p : 0.0;
     }
-    if (Z) return;
-    // the workgroup that ends the request's last chunk
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    if (threadIdx.x == 0) {
-      const uint32_t before = __hip_atomic_fetch_add(a.counters + r, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      s_last = before + 1 == (uint32_t)a.chunks;
-      if (s_last) __hip_atomic_store(a.counters + r, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = sum64(v[k]);
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k][threadIdx.x >> 6] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = s[k][0] + s[k][1] + s[k][2] + s[k][3];
+  return Sums{v[0], v[1], v[2], v[3]};
+}
+
+template <class T, class Q, bool PROBS>
+__global__ __launch_bounds__(kThreads) void k_next(DraftArgs a) {
+  __shared__ ChooseShared sh;
+  __shared__ double s[4], s4[4][4], s_part[64];
+  __shared__ int s_at[2], s_last;
+  const int r = blockIdx.x / a.chunks, g = blockIdx.x % a.chunks, lane = threadIdx.x & 63;
+  const Span sp = token_span(a.q_start, r, a.tokens);
+  Choice c;
+  if constexpr (PROBS) {
+    c = choose<T, Q, true>(a, r, sp, a.draft ? draft_rows_before(a, r, sp.t0) : 0, 1.0f, sh);
+    if (g == 0) put_rows(a, c, r);
+    if (g == 0 && r == a.requests - 1) {                // rows of no request
+      const int behind = a.q_start[a.requests];
+      for (int t = (behind < 0 ? 0 : behind) + threadIdx.x; t < a.tokens; t += kThreads) a.out[t] = -1;
+    }
+  } else {
+    if (sp.n <= 0) {                                    // (A has no row of it)
+      if (g == 0 && threadIdx.x == 0) a.accepted[r] = 0;
+      return;
+    }
+    c = a.choices[r];
+  }
+  if (!c.draw) return;
+  Sums* const parts = (Sums*)a.parts + (size_t)r * a.chunks;
+  const bool two = !PROBS && c.q_row >= 0;              // Z is still to be found
+  if (two) {
+    const Sums v = chunk_sums<T, Q>(a, c, g, 1.0 / c.z, s4);
+    if (threadIdx.x < 4) store_agent((double*)(parts + g) + threadIdx.x, threadIdx.x == 0 ? v.e : threadIdx.x == 1 ? v.e_s
+                                                                         : threadIdx.x == 2 ? v.q_s : v.near);
+  } else {
+    const double sum = chunk_sum<T, Q, PROBS>(a, c, g, 1.0, false, s);
+    if (threadIdx.x == 0) store_agent(&parts[g].e, sum);
+  }
+  if (!last_of(counter_of(a, r), (uint32_t)a.chunks, &s_last)) return;
+  double mine = lane < a.chunks ? load_agent(&parts[lane].e) : 0.0, inv_z = 1.0;
+  bool again = false, none = false;
+  if (two) {
+    const double z = sum64(mine);
+    inv_z = 1.0 / z;
+    double near = 0.0;
+    mine = 0.0;
+    if (lane < a.chunks) {
+      mine = load_agent(&parts[lane].e_s) * inv_z - load_agent(&parts[lane].q_s);
+      near = load_agent(&parts[lane].near);
+      mine = mine < 0.0 ? 0.0 : mine;
+    }
+    const double off = __builtin_fabs(c.z * inv_z - 1.0);
+    again = off > kNear * 0.5 || off * sum64(near) > kOff * sum64(mine);
+  }
+  Found f = find_chunk(mine, a.u_next[r], none);
+  bool plain = false;
+  for (int turn = 0; turn < 2; ++turn) {
+    // the chunks' weights with Z, or, where nothing is left of p, of p itself
+    if (turn == 0 && !again) continue;
+    if (turn == 1) {
+      if (!none || (c.q_row < 0 && c.without < 0)) break;
+      plain = true;
+    }
+    for (int k = 0; k < a.chunks; ++k) {
+      const double one = chunk_sum<T, Q, PROBS>(a, c, k, inv_z, plain, s);
+      if (threadIdx.x == 0) s_part[k] = one;
     }
     __syncthreads();
-    if (!s_last) return;
-    for (int plain = 0; plain < 2; ++plain) {
-      if (plain && c.q_row < 0 && c.without < 0) break;
-      if (threadIdx.x < a.chunks && !plain)
-        s_part[threadIdx.x] = __builtin_bit_cast(double, __hip_atomic_load((uint64_t*)parts + threadIdx.x, __ATOMIC_RELAXED,
-                                                                           __HIP_MEMORY_SCOPE_AGENT));
-      if (plain) {
-        // nothing is left of p after q: drawn from p (chunks summed again, here)
-        for (int k = 0; k < a.chunks; ++k) {
-          double one = 0.0;
-          for (int j = k * per + threadIdx.x * kVec; j < k * per + per && j < a.vocab; j += kThreads * kVec) {
-            double w[kVec];
-            weights<T, Q, PROBS>(a, c, j, inv_z, true, w);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) one += j + i < k * per + per && j + i < a.vocab ? w[i] : 0.0;
-          }
-          one = block_sum(one, s);
-          if (threadIdx.x == 0) s_part[k] = one;
-        }
-      }
-      __syncthreads();
-      double total = 0.0;
-      for (int k = 0; k < a.chunks; ++k) total += s_part[k];
-      if (total == 0.0 && !plain) continue;
-      next = -1;
-      if (total > 0.0 && total < __builtin_inf()) {
-        const double t = (double)a.u_next[r] * total;
-        double before = 0.0, at_before = 0.0, run = 0.0;
-        int chunk = -1;
-        for (int k = 0; k < a.chunks; ++k) {
-          run += s_part[k];
-          if (chunk < 0 && run > t) {
-            chunk = k;
-            at_before = before;
-          }
-          before = run;
-        }
-        if (chunk < 0) {                              // u of 1 or more: the last weight
-          for (int k = 0; k < a.chunks; ++k)
-            if (s_part[k] > 0.0) chunk = k;
-        }
-        next = place_in<T, Q, PROBS>(a, c, chunk, at_before, t, inv_z, plain, s, s_at);
-      }
-      break;
-    }
-  } else if (Z || g != 0) {
-    return;
+    f = find_chunk(lane < a.chunks ? s_part[lane] : 0.0, a.u_next[r], none);
+    __syncthreads();
   }
-  // a request's rows: the accepted drafts, the next token, -1
-  for (int i = threadIdx.x; i < c.n; i += kThreads)
-    a.out[c.t0 + i] = i < c.count ? a.ids[c.t0 + i + 1] : i == c.count ? next : -1;
-  if (threadIdx.x == 0) a.accepted[r] = c.count;
-  if (r == a.requests - 1) {                          // rows of no request
-    int behind = a.q_start[a.requests];
-    behind = behind < 0 ? 0 : behind;
-    for (int t = behind + threadIdx.x; t < a.tokens; t += kThreads) a.out[t] = -1;
-  }
+  const int next = f.chunk < 0 ? -1 : place_in<T, Q, PROBS>(a, c, f.chunk, f.before, f.t, inv_z, plain, s, s_at);
+  if (threadIdx.x == 0) a.out[c.t0 + c.count] = next;
 }
 
 template <class T, class Q>
 void run(const DraftArgs& a, hipStream_t st) {
   const dim3 block(kThreads), next((unsigned)(a.requests * a.chunks));
   if (a.probs) {
-    hipLaunchKernelGGL((k_next<T, Q, true, false>), next, block, 0, st, a);
+    hipLaunchKernelGGL((k_next<T, Q, true>), next, block, 0, st, a);
     return;
   }
-  hipLaunchKernelGGL((k_stats<T>), dim3((unsigned)(a.tokens * a.splits)), block, 0, st, a);
-  if (a.draft) hipLaunchKernelGGL((k_next<T, Q, false, true>), next, block, 0, st, a);
-  hipLaunchKernelGGL((k_next<T, Q, false, false>), next, block, 0, st, a);
+  hipLaunchKernelGGL((k_stats<T, Q>), dim3((unsigned)(a.tokens * a.splits)), block, 0, st, a);
+  hipLaunchKernelGGL((k_next<T, Q, false>), next, block, 0, st, a);
 }
 
 }  // namespace
 
+// A: about 768 workgroups, none below 4096 elements (208 rows of 131072 in bf16:
+// 18.4 us; 2048 workgroups 22.1); a drawn row in chunks of 2048, one load a lane, 64
+// at most.
 DraftPlan draft_plan(int tokens, int requests, int vocab, int probs) {
-  DraftPlan p{1, 1, 0, 0};
-  auto ways = [&](int64_t rows, int least, int most) {
-    int64_t w = (2048 + rows - 1) / rows;
-    const int64_t fit = (vocab + least - 1) / least;
-    w = w < fit ? w : fit;
-    return (int)(w < 1 ? 1 : w > most ? most : w);
-  };
-  p.splits = ways(tokens > 0 ? tokens : 1, 4096, 64);
-  p.chunks = ways(requests > 0 ? requests : 1, 4096, 64);
-  p.stats_bytes = probs ? 0 : (size_t)tokens * p.splits * sizeof(RowStat);
-  p.bytes = p.stats_bytes + (size_t)2 * requests * p.chunks * sizeof(double);
+  DraftPlan p{1, 1, 0, 0, 0, 0};
+  const int64_t want = tokens > 0 ? (768 + tokens - 1) / tokens : 1, fit = (vocab + 4095) / 4096;
+  p.splits = (int)(want < fit ? want : fit);
+  p.splits = p.splits < 1 ? 1 : p.splits > 64 ? 64 : p.splits;
+  p.chunks = (vocab + 2047) / 2048;
+  p.chunks = p.chunks > 64 ? 64 : p.chunks;
+  p.drafts_at = probs ? 0 : (size_t)tokens * p.splits * sizeof(RowStat);
+  p.choices_at = p.drafts_at + (probs ? 0 : (size_t)tokens * sizeof(RowDraft));
+  p.parts_at = p.choices_at + (probs ? 0 : (size_t)requests * sizeof(Choice));
+  p.bytes = p.parts_at + (size_t)requests * p.chunks * sizeof(Sums);
   return p;
 }
 

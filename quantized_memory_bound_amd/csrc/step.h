@@ -9,6 +9,8 @@
 namespace ocq {
 
 struct RowStat;   // drafts.hip
+struct RowDraft;
+struct Choice;
 
 struct DraftArgs {
   const void* target;        // [tokens][vocab]: logits or probabilities
@@ -26,13 +28,15 @@ struct DraftArgs {
   int32_t* out;              // [tokens]
   int splits, chunks;        // workgroups of a row's statistics, and of a request's drawn row
   RowStat* stats;            // [tokens][splits]
-  double* parts;             // [2][requests][chunks]: sums of the drawn row's exponentials, of its weights
+  RowDraft* row_drafts;      // [tokens]
+  Choice* choices;           // [requests]
+  double* parts;             // [requests][chunks][4]: sums of the drawn row
   uint32_t* counters;        // [OCQ_ATTENTION_COUNTERS], 0 between calls
 };
 
 struct DraftPlan {
   int splits, chunks;
-  size_t stats_bytes, bytes;   // of the workspace: the statistics, all
+  size_t drafts_at, choices_at, parts_at, bytes;   // of the workspace
 };
 DraftPlan draft_plan(int tokens, int requests, int vocab, int probs);
 

@@ -118,7 +118,9 @@ ocq_status ocq_verify_drafts(const void* target_dev, int64_t target_stride, int 
   a.splits = plan.splits;
   a.chunks = plan.chunks;
   a.stats = (RowStat*)workspace_dev;
-  a.parts = (double*)((uint8_t*)workspace_dev + plan.stats_bytes);
+  a.row_drafts = (RowDraft*)((uint8_t*)workspace_dev + plan.drafts_at);
+  a.choices = (Choice*)((uint8_t*)workspace_dev + plan.choices_at);
+  a.parts = (double*)((uint8_t*)workspace_dev + plan.parts_at);
   a.counters = (uint32_t*)batch->counters_dev;
   const int rc = launch_drafts(a, stream);
   return rc ? hip_error(rc) : OCQ_OK;

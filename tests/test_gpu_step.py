@@ -145,6 +145,21 @@ def test_drafts_that_all_stay_and_that_none_does():
     assert accepted.tolist() == [0, 0]
 
 
+@pytest.mark.parametrize("vocab", [50, 3001, 40000, 150000])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_drafts_whose_probabilities_are_the_targets_but_for_roundings(vocab, dtype):
+    """q is p rounded to bf16, random numbers next to 1 refuse where it was rounded up: the weights are what roundings
+    left, far below p and q."""
+    for seed in range(4):
+        s = make_drafts([5, 3, 9], vocab, seed, dtype, torch.bfloat16, near=0.0, temps=[1.0, 0.8, 1.3])
+        # of the logits as they are held
+        p = torch.softmax(s["target"].double() / torch.tensor([1.0] * 5 + [0.8] * 3 + [1.3] * 9, device=DEV)[:, None], -1)
+        of = torch.tensor([0, 1, 2, 3, 5, 6, 8, 9, 10, 11, 12, 13, 14, 15], device=DEV)
+        s["draft"].copy_(p[of])
+        s["u_accept"][:] = 1 - 2.0 ** -24
+        check_drafts(s)
+
+
 @pytest.mark.parametrize("u", [0.0, 2.0 ** -24, 0.5, 1 - 2.0 ** -24])
 @pytest.mark.parametrize("vocab", [3, 2049, 20000])
 def test_drafts_random_numbers_at_their_ends(u, vocab):
