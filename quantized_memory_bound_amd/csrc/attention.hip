@@ -619,6 +619,23 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   }
   auto products = [&](auto slot_c, scores& s) {
     constexpr int slot = decltype(slot_c)::value;
+    // codes and scales of the whole stage before the first product: the compiler
+    // would ask for them one by one and wait for each
+    constexpr int NX = G::KV4 ? G::QS / G::KW : 1;
+    typedef std::conditional_t<G::KW == 4, v4i, v2i> codes_t;
+    codes_t k_raw[G::NKT][NX];
+    uint32_t k_sc[G::NKT][NX];
+    if constexpr (G::KV4) {
+#pragma unroll
+      for (int kt = 0; kt < G::NKT; ++kt)
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+          const uint8_t* const sc = ring + slot + G::PART + (kt * G::MT + r) * G::SB + (x * G::LG + g) * (G::KW / 2);
+          k_sc[kt][x] = G::KW == 4 ? *(const uint16_t*)sc : *sc;
+          k_raw[kt][x] = *(const codes_t*)(ring + slot + kt * G::MT * G::RB + (k_off[x] ^ (swz<G>(kt * G::MT) << 4)));
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int kt = 0; kt < G::NKT; ++kt) {
 #pragma unroll
@@ -628,21 +645,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
       if constexpr (G::KV4) {
 #pragma unroll
         for (int x = 0; x < G::QS; x += G::KW) {
-          // the read's codes, 16 to a scale
-          const uint8_t* const sc = ring + slot + G::PART + (kt * G::MT + r) * G::SB + (x / G::KW * G::LG + g) * (G::KW / 2);
           v2h s0, s1;
-          uint32_t u[4];
-          if constexpr (G::KW == 4) {
-            e4m3x2_scales(*(const uint16_t*)sc, s0, s1);
-            const v4i w = *(const v4i*)(ring + at + (k_off[x / 4] ^ f));
-            for (int j = 0; j < 4; ++j) u[j] = w[j];
-          } else {
-            e4m3x2_scales(*sc, s0, s1);
-            const v2i w = *(const v2i*)(ring + at + (k_off[x / 2] ^ f));
-            for (int j = 0; j < 2; ++j) u[j] = w[j];
-          }
+          e4m3x2_scales(k_sc[kt][x / G::KW], s0, s1);
 #pragma unroll
-          for (int j = 0; j < G::KW; ++j) s[kt] = mfma(e2m1x8_to_f16(u[j], j < 2 ? s0 : s1), q[x + j], s[kt]);
+          for (int j = 0; j < G::KW; ++j)
+            s[kt] = mfma(e2m1x8_to_f16((uint32_t)k_raw[kt][x / G::KW][j], j < 2 ? s0 : s1), q[x + j], s[kt]);
         }
       } else if constexpr (!G::KV8) {
 #pragma unroll
@@ -745,9 +752,20 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
         p[(kt * AN + 4 * i4) / 2 + 1] = G::KV4 ? pack_f16(e[2], e[3]) : pack_bf16(e[2], e[3]);
       }
     if constexpr (G::KV4) {
-      // four reads at a time (keys of steps 2 x and 2 x + 1, tile d of the output)
+      // Fragment f: keys of steps 2 y and 2 y + 1, tile d of the output, f = y DT + d.
+      // Codes of four fragments at a time, scales of the next fragment while this one
+      // is multiplied (the compiler would ask for them when they are needed).
+      constexpr int NF = G::PS / 2 * G::DT, KB = G::MT == 16 ? 16 : 8;
       const int dh = G::MT == 32 ? (lane >> 4) & 1 : 0;
-      unrolled<G::PS / 2 * G::DT / 4>([&](auto blk) {
+      const _Float16* const v_sc = v_tab + dh * G::TK + 4 * g;
+      v4h vs[2][4];   // the scales of the lane's 16 keys, of this fragment and the next
+      auto scales_of = [&](int f, v4h (&to)[4]) {
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+          to[k4] = *(const v4h*)(v_sc + f % G::DT * (G::MT / 16) * G::TK + f / G::DT * 2 * G::KS + k4 * KB);
+      };
+      scales_of(0, vs[0]);
+      unrolled<NF / 4>([&](auto blk) {
         constexpr int F0 = 4 * decltype(blk)::value;
         auto at_key = [](int f) constexpr { return decltype(v_at)::value + f / G::DT * 2 * G::KS * G::RB; };
         uint32_t ad[4];
@@ -757,22 +775,24 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
         read_tr4<at_key(F0), at_key(F0 + 1), at_key(F0 + 2), at_key(F0 + 3)>(x, ad);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          constexpr int DT = G::DT, KB = G::MT == 16 ? 16 : 8;
-          const int y = (F0 + j) / DT, d = (F0 + j) % DT;
-          v2h vs[8];   // the scales of the lane's 16 keys
+          const int f = F0 + j, y = f / G::DT, d = f % G::DT;
+          if (f + 1 < NF) scales_of(f + 1, vs[(f + 1) & 1]);
+          __builtin_amdgcn_sched_barrier(0);
+          const v4h(&sc)[4] = vs[f & 1];
+          v2h pair[8];
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
-            const v4h w = *(const v4h*)(v_tab + (d * G::MT / 16 + dh) * G::TK + y * 2 * G::KS + k4 * KB + 4 * g);
-            vs[2 * k4] = __builtin_shufflevector(w, w, 0, 1);
-            vs[2 * k4 + 1] = __builtin_shufflevector(w, w, 2, 3);
+            pair[2 * k4] = __builtin_shufflevector(sc[k4], sc[k4], 0, 1);
+            pair[2 * k4 + 1] = __builtin_shufflevector(sc[k4], sc[k4], 2, 3);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int st2 = 2 * y + h;
             const v8h pb = __builtin_bit_cast(
                 v8h, (v4i{(int)p[4 * st2], (int)p[4 * st2 + 1], (int)p[4 * st2 + 2], (int)p[4 * st2 + 3]}));
-            o[d] = mfma(e2m1x8_pairs((uint32_t)x[j][h], vs + 4 * h), pb, o[d]);
+            o[d] = mfma(e2m1x8_pairs((uint32_t)x[j][h], pair + 4 * h), pb, o[d]);
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
       });
       return;
@@ -1094,6 +1114,55 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Widens the pages of an NVFP4 cache that some new token of a request can see to
+// bf16, which holds every value exactly, and writes the table that names them: a
+// workgroup per page, 16 values of a row per lane.  Bound by HBM's writes.
+template <int D>
+__global__ __launch_bounds__(256) void k_widen(AttnArgs a) {
+  constexpr int LPR = D / 16;
+  const int req = blockIdx.x / a.wide_pages, j = blockIdx.x % a.wide_pages;
+  if (threadIdx.x == 0) a.wide_table[blockIdx.x] = blockIdx.x;
+  const Span span = token_span(a.b.q_start, req, a.b.tokens);
+  const int kv = kv_bound(a.b.kv_lens[req], a.wide_pages, a.c.page_shift);
+  const int page_size = 1 << a.c.page_shift, first = j << a.c.page_shift;
+  if (span.n <= 0 || first >= kv) return;
+  const KeyRange range = key_range(kv - span.n, kv - 1, a.window, a.sinks);
+  if (first + page_size - 1 <= range.from && first >= range.sinks) return;
+  const int id = a.b.table[req * a.b.table_stride + j];
+  const bool there = page_there(id, a.c.num_pages);
+  const int items = page_size * a.c.kv_heads * LPR;
+  const int64_t out = (int64_t)blockIdx.x * items * 32;
+  uint8_t* const v_pool = a.wide + (int64_t)a.b.requests * a.wide_pages * items * 32;
+  for (int it = threadIdx.x; it < items; it += 256) {
+    const int i = it % LPR, row = it / LPR, head = row >> a.c.page_shift, key = row & (page_size - 1);
+    const uint64_t at = there ? row_offset(key, id, a.c.page_shift, a.c.page, a.c.token) + head * a.c.head + 8 * i : 0;
+    const uint64_t s_at = there ? row_offset(key, id, a.c.page_shift, a.c.s_page, a.c.s_token) + head * a.c.s_head + i : 0;
+    v2i code[2] = {{0, 0}, {0, 0}};
+    uint32_t sc[2] = {0, 0};
+    if (there) {
+      code[0] = *(const v2i*)(a.c.k + at);
+      code[1] = *(const v2i*)(a.c.v + at);
+      sc[0] = ((const uint8_t*)a.c.k_scale)[s_at];
+      sc[1] = ((const uint8_t*)a.c.v_scale)[s_at];
+    }
+#pragma unroll
+    for (int kv2 = 0; kv2 < 2; ++kv2) {
+      v2h s0, s1;
+      e4m3x2_scales(sc[kv2], s0, s1);
+      const float unit = kv2 ? a.c.v_unit : a.c.k_unit;
+      v4i* const to = (v4i*)((kv2 ? v_pool : a.wide) + out + (int64_t)it * 32);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v8h v = e2m1x8_to_f16((uint32_t)code[kv2][h], s0);
+        float f[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) f[x] = (float)v[x] * unit;
+        to[h] = pack8_bf16(f);
+      }
+    }
+  }
+}
+
 // The kernel for a call whose largest request has `rows` rows per kv head.
 // Up to 16 and 32 rows each wave takes all of them and a part of the keys,
 // without barriers; up to 64, two waves share the keys of two; beyond, four
@@ -1114,7 +1183,7 @@ auto visit_rows(int64_t rows, F f) {
   if constexpr (FMT == OCQ_CACHE_NVFP4) {
     if (rows <= 16) return f(Geo<D, FMT, 16, 1, D == 256 ? 2 : 4, 64, D == 256 ? 1 : 2>{});
     if constexpr (D < 256)
-      if (rows <= 32) return f(Geo<D, FMT, 32, 1, 4, 64, 2>{});
+      if (rows <= 32) return f(Geo<D, FMT, 32, 1, 4, D == 128 ? 32 : 64, 2>{});
     if (rows <= 64) return f(Geo<D, FMT, 32, 2, 2, 64, D == 256 ? 1 : 2>{});
     return f(Geo<D, FMT, 32, 4, 1, D == 256 ? 32 : 64, D == 256 ? 1 : 2>{});
   } else {
@@ -1181,8 +1250,24 @@ AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads,
   });
 }
 
-int launch_attn(const AttnArgs& a, void* stream) {
+int launch_attn(const AttnArgs& codes, void* stream) {
   hipStream_t st = (hipStream_t)stream;
+  AttnArgs a = codes;
+  if (a.wide) {
+    const dim3 grid((unsigned)(a.b.requests * a.wide_pages)), block(256);
+    if (a.dim == 64) hipLaunchKernelGGL((k_widen<64>), grid, block, 0, st, codes);
+    else if (a.dim == 128) hipLaunchKernelGGL((k_widen<128>), grid, block, 0, st, codes);
+    else hipLaunchKernelGGL((k_widen<256>), grid, block, 0, st, codes);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+    const int64_t row = a.dim * 2, head = row << a.c.page_shift, page = head * a.c.kv_heads;
+    a.format = OCQ_CACHE_BF16;
+    a.c = CacheArgs{codes.wide, codes.wide + (int64_t)a.b.requests * a.wide_pages * page, nullptr, nullptr, head, 0,
+                    (uint32_t)page, (uint32_t)row, 0, 0, a.b.requests * a.wide_pages, codes.c.page_shift, codes.c.kv_heads,
+                    1.0f, 1.0f};
+    a.b.table = codes.wide_table;
+    a.b.table_stride = a.b.max_pages = a.wide_pages;
+  }
   return (int)visit(a.dim, a.format, (int64_t)a.max_new * a.group,
                     [&](auto geo) { return run<decltype(geo)>(a, st); });
 }

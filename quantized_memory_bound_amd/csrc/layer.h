@@ -74,6 +74,11 @@ struct AttnArgs {
   float* part_o;             // [part_rows][dim]
   float* part_lse;           // [part_rows]
   uint32_t* counters;        // [OCQ_ATTENTION_COUNTERS], 0 between calls
+  // NVFP4 calls of many rows: room for every request's keys and values in bf16, `wide_pages`
+  // pages a request, and for their page table; null: the codes are attended
+  uint8_t* wide;
+  int32_t* wide_table;
+  int wide_pages;
 };
 
 // The values that an E4M3 or NVFP4 cache stands for, [pages][kv_heads][page_size][dim] bf16.
@@ -90,6 +95,29 @@ struct AttnPlan {
   size_t part_rows;          // rows of partial outputs in the workspace
   double lanes = 0;          // of the larger launch (a launch holds fewer than 2^32)
 };
+
+// Pages a request whose keys and values a call over an NVFP4 cache widens to bf16
+// first (0: it does not), and the bytes that they take.  Codes that every 32 rows
+// convert for themselves keep the vector unit busy; widened once they cost a pass
+// through memory.  32 heads of 128 on 8 kv heads, two requests over up to 10007 keys,
+// us with and without: 512 rows a kv head 76 (69), 1024 111 (113), 2048 177 (187),
+// 8192 466 (573); 16 requests, 2048 rows over 700 keys 114 (113).
+constexpr int kWideRows = 1024;
+constexpr int64_t kWideBytes = (int64_t)1 << 30;
+inline int64_t wide_bytes(int requests, int pages, int page_size, int kv_heads, int dim) {
+  return (int64_t)requests * pages * ((int64_t)page_size * kv_heads * dim * 4 + 4);
+}
+inline int wide_pages(int format, int requests, int64_t rows, int max_kv, int max_pages, int page_size, int kv_heads,
+                      int dim) {
+  if (format != OCQ_CACHE_NVFP4 || rows < kWideRows) return 0;
+  int64_t pages = ((int64_t)max_kv + page_size - 1) / page_size;
+  pages = pages < max_pages ? pages : max_pages;
+  // (a page of the widened cache is below 2^32 bytes, as of any cache)
+  if (pages < 1 || (int64_t)page_size * kv_heads * dim * 2 > 0xFFFFFFFFll || (int64_t)requests * pages >= (int64_t)1 << 31 ||
+      wide_bytes(requests, (int)pages, page_size, kv_heads, dim) > kWideBytes)
+    return 0;
+  return (int)pages;
+}
 
 // Lanes of one launch of the norm and the append (it holds fewer than 2^32); rows
 // or tokens that take more are several launches.

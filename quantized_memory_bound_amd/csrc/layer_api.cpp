@@ -10,9 +10,21 @@ namespace {
 
 int max_new(const ocq_token_batch* b) { return b->max_new < b->tokens ? b->max_new : b->tokens; }
 
-AttnPlan plan_of(int heads, const ocq_kv_cache* c, const ocq_token_batch* b, int window, int sinks) {
-  return attn_plan(b->tokens, b->requests, max_new(b), b->max_kv, heads, c->kv_heads, c->head_dim, c->format, window,
-                   sinks, (int64_t)b->max_pages * c->page_size);
+struct CallPlan {
+  AttnPlan attn;
+  int wide;                  // pages a request that are widened first
+  size_t wide_bytes, bytes;  // of the workspace: those, and all
+};
+CallPlan plan_of(int heads, const ocq_kv_cache* c, const ocq_token_batch* b, int window, int sinks) {
+  CallPlan p{};
+  p.wide = wide_pages(c->format, b->requests, (int64_t)max_new(b) * (heads / c->kv_heads), b->max_kv, b->max_pages,
+                      c->page_size, c->kv_heads, c->head_dim);
+  p.attn = attn_plan(b->tokens, b->requests, max_new(b), b->max_kv, heads, c->kv_heads, c->head_dim,
+                     p.wide ? OCQ_CACHE_BF16 : c->format, window, sinks,
+                     (int64_t)(p.wide ? p.wide : b->max_pages) * c->page_size);
+  if (p.wide) p.wide_bytes = ((size_t)wide_bytes(b->requests, p.wide, c->page_size, c->kv_heads, c->head_dim) + 15) & ~(size_t)15;
+  p.bytes = p.wide_bytes + p.attn.part_rows * (c->head_dim + 1) * sizeof(float);
+  return p;
 }
 
 }  // namespace
@@ -110,7 +122,7 @@ size_t ocq_attention_workspace_bytes(int heads, const ocq_kv_cache* cache, const
   set_error(OCQ_OK, "");
   if (check_cache(cache) != OCQ_OK || check_batch(batch, cache, heads) != OCQ_OK || window < 0 || sinks < 0) return 0;
   if (batch->requests == 0 || batch->tokens == 0) return 0;
-  return plan_of(heads, cache, batch, window, sinks).part_rows * (cache->head_dim + 1) * sizeof(float);
+  return plan_of(heads, cache, batch, window, sinks).bytes;
 }
 
 ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_t q_head_stride, int heads,
@@ -131,9 +143,10 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
     return invalid("device pointers must be 16-byte aligned");
   if (!stride_ok(q_token_stride, 8) || !stride_ok(q_head_stride, 8))
     return invalid("strides must be multiples of 8, not negative");
-  const AttnPlan plan = plan_of(heads, cache, batch, window, sinks);
+  const CallPlan call = plan_of(heads, cache, batch, window, sinks);
+  const AttnPlan& plan = call.attn;
   if (plan.lanes >= 4294967296.0) return unsupported("too many row tiles for one launch");
-  const size_t need = plan.part_rows * (cache->head_dim + 1) * sizeof(float);
+  const size_t need = call.bytes;
   if (workspace_bytes < need)
     return set_error(OCQ_ERR_BUFFER_TOO_SMALL, "workspace_bytes < ocq_attention_workspace_bytes()");
   if (need && !workspace_dev) return invalid("null workspace");
@@ -158,8 +171,14 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
   a.groups = plan.groups;
   a.slots = plan.slots;
   a.counters = (uint32_t*)batch->counters_dev;
-  a.part_o = (float*)workspace_dev;
-  a.part_lse = (float*)workspace_dev + plan.part_rows * cache->head_dim;
+  a.part_o = (float*)((uint8_t*)workspace_dev + call.wide_bytes);
+  a.part_lse = a.part_o + plan.part_rows * cache->head_dim;
+  if (call.wide) {
+    a.wide = (uint8_t*)workspace_dev;
+    a.wide_pages = call.wide;
+    a.wide_table = (int32_t*)(a.wide + wide_bytes(batch->requests, call.wide, cache->page_size, cache->kv_heads,
+                                                  cache->head_dim) - (int64_t)4 * batch->requests * call.wide);
+  }
   const int rc = launch_attn(a, stream);
   return rc ? hip_error(rc) : OCQ_OK;
 }
