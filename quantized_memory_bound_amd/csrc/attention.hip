@@ -115,7 +115,8 @@ struct Geo {
   static constexpr int VTAB = KV4 ? TK * SB * 2 : 0;                    // a wave's fp16 scales of V, key by key
   static constexpr int RING = WK * NST * (KSTG + VSTG);
   static constexpr int QI = (PART / 1024 + WR - 1) / WR;                // K (or V) loads per wave and stage
-  static constexpr int SI = KV4 ? SCB / 256 : KV8 ? 1 : 0;              // loads of its scales
+  static constexpr int SL = KV4 ? SCB / 256 : 1;                        // loads of its scales, and a wave's of them
+  static constexpr int SI = KV4 ? (SL + WR - 1) / WR : KV8 ? 1 : 0;
   static constexpr int PW = 2 * QI + 1 + 2 * SI;                        // all loads per wave and stage
   static constexpr int KW = KV4 ? (RB / LG_(MT) >= 16 ? 4 : 2) : KV8 ? 2 : 1;   // steps of S that a read of K serves
   static constexpr int AHEAD = WR > 1 ? NST - 1 : NST;                  // stages on their way, see the ring
@@ -509,9 +510,10 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   auto tile_key = [&](int st) { return tile_of(pc.tiles, pc.s0 + st) * G::TT + wk * G::TK; };
   // load i of the stage's PART / 1024 (where waves outnumber them, some come twice)
   auto nth = [&](int i) { return (i * G::WR + wr) % (G::PART / 1024); };
+  auto s_nth = [&](int i) { return G::SL == 1 ? 0 : (i * G::WR + wr) % G::SL; };
   auto q_row = [&](int i) {   // row of load i of K and V, or (from i = QI) of the scales
     if (i < G::QI) return (nth(i) * 64 + lane) / G::CH;
-    return G::KV4 ? ((i - G::QI) * 64 + lane) / (G::SB / 4) % G::TK : lane % G::TK;
+    return G::KV4 ? (s_nth(i - G::QI) * 64 + lane) / (G::SB / 4) % G::TK : lane % G::TK;
   };
   uint32_t part[G::QI], s_part[G::SI + 1];
 #pragma unroll
@@ -568,7 +570,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
     for (int i = 0; i < G::SI; ++i) {
       s_src[i] = ks_head + (uint64_t)(uint32_t)(key0 & page_mask) * a.c.s_token * SE +
                  (uint64_t)(uint32_t)sid[i] * a.c.s_page * SE + s_part[i];
-      dma4(s_there[i] ? s_src[i] : zero, to + G::PART + i * 256);
+      dma4(s_there[i] ? s_src[i] : zero, to + G::PART + s_nth(i) * 256);
     }
   };
   auto issue_v = [&](int slot) {
@@ -576,7 +578,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
 #pragma unroll
     for (int i = 0; i < G::QI; ++i) dma16<G::EVEN>(there[i] ? src[i] + v_less_k : zero, to + nth(i) * 1024);
 #pragma unroll
-    for (int i = 0; i < G::SI; ++i) dma4(s_there[i] ? s_src[i] + vs_less_ks : zero, to + G::PART + i * 256);
+    for (int i = 0; i < G::SI; ++i) dma4(s_there[i] ? s_src[i] + vs_less_ks : zero, to + G::PART + s_nth(i) * 256);
   };
 
   acc_t o[G::DT];
