@@ -193,10 +193,11 @@ __device__ __forceinline__ double exp64(double y) {
 
 // ---------------------------------------------------------------- which drafts stay
 
+constexpr int kRows = kThreads / 16;    // rows of a request compared at a time
 struct ChooseShared {
-  double z[64];
-  float top[64];
-  int at[64], id[64], first;
+  double z[kRows];
+  float top[kRows];
+  int at[kRows], id[kRows], first;
 };
 
 // The draft's rows before request r's: one less than its tokens for each request
@@ -229,15 +230,15 @@ __device__ __forceinline__ Draft draft_of(const DraftArgs& a, int t, int i, int 
   return d;
 }
 
-// By all threads of a workgroup; four lanes share a row's parts, 64 rows at a time.
+// By all threads of a workgroup; 16 lanes share a row's parts (64 at most).
 template <class T, class Q, bool PROBS>
 __device__ __forceinline__ Choice choose(const DraftArgs& a, int r, const Span& sp, int64_t before, float temp,
                                          ChooseShared& sh) {
   const int n = sp.n < 0 ? 0 : sp.n;
   const double inv_t = 1.0 / (double)temp;
   Choice c{0.0, inv_t, 0.0, -1, sp.t0, n, 0, 1, -1, -1};
-  for (int i0 = 0; i0 < n; i0 += 64) {
-    const int row = threadIdx.x >> 2, i = i0 + row, t = sp.t0 + (i < n ? i : 0);
+  for (int i0 = 0; i0 < n; i0 += kRows) {
+    const int row = threadIdx.x >> 4, i = i0 + row, t = sp.t0 + (i < n ? i : 0);
     Draft d;
     if constexpr (PROBS) {
       d = draft_of<T, Q>(a, t, i, n, before);
@@ -250,21 +251,26 @@ __device__ __forceinline__ Choice choose(const DraftArgs& a, int r, const Span& 
     double z = 0.0;
     if constexpr (!PROBS) {
       const RowStat* const st = a.stats + (size_t)t * a.splits;
-#pragma unroll 4
-      for (int k = threadIdx.x & 3; k < a.splits; k += 4) {
-        const uint64_t ta = load_agent(&st[k].top_at);
-        best(top, at, __uint_as_float((uint32_t)ta), (int)(ta >> 32));
+      uint64_t ta[4];
+      double part[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {      // all of them on their way together
+        const int k = (threadIdx.x & 15) + 16 * b;
+        ta[b] = load_agent(&st[k < a.splits ? k : 0].top_at);
+        part[b] = load_agent(&st[k < a.splits ? k : 0].sum);
       }
 #pragma unroll
-      for (int b = 1; b < 4; b <<= 1) best(top, at, __shfl_xor(top, b), __shfl_xor(at, b));
-#pragma unroll 2
-      for (int k = threadIdx.x & 3; k < a.splits; k += 4) {
-        const float v = __uint_as_float((uint32_t)load_agent(&st[k].top_at));
-        const double s = load_agent(&st[k].sum);
-        z += temp == 0.0f || s == 0.0 ? s : s * exp64(((double)v - (double)top) * inv_t);
+      for (int b = 0; b < 4; ++b) best(top, at, __uint_as_float((uint32_t)ta[b]), (int)(ta[b] >> 32));
+#pragma unroll
+      for (int b = 1; b < 16; b <<= 1) best(top, at, __shfl_xor(top, b), __shfl_xor(at, b));
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float v = __uint_as_float((uint32_t)ta[b]);
+        if ((int)(threadIdx.x & 15) + 16 * b < a.splits)
+          z += temp == 0.0f || part[b] == 0.0 ? part[b] : part[b] * exp64(((double)v - (double)top) * inv_t);
       }
 #pragma unroll
-      for (int b = 1; b < 4; b <<= 1) z += __shfl_xor(z, b);
+      for (int b = 1; b < 16; b <<= 1) z += __shfl_xor(z, b);
     }
     bool keep = false;
     if (d.x >= 0) {
@@ -274,8 +280,8 @@ __device__ __forceinline__ Choice choose(const DraftArgs& a, int r, const Span& 
     }
     if (threadIdx.x == 0) sh.first = 0x7FFFFFFF;
     __syncthreads();
-    if (i < n && !keep && (threadIdx.x & 3) == 0) atomicMin(&sh.first, i);
-    if ((threadIdx.x & 3) == 0) {
+    if (i < n && !keep && (threadIdx.x & 15) == 0) atomicMin(&sh.first, i);
+    if ((threadIdx.x & 15) == 0) {
       sh.z[row] = z;
       sh.top[row] = top;
       sh.at[row] = at;
@@ -635,6 +641,7 @@ __global__ __launch_bounds__(kThreads) void k_next(DraftArgs a) {
     c = a.choices[r];
   }
   if (!c.draw) return;
+  const float u = a.u_next[r];
   Sums* const parts = (Sums*)a.parts + (size_t)r * a.chunks;
   const bool two = !PROBS && c.q_row >= 0;              // Z is still to be found
   if (two) {
@@ -649,19 +656,16 @@ __global__ __launch_bounds__(kThreads) void k_next(DraftArgs a) {
   double mine = lane < a.chunks ? load_agent(&parts[lane].e) : 0.0, inv_z = 1.0;
   bool again = false, none = false;
   if (two) {
-    const double z = sum64(mine);
-    inv_z = 1.0 / z;
-    double near = 0.0;
-    mine = 0.0;
-    if (lane < a.chunks) {
-      mine = load_agent(&parts[lane].e_s) * inv_z - load_agent(&parts[lane].q_s);
-      near = load_agent(&parts[lane].near);
-      mine = mine < 0.0 ? 0.0 : mine;
-    }
+    const int k = lane < a.chunks ? lane : 0;
+    const double e_s = load_agent(&parts[k].e_s), q_s = load_agent(&parts[k].q_s), near = load_agent(&parts[k].near);
+    __builtin_amdgcn_sched_barrier(0);                  // (all loads before the first wait)
+    inv_z = 1.0 / sum64(mine);
+    mine = lane < a.chunks ? e_s * inv_z - q_s : 0.0;
+    mine = mine < 0.0 ? 0.0 : mine;
     const double off = __builtin_fabs(c.z * inv_z - 1.0);
-    again = off > kNear * 0.5 || off * sum64(near) > kOff * sum64(mine);
+    again = off > kNear * 0.5 || off * sum64(lane < a.chunks ? near : 0.0) > kOff * sum64(mine);
   }
-  Found f = find_chunk(mine, a.u_next[r], none);
+  Found f = find_chunk(mine, u, none);
   bool plain = false;
   for (int turn = 0; turn < 2; ++turn) {
     // the chunks' weights with Z, or, where nothing is left of p, of p itself
@@ -675,7 +679,7 @@ __global__ __launch_bounds__(kThreads) void k_next(DraftArgs a) {
       if (threadIdx.x == 0) s_part[k] = one;
     }
     __syncthreads();
-    f = find_chunk(lane < a.chunks ? s_part[lane] : 0.0, a.u_next[r], none);
+    f = find_chunk(lane < a.chunks ? s_part[lane] : 0.0, u, none);
     __syncthreads();
   }
   const int next = f.chunk < 0 ? -1 : place_in<T, Q, PROBS>(a, c, f.chunk, f.before, f.t, inv_z, plain, s, s_at);

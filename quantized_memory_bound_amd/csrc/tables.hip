@@ -13,7 +13,9 @@
 // One workgroup sums over the requests.  A small step (kSmall tokens, one request a
 // thread) ends in the same launch: a thread per page that moves and per token,
 // its request found in LDS.  A large one hands each request's sums to a second
-// launch with a workgroup per request.  Latency bounds it: three dependent reads.
+// launch with workgroups of every request.  Latency bounds it: 16 requests of 13 tokens
+// 4.3 us; 2048 requests, 128 of them starting on up to 4096 tokens each, 5.7 and 11
+// (their 5 MB: 1).
 #include "kcommon.h"
 #include "step.h"
 
@@ -39,21 +41,28 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-__device__ __forceinline__ int ring_at(const TableArgs& a, uint64_t n) { return (int)(n % (uint64_t)a.ring_size); }
-
-// page j of a request's row after the step, from what was there before it
-__device__ __forceinline__ int page_of(const TableArgs& a, const Rec& q, int r, int j, uint64_t taken) {
-  if (j < 0 || j >= a.max_pages) return -1;
-  if (j < q.held) return a.table[r * a.table_stride + j];
-  return j < q.got ? a.ring[ring_at(a, taken + (uint64_t)(q.take + j - q.held))] : -1;
+// The place `n` entries behind place `from` of the ring, both below its size (a
+// remainder in 64 bits for every token took longer than all else; counts that no step
+// leaves give any n).
+__device__ __forceinline__ int ring_at(const TableArgs& a, int from, int n) {
+  uint32_t at = (uint32_t)from + (uint32_t)n;
+  at = at >= (uint32_t)a.ring_size ? at - (uint32_t)a.ring_size : at;
+  return at < (uint32_t)a.ring_size ? (int)at : 0;
 }
 
-__device__ __forceinline__ void put_token(const TableArgs& a, const Rec& q, int r, int t, int i, uint64_t taken) {
-  const int place = (int)((unsigned)q.kept + (unsigned)i);   // (past 2^31: no page)
-  if (a.slots) {
-    const int page = page_of(a, q, r, place >> a.page_shift, taken);
-    a.slots[t] = page >= 0 ? ((int64_t)page << a.page_shift) + (place & ((1 << a.page_shift) - 1)) : -1;
-  }
+// page j of a request's row after the step, from what was there before it
+__device__ __forceinline__ int page_of(const TableArgs& a, const Rec& q, int r, int j, int taken) {
+  if (j < 0 || j >= a.max_pages) return -1;
+  if (j < q.held) return a.table[r * a.table_stride + j];
+  return j < q.got ? a.ring[ring_at(a, taken, q.take + j - q.held)] : -1;
+}
+
+// place of a request's new token i (past 2^31: below 0, without a page)
+__device__ __forceinline__ int place_of(const Rec& q, int i) { return (int)((unsigned)q.kept + (unsigned)i); }
+
+__device__ __forceinline__ void put_token(const TableArgs& a, const Rec& q, int r, int t, int i, int page) {
+  const int place = place_of(q, i);
+  if (a.slots) a.slots[t] = page >= 0 ? ((int64_t)page << a.page_shift) + (place & ((1 << a.page_shift) - 1)) : -1;
   if (a.positions) a.positions[t] = place;
   if (a.owners) a.owners[t] = r;
 }
@@ -65,13 +74,13 @@ __device__ __forceinline__ void no_token(const TableArgs& a, int t) {
 }
 
 // (numbers of tokens whose sums pass 2^31 give any j)
-__device__ __forceinline__ void take_page(const TableArgs& a, const Rec& q, int r, int j, uint64_t taken) {
+__device__ __forceinline__ void take_page(const TableArgs& a, const Rec& q, int r, int j, int taken) {
   if (j < q.held || j >= q.need) return;
-  a.table[r * a.table_stride + j] = j < q.got ? a.ring[ring_at(a, taken + (uint64_t)(q.take + j - q.held))] : -1;
+  a.table[r * a.table_stride + j] = j < q.got ? a.ring[ring_at(a, taken, q.take + j - q.held)] : -1;
 }
-__device__ __forceinline__ void give_page(const TableArgs& a, const Rec& q, int r, int j, uint64_t given) {
+__device__ __forceinline__ void give_page(const TableArgs& a, const Rec& q, int r, int j, int given) {
   if (j < q.need || j >= q.held) return;
-  a.ring[ring_at(a, given + (uint64_t)(q.give + j - q.need))] = a.table[r * a.table_stride + j];
+  a.ring[ring_at(a, given, q.give + j - q.need)] = a.table[r * a.table_stride + j];
 }
 
 // the last of n (> 0) sorted numbers that is not above v, the first of them not above it
@@ -89,7 +98,8 @@ __global__ __launch_bounds__(kWide) void k_sums(TableArgs a) {
   __shared__ Rec s_rec[SMALL ? kWide : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint64_t taken = (uint64_t)a.counts_in[0], given = (uint64_t)a.counts_in[1];
-  const uint64_t span = given - taken;
+  const uint64_t span = given - taken, size = (uint64_t)a.ring_size;
+  const int from = (int)(taken % size), to = (int)(given % size);   // where entries come from and go to
   const int free = (int64_t)span < 0 ? 0 : span > (uint64_t)a.ring_size ? a.ring_size : (int)span;
   int c_new = 0, c_want = 0, c_back = 0, over = 0;
   for (int base = 0; base < a.requests; base += kWide) {
@@ -166,9 +176,9 @@ __global__ __launch_bounds__(kWide) void k_sums(TableArgs a) {
     a.counts_out[0] = (int64_t)(taken + (uint64_t)(c_want < free ? c_want : free));
     a.counts_out[1] = (int64_t)(given + (uint64_t)c_back);
     if constexpr (!SMALL) {
-      ((uint64_t*)a.records)[0] = taken;
-      ((uint64_t*)a.records)[1] = given;
-      a.records[4] = c_new;
+      a.records[0] = from;
+      a.records[1] = to;
+      a.records[2] = c_new;
     }
   }
   if constexpr (SMALL) {
@@ -181,15 +191,17 @@ __global__ __launch_bounds__(kWide) void k_sums(TableArgs a) {
         continue;
       }
       const int r = last_le(s_start, n, t);
-      put_token(a, s_rec[r], r, t, t - s_rec[r].start, taken);
+      const Rec& q = s_rec[r];
+      const int i = t - q.start;
+      put_token(a, q, r, t, i, a.slots ? page_of(a, q, r, place_of(q, i) >> a.page_shift, from) : -1);
     }
     for (int i = threadIdx.x; i < c_want; i += kWide) {
       const int r = last_le(s_take, n, i);
-      take_page(a, s_rec[r], r, s_rec[r].held + i - s_take[r], taken);
+      take_page(a, s_rec[r], r, s_rec[r].held + i - s_take[r], from);
     }
     for (int i = threadIdx.x; i < c_back; i += kWide) {
       const int r = last_le(s_give, n, i);
-      give_page(a, s_rec[r], r, s_rec[r].need + i - s_give[r], given);
+      give_page(a, s_rec[r], r, s_rec[r].need + i - s_give[r], to);
     }
   }
 }
@@ -197,14 +209,27 @@ __global__ __launch_bounds__(kWide) void k_sums(TableArgs a) {
 // A request's pages and tokens; grid.y workgroups share them.
 __global__ __launch_bounds__(256) void k_fill(TableArgs a) {
   const int r = blockIdx.x, first = blockIdx.y * 256 + threadIdx.x, step = gridDim.y * 256;
-  const uint64_t taken = ((const uint64_t*)a.records)[0], given = ((const uint64_t*)a.records)[1];
+  const int taken = a.records[0], given = a.records[1];
   const Rec q = ((const Rec*)a.records)[1 + r];
-  if (q.start >= 0)
-    for (int i = first; i < q.fresh && i < a.tokens - q.start; i += step) put_token(a, q, r, q.start + i, i, taken);
+  if (q.start >= 0) {
+    // four tokens of a lane at a time: their pages are on their way together
+    const int n = q.fresh < a.tokens - q.start ? q.fresh : a.tokens - q.start;
+    for (int i0 = first; i0 < n; i0 += 4 * step) {
+      int page[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * step;
+        page[k] = a.slots && i < n ? page_of(a, q, r, place_of(q, i) >> a.page_shift, taken) : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i0 + k * step < n) put_token(a, q, r, q.start + i0 + k * step, i0 + k * step, page[k]);
+    }
+  }
   for (int j = q.held + first; j < q.need; j += step) take_page(a, q, r, j, taken);
   for (int j = q.need + first; j < q.held; j += step) give_page(a, q, r, j, given);
   if (r == a.requests - 1)
-    for (int t = (a.records[4] < 0 ? 0 : a.records[4]) + first; t < a.tokens; t += step) no_token(a, t);
+    for (int t = (a.records[2] < 0 ? 0 : a.records[2]) + first; t < a.tokens; t += step) no_token(a, t);
 }
 
 bool small(int requests, int tokens) { return requests <= kWide && tokens <= kSmall; }
@@ -222,7 +247,9 @@ int launch_tables(const TableArgs& a, void* stream) {
     return (int)hipGetLastError();
   }
   hipLaunchKernelGGL((k_sums<false>), dim3(1), dim3(kWide), 0, st, a);
-  int y = a.tokens / (a.requests * 256) + 1;
+  // (2048 requests, 128 of them starting on 4096 tokens: 13.0 us, twice as many
+  // workgroups 11.0)
+  int y = 2 * (a.tokens / (a.requests * 256) + 1);
   y = y > 64 ? 64 : y;
   hipLaunchKernelGGL(k_fill, dim3((unsigned)a.requests, (unsigned)y), dim3(256), 0, st, a);
   return (int)hipGetLastError();

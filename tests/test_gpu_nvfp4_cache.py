@@ -7,7 +7,9 @@ asked for.  Attention: q, k and v are exact in the products, probabilities are r
 are fp32 sums of exact products, 2^-20 of their size (at most 2^5 here but where a test says more), which the exponential
 turns into a relative 2^-15 of each weight: |out - ref| <= 2^-8 |ref| (the output's own rounding) + (2^-11 + 2^-14) sum_j
 w_j |v_j|.  Below fp16's normal range a rounding is absolute, 2^-25, of probabilities whose largest is 2^7 at least: 2^-32
-sum_j |v_j| more over the keys that a token sees.  The log-sum-exp as for the other formats.
+sum_j |v_j| more over the keys that a token sees.  Calls of 1024 rows a kv head and more go over a bf16 copy of the
+pages: their probabilities are rounded to bf16, 2^-8 relative in the place of 2^-11.  The log-sum-exp as for the other
+formats.
 """
 
 import math
@@ -100,7 +102,9 @@ def check_attention(q, cache, batch, news, kvs, scale=None, window=0, sinks=0, s
     assert torch.equal(torch.isinf(lse), empty) and not out[empty].float().any()
     d = (lse.double() - rl)[~empty].abs()
     assert not d.numel() or d.max() <= 2.0 ** -18 + rl[~empty].abs().max() * 2.0 ** -18
-    tol = ref.abs() * 2.0 ** -8 + mag[0] * (2.0 ** -11 + score * 2.0 ** -19) + mag[1] * 2.0 ** -32 + 1e-30
+    widened = max(news) * q.shape[1] // cache.kv_heads >= 1024
+    half = 2.0 ** -8 if widened else 2.0 ** -11
+    tol = ref.abs() * 2.0 ** -8 + mag[0] * (half + score * 2.0 ** -19) + mag[1] * 2.0 ** -32 + 1e-30
     bad = ~((out.double() - ref).abs() <= tol)
     assert not bad.any(), "%d of %d off, worst %.3g" % (int(bad.sum()), bad.numel(), float((out.double() - ref).abs().max()))
     return out, lse
@@ -158,6 +162,76 @@ def test_append(dim, rot, interleaved, order, page):
             at += 1
     for t, old in zip((cache.k, cache.v, cache.k_scale.view(torch.uint8), cache.v_scale.view(torch.uint8)), before):
         assert torch.equal(t, old)                                        # nothing else was written
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_of_many_tokens(interleaved):
+    """Prompts of uneven lengths in one call and in calls of few tokens: the same bits."""
+    g = _gen(4)
+    news, kvs, page = [700, 0, 1, 601, 5], [700, 40, 30, 900, 5], 16
+    batch, pages = make_batch(news, kvs, page, g)
+    rope = ocq.Rope.make(64, interleaved=interleaved, device=DEV)
+    q, k, v = _bf((sum(news), 5, 128), g), _bf((sum(news), 5, 128), g), _bf((sum(news), 5, 128), g)
+    whole, parts = (ocq.PagedKVCache.allocate(pages, page, 5, 128, nvfp4=True, device=DEV) for _ in range(2))
+    got = ocq.rope_append(q, k, v, rope, whole, batch)
+    at = 0
+    for r, (n, kv) in enumerate(zip(news, kvs)):
+        for i in range(0, n, 350):
+            m = min(350, n - i)
+            one = ocq.TokenBatch(torch.tensor([0, m], dtype=torch.int32, device=DEV),
+                                 torch.tensor([kv - n + i + m], dtype=torch.int32, device=DEV), batch.page_table[r:r + 1], m, kv)
+            rows = slice(at + i, at + i + m)
+            assert torch.equal(ocq.rope_append(q[rows], k[rows], v[rows], rope, parts, one), got[rows])
+        at += n
+    for a, b in ((whole.k, parts.k), (whole.v, parts.v), (whole.k_scale, parts.k_scale), (whole.v_scale, parts.v_scale)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (256, 1)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (333, 0), (100, 130)])
+def test_attention_of_many_rows(dim, page, window, sinks):
+    """Calls whose pages are widened first: ragged prompts, pages that are none, NaN behind the context and a window."""
+    g = _gen(dim + window)
+    news, kvs = [257, 3, 0, 700], [257, 900, 40, 1501]
+    batch, pages = make_batch(news, kvs, page, g)
+    cache = make_cache(pages, 2, page, dim, g, "tokens", (0.25, 2.0 ** 5))
+    used = torch.zeros((pages, page), dtype=torch.bool, device=DEV)
+    for r, kv in enumerate(kvs):
+        p = torch.arange(kv, device=DEV)
+        used[batch.page_table[r][p // page].long(), p % page] = True
+    for x in (cache.k_scale, cache.v_scale):
+        x.view(torch.uint8).transpose(1, 2)[~used] = 0x7F
+    if window == 333:
+        p = torch.arange(0, 1501 - 700 - 333 + 1, device=DEV)
+        for x in (cache.k_scale, cache.v_scale):
+            x.view(torch.uint8).transpose(1, 2)[batch.page_table[3][p // page].long(), p % page] = 0x7F
+    batch.page_table[1, 0], batch.page_table[3, 900 // page] = -1, pages + 5
+    q = _bf((sum(news), 4, dim), g)
+    many = q.repeat_interleave(2, 1)                       # 4 heads a kv head: 2800 rows
+    if window == 333:                                      # (what lies behind the window is 0 in the reference)
+        ref_cache = ocq.PagedKVCache(cache.k.clone(), cache.v.clone(), cache.k_scale.clone(), cache.v_scale.clone(), 0.25,
+                                     2.0 ** 5)
+        for x in (ref_cache.k_scale, ref_cache.v_scale):
+            u = x.view(torch.uint8)
+            u[u == 0x7F] = 0
+        out, lse = ocq.paged_attention(many, cache, batch, window=window, sinks=sinks, want_lse=True)
+        a, b = check_attention_bf16(many, ref_cache, batch, news, kvs, window, sinks)
+        assert torch.equal(out, a) and torch.equal(lse, b)
+    else:
+        check_attention_bf16(many, cache, batch, news, kvs, window, sinks)
+
+
+def check_attention_bf16(q, cache, batch, news, kvs, window, sinks):
+    """As over a bf16 cache: probabilities are rounded to bf16, 2^-8 of each weight."""
+    batch.of(len(q))
+    assert ocq.attention_workspace_bytes(q.shape[1], cache, batch, window, sinks) > sum(kvs) * 2 * cache.head_dim * 4
+    out, lse = ocq.paged_attention(q, cache, batch, window=window, sinks=sinks, want_lse=True)
+    ref, rl, mag = attention_ref(q, cache, batch, news, kvs, q.shape[2] ** -0.5, window, sinks)
+    assert not torch.isinf(rl).any()
+    d = (lse.double() - rl).abs()
+    assert d.max() <= 2.0 ** -18 + rl.abs().max() * 2.0 ** -18
+    assert torch.all((out.double() - ref).abs() <= ref.abs() * 2.0 ** -8 + mag[0] * 2.0 ** -8 + 1e-30)
+    return out, lse
 
 
 def test_append_codes_at_every_border():
