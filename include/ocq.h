@@ -469,9 +469,9 @@ ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_
  * scale > 0 and finite, window >= 0 (0: none), sinks >= 0 (0 without a
  * window).  Over NVFP4 caches both products are of fp16 operands: q after a power of
  * two of each row, the probabilities rounded to fp16; but where max_new x heads /
- * kv_heads is 1024 or more the pages are widened to bf16 in the workspace first, if
- * those of max_kv tokens a request fit 1 GiB (keys past max_kv are then not read),
- * and attended as a bf16 cache's.  Requests x kv heads x row tiles (of 16 to 128 of the max_new *
+ * kv_heads is 1024 or more the pages are widened to fp16 in the workspace first, if
+ * those of max_kv tokens a request fit 1 GiB (keys past max_kv are then not read).
+ * Requests x kv heads x row tiles (of 16 to 128 of the max_new *
  * heads / kv_heads rows) are one launch of fewer than 2^32 lanes, 64 to 256 a
  * tile; beyond that: OCQ_ERR_UNSUPPORTED.  Scores, softmax statistics and sums are fp32; probabilities are
  * rounded to bf16 for the second product.

@@ -59,7 +59,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLow = -3.4028234663852886e38f;   // below every score that is visible
 constexpr float kSlack = 8.0f;                    // see above
-// NVFP4: probabilities are fp16, up to 2^(8 + 7) of its 65504, so that only those
+// NVFP4, widened or not: probabilities are fp16, up to 2^(8 + 7) of its 65504, so that only those
 // below 2^-31 of the largest round as if they were 0
 constexpr float kUp = 7.0f;
 
@@ -106,6 +106,7 @@ struct Geo {
   static constexpr int MINW = MINW_, NST = 2;
   static constexpr int D = D_, MT = MT_, WR = WR_, WK = WK_, TK = TK_;
   static constexpr bool KV8 = FMT_ == OCQ_CACHE_E4M3, KV4 = FMT_ == OCQ_CACHE_NVFP4;
+  static constexpr bool F16 = KV4 || FMT_ == kWidened;                  // operands of the products: fp16, or bf16
   static constexpr int NW = WR * WK, THREADS = 64 * NW, ROWS = MT * WR;
   static constexpr int RB = KV4 ? D / 2 : KV8 ? D : 2 * D, CH = RB / 16;   // bytes and chunks of a row
   static constexpr int PART = TK * RB;                                  // K (or V) bytes of a key group's stage
@@ -462,11 +463,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   const int tok = live ? row / a.group : 0, head = kvh * a.group + (live ? row % a.group : 0);
   const int place = live ? base + tok : -1;
   const size_t at = (size_t)(t0 + tok) * a.heads + head;
-  typedef std::conditional_t<G::KV4, v8h, v8bf> operand;
+  typedef std::conditional_t<G::F16, v8h, v8bf> operand;
   operand q[G::QS];
   const uint16_t* qp = a.q + (t0 + tok) * a.q_token + head * a.q_head;
   float c = a.scale * kLog2e;
-  if constexpr (G::KV4) {
+  if constexpr (G::F16) {
     // Codes times their scales are exact in fp16, not all in bf16 with one
     // instruction less; q goes to fp16 after a power of two that brings the row's
     // largest value to 2^14 .. 2^15, which is exact down to 2^-28 of it (and off by
@@ -656,7 +657,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
       } else if constexpr (!G::KV8) {
 #pragma unroll
         for (int x = 0; x < G::QS; ++x) {
-          const v8bf ka = *(const v8bf*)(ring + at + (k_off[x] ^ f));
+          const operand ka = *(const operand*)(ring + at + (k_off[x] ^ f));
           s[kt] = mfma(ka, q[x], s[kt]);
         }
       } else {
@@ -732,7 +733,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
     }
     products(k_next, sb);
     const float* sc = (const float*)(ring + decltype(v_at)::value + G::PART);
-    const float from = G::KV4 ? kUp - m : -m;
+    const float from = G::F16 ? kUp - m : -m;
     uint32_t p[G::NKT * AN / 2];
 #pragma unroll
     for (int kt = 0; kt < G::NKT; ++kt)
@@ -750,8 +751,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
         // bf16 is what the matrix instruction takes beside bf16 (or converted)
         // values: an output is off by 0.0023 of its size where its own rounding
         // is 0.0017.  Two halves of each probability would double the products.
-        p[(kt * AN + 4 * i4) / 2] = G::KV4 ? pack_f16(e[0], e[1]) : pack_bf16(e[0], e[1]);
-        p[(kt * AN + 4 * i4) / 2 + 1] = G::KV4 ? pack_f16(e[2], e[3]) : pack_bf16(e[2], e[3]);
+        p[(kt * AN + 4 * i4) / 2] = G::F16 ? pack_f16(e[0], e[1]) : pack_bf16(e[0], e[1]);
+        p[(kt * AN + 4 * i4) / 2 + 1] = G::F16 ? pack_f16(e[2], e[3]) : pack_bf16(e[2], e[3]);
       }
     if constexpr (G::KV4) {
       // Fragment f: keys of steps 2 y and 2 y + 1, tile d of the output, f = y DT + d.
@@ -803,7 +804,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
     if constexpr (!G::KV4) unrolled<G::PS * G::DT / 4>([&](auto blk) {
       constexpr int F0 = 4 * decltype(blk)::value;
       auto at_key = [](int f) constexpr { return decltype(v_at)::value + f / G::DT * G::KS * G::RB; };
-      v8bf va[4];
+      operand va[4];
       if constexpr (!G::KV8) {
         uint32_t ad[8];
         v2i x[8];
@@ -812,7 +813,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
         read_tr16<at_key(F0), at_key(F0 + 1), at_key(F0 + 2), at_key(F0 + 3)>(x, ad);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          va[j] = __builtin_bit_cast(v8bf, __builtin_shufflevector(x[2 * j], x[2 * j + 1], 0, 1, 2, 3));
+          va[j] = __builtin_bit_cast(operand, __builtin_shufflevector(x[2 * j], x[2 * j + 1], 0, 1, 2, 3));
       } else {
         uint32_t ad[4];
         v2i x[4];
@@ -826,8 +827,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
       for (int j = 0; j < 4; ++j) {
         constexpr int DT = G::DT;
         const int x = (F0 + j) / DT, d = (F0 + j) % DT;
-        const v8bf pb = __builtin_bit_cast(
-            v8bf, (v4i{(int)p[4 * x], (int)p[4 * x + 1], (int)p[4 * x + 2], (int)p[4 * x + 3]}));
+        const operand pb = __builtin_bit_cast(
+            operand, (v4i{(int)p[4 * x], (int)p[4 * x + 1], (int)p[4 * x + 2], (int)p[4 * x + 3]}));
         o[d] = mfma(va[j], pb, o[d]);
       }
     });
@@ -900,7 +901,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   }
 
   // ---- join the lane groups' sums and the key groups' parts, and write
-  const float v_unit = G::KV4 ? a.c.v_unit : 1.0f, up2 = G::KV4 ? kUp : 0.0f;
+  const float v_unit = G::F16 ? a.c.v_unit : 1.0f, up2 = G::F16 ? kUp : 0.0f;
 #pragma unroll
   for (int x = G::MT; x < 64; x <<= 1) l += __shfl_xor(l, x);
   if constexpr (G::WK == 1) {
@@ -1117,7 +1118,7 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
 }
 
 // Widens the pages of an NVFP4 cache that some new token of a request can see to
-// bf16, which holds every value exactly, and writes the table that names them: a
+// fp16, which holds code times scale exactly, and writes the table that names them: a
 // workgroup per page, 16 values of a row per lane.  Bound by HBM's writes.
 template <int D>
 __global__ __launch_bounds__(256) void k_widen(AttnArgs a) {
@@ -1151,16 +1152,9 @@ __global__ __launch_bounds__(256) void k_widen(AttnArgs a) {
     for (int kv2 = 0; kv2 < 2; ++kv2) {
       v2h s0, s1;
       e4m3x2_scales(sc[kv2], s0, s1);
-      const float unit = kv2 ? a.c.v_unit : a.c.k_unit;
-      v4i* const to = (v4i*)((kv2 ? v_pool : a.wide) + out + (int64_t)it * 32);
+      v8h* const to = (v8h*)((kv2 ? v_pool : a.wide) + out + (int64_t)it * 32);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v8h v = e2m1x8_to_f16((uint32_t)code[kv2][h], s0);
-        float f[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) f[x] = (float)v[x] * unit;
-        to[h] = pack8_bf16(f);
-      }
+      for (int h = 0; h < 2; ++h) to[h] = e2m1x8_to_f16((uint32_t)code[kv2][h], s0);
     }
   }
 }
@@ -1182,7 +1176,9 @@ __global__ __launch_bounds__(256) void k_widen(AttnArgs a) {
 template <int D, int FMT, class F>
 auto visit_rows(int64_t rows, F f) {
   constexpr bool KV8 = FMT == OCQ_CACHE_E4M3;
-  if constexpr (FMT == OCQ_CACHE_NVFP4) {
+  if constexpr (FMT == kWidened) {
+    return f(Geo<D, FMT, 32, 4, 1, D == 256 ? 32 : 64, D == 256 ? 1 : D == 64 ? 3 : 2>{});   // (kWideRows)
+  } else if constexpr (FMT == OCQ_CACHE_NVFP4) {
     if (rows <= 16) return f(Geo<D, FMT, 16, 1, D == 256 ? 2 : 4, 64, D == 256 ? 1 : 2>{});
     if constexpr (D < 256)
       if (rows <= 32) return f(Geo<D, FMT, 32, 1, 4, D == 128 ? 32 : 64, 2>{});
@@ -1199,7 +1195,8 @@ auto visit_rows(int64_t rows, F f) {
 template <int D, class F>
 auto visit_format(int format, int64_t rows, F f) {
   return format == OCQ_CACHE_BF16 ? visit_rows<D, OCQ_CACHE_BF16>(rows, f)
-         : format == OCQ_CACHE_E4M3 ? visit_rows<D, OCQ_CACHE_E4M3>(rows, f) : visit_rows<D, OCQ_CACHE_NVFP4>(rows, f);
+         : format == OCQ_CACHE_E4M3 ? visit_rows<D, OCQ_CACHE_E4M3>(rows, f)
+         : format == OCQ_CACHE_NVFP4 ? visit_rows<D, OCQ_CACHE_NVFP4>(rows, f) : visit_rows<D, kWidened>(rows, f);
 }
 template <class F>
 auto visit(int dim, int format, int64_t rows, F f) {
@@ -1263,10 +1260,10 @@ int launch_attn(const AttnArgs& codes, void* stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
     const int64_t row = a.dim * 2, head = row << a.c.page_shift, page = head * a.c.kv_heads;
-    a.format = OCQ_CACHE_BF16;
+    a.format = kWidened;
     a.c = CacheArgs{codes.wide, codes.wide + (int64_t)a.b.requests * a.wide_pages * page, nullptr, nullptr, head, 0,
                     (uint32_t)page, (uint32_t)row, 0, 0, a.b.requests * a.wide_pages, codes.c.page_shift, codes.c.kv_heads,
-                    1.0f, 1.0f};
+                    codes.c.k_unit, codes.c.v_unit};
     a.b.table = codes.wide_table;
     a.b.table_stride = a.b.max_pages = a.wide_pages;
   }

@@ -74,7 +74,7 @@ struct AttnArgs {
   float* part_o;             // [part_rows][dim]
   float* part_lse;           // [part_rows]
   uint32_t* counters;        // [OCQ_ATTENTION_COUNTERS], 0 between calls
-  // NVFP4 calls of many rows: room for every request's keys and values in bf16, `wide_pages`
+  // NVFP4 calls of many rows: room for every request's keys and values in fp16, `wide_pages`
   // pages a request, and for their page table; null: the codes are attended
   uint8_t* wide;
   int32_t* wide_table;
@@ -96,12 +96,13 @@ struct AttnPlan {
   double lanes = 0;          // of the larger launch (a launch holds fewer than 2^32)
 };
 
-// Pages a request whose keys and values a call over an NVFP4 cache widens to bf16
+// Pages a request whose keys and values a call over an NVFP4 cache widens to fp16
 // first (0: it does not), and the bytes that they take.  Codes that every 32 rows
 // convert for themselves keep the vector unit busy; widened once they cost a pass
 // through memory.  32 heads of 128 on 8 kv heads, two requests over up to 10007 keys,
 // us with and without: 512 rows a kv head 76 (69), 1024 111 (113), 2048 177 (187),
 // 8192 466 (573); 16 requests, 2048 rows over 700 keys 114 (113).
+constexpr int kWidened = 3;               // format of such a call's second launch
 constexpr int kWideRows = 1024;
 constexpr int64_t kWideBytes = (int64_t)1 << 30;
 inline int64_t wide_bytes(int requests, int pages, int page_size, int kv_heads, int dim) {

@@ -20,7 +20,7 @@ CallPlan plan_of(int heads, const ocq_kv_cache* c, const ocq_token_batch* b, int
   p.wide = wide_pages(c->format, b->requests, (int64_t)max_new(b) * (heads / c->kv_heads), b->max_kv, b->max_pages,
                       c->page_size, c->kv_heads, c->head_dim);
   p.attn = attn_plan(b->tokens, b->requests, max_new(b), b->max_kv, heads, c->kv_heads, c->head_dim,
-                     p.wide ? OCQ_CACHE_BF16 : c->format, window, sinks,
+                     p.wide ? kWidened : c->format, window, sinks,
                      (int64_t)(p.wide ? p.wide : b->max_pages) * c->page_size);
   if (p.wide) p.wide_bytes = ((size_t)wide_bytes(b->requests, p.wide, c->page_size, c->kv_heads, c->head_dim) + 15) & ~(size_t)15;
   p.bytes = p.wide_bytes + p.attn.part_rows * (c->head_dim + 1) * sizeof(float);

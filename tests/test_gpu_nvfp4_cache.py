@@ -7,9 +7,7 @@ asked for.  Attention: q, k and v are exact in the products, probabilities are r
 are fp32 sums of exact products, 2^-20 of their size (at most 2^5 here but where a test says more), which the exponential
 turns into a relative 2^-15 of each weight: |out - ref| <= 2^-8 |ref| (the output's own rounding) + (2^-11 + 2^-14) sum_j
 w_j |v_j|.  Below fp16's normal range a rounding is absolute, 2^-25, of probabilities whose largest is 2^7 at least: 2^-32
-sum_j |v_j| more over the keys that a token sees.  Calls of 1024 rows a kv head and more go over a bf16 copy of the
-pages: their probabilities are rounded to bf16, 2^-8 relative in the place of 2^-11.  The log-sum-exp as for the other
-formats.
+sum_j |v_j| more over the keys that a token sees.  The log-sum-exp as for the other formats.
 """
 
 import math
@@ -102,9 +100,7 @@ def check_attention(q, cache, batch, news, kvs, scale=None, window=0, sinks=0, s
     assert torch.equal(torch.isinf(lse), empty) and not out[empty].float().any()
     d = (lse.double() - rl)[~empty].abs()
     assert not d.numel() or d.max() <= 2.0 ** -18 + rl[~empty].abs().max() * 2.0 ** -18
-    widened = max(news) * q.shape[1] // cache.kv_heads >= 1024
-    half = 2.0 ** -8 if widened else 2.0 ** -11
-    tol = ref.abs() * 2.0 ** -8 + mag[0] * (half + score * 2.0 ** -19) + mag[1] * 2.0 ** -32 + 1e-30
+    tol = ref.abs() * 2.0 ** -8 + mag[0] * (2.0 ** -11 + score * 2.0 ** -19) + mag[1] * 2.0 ** -32 + 1e-30
     bad = ~((out.double() - ref).abs() <= tol)
     assert not bad.any(), "%d of %d off, worst %.3g" % (int(bad.sum()), bad.numel(), float((out.double() - ref).abs().max()))
     return out, lse
@@ -215,23 +211,16 @@ def test_attention_of_many_rows(dim, page, window, sinks):
             u = x.view(torch.uint8)
             u[u == 0x7F] = 0
         out, lse = ocq.paged_attention(many, cache, batch, window=window, sinks=sinks, want_lse=True)
-        a, b = check_attention_bf16(many, ref_cache, batch, news, kvs, window, sinks)
+        a, b = check_widened(many, ref_cache, batch, news, kvs, window, sinks)
         assert torch.equal(out, a) and torch.equal(lse, b)
     else:
-        check_attention_bf16(many, cache, batch, news, kvs, window, sinks)
+        check_widened(many, cache, batch, news, kvs, window, sinks)
 
 
-def check_attention_bf16(q, cache, batch, news, kvs, window, sinks):
-    """As over a bf16 cache: probabilities are rounded to bf16, 2^-8 of each weight."""
+def check_widened(q, cache, batch, news, kvs, window, sinks):
     batch.of(len(q))
     assert ocq.attention_workspace_bytes(q.shape[1], cache, batch, window, sinks) > sum(kvs) * 2 * cache.head_dim * 4
-    out, lse = ocq.paged_attention(q, cache, batch, window=window, sinks=sinks, want_lse=True)
-    ref, rl, mag = attention_ref(q, cache, batch, news, kvs, q.shape[2] ** -0.5, window, sinks)
-    assert not torch.isinf(rl).any()
-    d = (lse.double() - rl).abs()
-    assert d.max() <= 2.0 ** -18 + rl.abs().max() * 2.0 ** -18
-    assert torch.all((out.double() - ref).abs() <= ref.abs() * 2.0 ** -8 + mag[0] * 2.0 ** -8 + 1e-30)
-    return out, lse
+    return check_attention(q, cache, batch, news, kvs, window=window, sinks=sinks)
 
 
 def test_append_codes_at_every_border():
