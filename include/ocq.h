@@ -402,10 +402,11 @@ typedef struct {
  * max_new, max_kv: host bounds of the new tokens and of kv_lens of any
  * request.  Tokens past max_new of a request are not attended, nor are tokens
  * of no request: what out and lse hold for them is not defined.  max_kv only
- * shapes the split of the work.
- * counters_dev: uint32 [OCQ_ATTENTION_COUNTERS] for ocq_paged_attention (not
- * read by the others): zeroed by the caller before the first call in that
- * call's order, zero again after every call; attention calls that share it must
+ * shapes the split of the work (but see ocq_paged_attention for NVFP4 calls of many
+ * rows).
+ * counters_dev: uint32 [OCQ_ATTENTION_COUNTERS] for ocq_paged_attention and
+ * ocq_verify_drafts (not read by the others): zeroed by the caller before the first call in that
+ * call's order, zero again after every call; calls that share it must
  * be ordered on one stream.  If the device arrays change while a call runs its
  * counts may stay wrong: zero them again.
  * tokens * heads and max_pages * page_size stay below 2^31. */
@@ -520,7 +521,8 @@ ocq_status ocq_cache_values(const ocq_kv_cache* cache, void* k_out_dev, void* v_
  * likewise, draft_rows rows.  tokens_dev int32 [tokens], u_accept_dev float
  * [tokens] and u_next_dev float [requests], numbers in [0, 1); temperature_dev float
  * [requests], or NULL: temperature for all (neither is read with probabilities 1).
- * accepted_dev int32 [requests], out_dev int32 [tokens].  Of the batch q_start,
+ * accepted_dev int32 [requests], out_dev int32 [tokens]: not overlapping the inputs;
+ * a batch without requests writes neither.  Of the batch q_start,
  * requests (up to OCQ_ATTENTION_COUNTERS), tokens (up to 2^20) and the counters are
  * used, the counters as attention uses them.
  * workspace_dev: ocq_verify_drafts_workspace_bytes(...) bytes, contents need not be
@@ -570,7 +572,7 @@ typedef struct {
  * and missing nullable.
  * before and after may be the same; they share the page table and the ring, which
  * are changed in place.  No output may overlap news or accepted. */
-size_t ocq_step_tables_workspace_bytes(int requests, int tokens);
+size_t ocq_step_tables_workspace_bytes(const ocq_page_tables* tables, int tokens);
 ocq_status ocq_step_tables(const ocq_page_tables* before, const ocq_page_tables* after, const void* news_dev,
                            const void* accepted_dev, int tokens, void* slots_dev, void* positions_dev,
                            void* requests_dev, void* missing_dev, void* workspace_dev, size_t workspace_bytes,

@@ -411,7 +411,7 @@ __global__ __launch_bounds__(kThreads) void k_stats(DraftArgs a) {
     if (top == -__builtin_inff()) at = 0x7FFFFFFF;
     if (bad) sum = __builtin_nan("");
   } else {
-    const float c = (float)(kLog2e / (double)temp);
+    const float c = fminf((float)(kLog2e / (double)temp), 1e30f);   // (finite at any T > 0: 0 times it is 0)
     float s = rest == -__builtin_inff() ? 0.0f : 1.0f + 0.0f * rest;   // e^0; NaN and inf are none
     if (rest != rest) top = -__builtin_inff();
     for (int j = j0; j < end; j += TILE) {

@@ -61,7 +61,7 @@ struct TableArgs {
   int requests, tokens, max_pages, ring_size, page_shift;
   int32_t* records;          // workspace of a step in two launches
 };
-size_t table_workspace(int requests, int tokens);
+size_t table_workspace(int requests, int tokens, int max_pages);
 
 // each enqueues on `stream` and returns 0 or a hipError_t value
 int launch_drafts(const DraftArgs& a, void* stream);

@@ -126,8 +126,10 @@ ocq_status ocq_verify_drafts(const void* target_dev, int64_t target_stride, int 
   return rc ? hip_error(rc) : OCQ_OK;
 }
 
-size_t ocq_step_tables_workspace_bytes(int requests, int tokens) {
-  return requests < 0 || tokens < 0 || requests > 65536 ? 0 : table_workspace(requests, tokens);
+size_t ocq_step_tables_workspace_bytes(const ocq_page_tables* tables, int tokens) {
+  set_error(OCQ_OK, "");
+  if (check_tables(tables) != OCQ_OK || tokens < 0) return 0;
+  return table_workspace(tables->requests, tokens, tables->max_pages);
 }
 
 ocq_status ocq_step_tables(const ocq_page_tables* before, const ocq_page_tables* after, const void* news_dev,
@@ -151,7 +153,7 @@ ocq_status ocq_step_tables(const ocq_page_tables* before, const ocq_page_tables*
   for (const void* p : ptrs)
     if (!aligned(p, 4)) return invalid("misaligned device pointer");
   if (!aligned(slots_dev, 8)) return invalid("slots must be 8-byte aligned");
-  const size_t need = table_workspace(before->requests, tokens);
+  const size_t need = table_workspace(before->requests, tokens, before->max_pages);
   if (workspace_bytes < need)
     return set_error(OCQ_ERR_BUFFER_TOO_SMALL, "workspace_bytes < ocq_step_tables_workspace_bytes()");
   if (need && (!workspace_dev || !aligned(workspace_dev))) return invalid("the workspace must be a 16-byte aligned pointer");

@@ -134,7 +134,7 @@ def lib():
     L.ocq_verify_drafts.argtypes = [vp, i64, i, i, vp, i64, i64, i, vp, vp, vp, vp, f, i, bp, vp, vp, vp, sz, vp]
     L.ocq_verify_drafts.restype = i
     tp = ctypes.POINTER(PageTablesStruct)
-    L.ocq_step_tables_workspace_bytes.argtypes, L.ocq_step_tables_workspace_bytes.restype = [i, i], sz
+    L.ocq_step_tables_workspace_bytes.argtypes, L.ocq_step_tables_workspace_bytes.restype = [tp, i], sz
     L.ocq_step_tables.argtypes, L.ocq_step_tables.restype = [tp, tp, vp, vp, i, vp, vp, vp, vp, vp, sz, vp], i
     _lib = L
     return L
@@ -618,7 +618,7 @@ class TokenBatch:
     entries or more apart): CUDA tensors whose contents may change between calls.  tokens (the rows of q), max_new and
     max_kv are host numbers: bounds of the new tokens and of kv_lens of any request.
 
-    Attention calls over one batch count their finished work in memory of the batch, 0 between calls, apart for every
+    Attention calls over one batch (and verify_drafts) count their finished work in memory of the batch, 0 between calls, apart for every
     stream that they run on.  A captured call counts where calls on the stream that the batch was made on do: its replays
     are ordered with those, and the batch outlives the graph.  The device arrays must not change while a call runs (its
     counts could stay wrong for the next one).
@@ -958,7 +958,7 @@ def step_tables(tables, news, tokens, accepted=None, out=None, slots=None, posit
         given.append(t)
     L = lib()
     if workspace is None:
-        need = L.ocq_step_tables_workspace_bytes(n, tokens)
+        need = L.ocq_step_tables_workspace_bytes(tables.ref, tokens)
         if need:
             workspace = _empty(need, _torch.uint8, i, stream)
     else:

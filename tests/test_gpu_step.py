@@ -214,6 +214,16 @@ def test_drafts_weights_that_are_none():
         assert check_drafts(s)[1].tolist() == [123, -1]
 
 
+def test_drafts_at_the_smallest_and_largest_temperatures():
+    """Next to 0 the largest logits share all the weight, at 10^30 all tokens do (but those ruled out)."""
+    s = make_drafts([1, 1, 1], 3000, 4, torch.float32, temps=[1e-40, 1e-30, 1e30])
+    s["target"][:2, 17], s["target"][:2, 2900] = 50.0, 50.0
+    s["target"][2, :1500] = -float("inf")
+    for u, want in ((0.25, [17, 17, 1875]), (0.75, [2900, 2900, 2625])):
+        s["u_next"][:] = u
+        assert check_drafts(s)[1].tolist() == want
+
+
 def test_drafts_ids_that_are_none():
     s = make_drafts([5, 5], 700, 6, torch.float32, near=0.0)
     s["ids"][2], s["ids"][6] = 700, -3
@@ -408,6 +418,17 @@ def test_tables_with_too_few_pages(requests):
     assert t["missing"][0] > 0
     t, tables = check_tables(t, [-1] + [0] * (requests - 1), 4, None, tables)
     t, tables = check_tables(t, [0] * requests, 0, None, tables)
+
+
+def test_tables_that_give_all_pages_back():
+    """Many long requests end in a step of few tokens."""
+    requests, most = 70, 8000
+    t = dict(q_start=list(range(requests + 1)), kv=[16 * most - r for r in range(requests)], held=[most] * requests,
+             table=[list(range(r * most, (r + 1) * most)) for r in range(requests)], ring=[-1] * (requests * most),
+             counts=[5, 5], page=16)
+    t, tables = check_tables(t, [-1] * requests, 3, [0] * requests)
+    assert sorted(t["ring"]) == list(range(requests * most))
+    check_tables(t, [16 * most if r == 3 else 0 for r in range(requests)], 16 * most, None, tables)
 
 
 def test_tables_past_the_table():

@@ -86,8 +86,9 @@ def test_step_refusals(fault, status):
 
 def test_steps_of_nothing_and_workspace():
     assert _step(_tables(requests=0)) == 0
-    need = ocq.lib().ocq_step_tables_workspace_bytes
-    assert need(-1, 5) == 0 and need(3, -1) == 0 and need(16, 208) == 0 and need(4096, 20480) > 0
+    need = lambda tokens, **kw: ocq.lib().ocq_step_tables_workspace_bytes(ctypes.byref(_tables(**kw)), tokens)  # noqa: E731
+    assert need(5, requests=-1) == 0 and need(-1) == 0 and need(208, requests=16) == 0 and need(20480, requests=4096) > 0
+    assert need(208, requests=600, max_pages=1000, table_stride=1000) > 0
 
 
 @pytest.mark.parametrize("fault,status", [
