@@ -1123,12 +1123,12 @@ hipError_t run(const AttnArgs& a, hipStream_t st) {
 
 // Widens the pages of an NVFP4 cache that some new token of a request can see to
 // fp16, which holds code times scale exactly, and writes the table that names them: a
-// workgroup per page, 16 values of a row per lane.  Bound by HBM's writes.
+// workgroup per page and 1024 lanes' work, 8 values of a row per lane.  Bound by HBM's writes.
 template <int D>
 __global__ __launch_bounds__(256) void k_widen(AttnArgs a) {
-  constexpr int LPR = D / 16;
+  constexpr int LPR = D / 8;
   const int req = blockIdx.x / a.wide_pages, j = blockIdx.x % a.wide_pages;
-  if (threadIdx.x == 0) a.wide_table[blockIdx.x] = blockIdx.x;
+  if (threadIdx.x == 0 && blockIdx.y == 0) a.wide_table[blockIdx.x] = blockIdx.x;
   const Span span = token_span(a.b.q_start, req, a.b.tokens);
   const int kv = kv_bound(a.b.kv_lens[req], a.wide_pages, a.c.page_shift);
   const int page_size = 1 << a.c.page_shift, first = j << a.c.page_shift;
@@ -1138,17 +1138,17 @@ __global__ __launch_bounds__(256) void k_widen(AttnArgs a) {
   const int id = a.b.table[req * a.b.table_stride + j];
   const bool there = page_there(id, a.c.num_pages);
   const int items = page_size * a.c.kv_heads * LPR;
-  const int64_t out = (int64_t)blockIdx.x * items * 32;
-  uint8_t* const v_pool = a.wide + (int64_t)a.b.requests * a.wide_pages * items * 32;
-  for (int it = threadIdx.x; it < items; it += 256) {
+  const int64_t out = (int64_t)blockIdx.x * items * 16;
+  uint8_t* const v_pool = a.wide + (int64_t)a.b.requests * a.wide_pages * items * 16;
+#pragma unroll 4
+  for (int it = blockIdx.y * 256 + threadIdx.x; it < items; it += 256 * gridDim.y) {
     const int i = it % LPR, row = it / LPR, head = row >> a.c.page_shift, key = row & (page_size - 1);
-    const uint64_t at = there ? row_offset(key, id, a.c.page_shift, a.c.page, a.c.token) + head * a.c.head + 8 * i : 0;
-    const uint64_t s_at = there ? row_offset(key, id, a.c.page_shift, a.c.s_page, a.c.s_token) + head * a.c.s_head + i : 0;
-    v2i code[2] = {{0, 0}, {0, 0}};
-    uint32_t sc[2] = {0, 0};
+    const uint64_t at = there ? row_offset(key, id, a.c.page_shift, a.c.page, a.c.token) + head * a.c.head + 4 * i : 0;
+    const uint64_t s_at = there ? row_offset(key, id, a.c.page_shift, a.c.s_page, a.c.s_token) + head * a.c.s_head + i / 2 : 0;
+    uint32_t code[2] = {0, 0}, sc[2] = {0, 0};
     if (there) {
-      code[0] = *(const v2i*)(a.c.k + at);
-      code[1] = *(const v2i*)(a.c.v + at);
+      code[0] = *(const uint32_t*)(a.c.k + at);
+      code[1] = *(const uint32_t*)(a.c.v + at);
       sc[0] = ((const uint8_t*)a.c.k_scale)[s_at];
       sc[1] = ((const uint8_t*)a.c.v_scale)[s_at];
     }
@@ -1156,9 +1156,7 @@ __global__ __launch_bounds__(256) void k_widen(AttnArgs a) {
     for (int kv2 = 0; kv2 < 2; ++kv2) {
       v2h s0, s1;
       e4m3x2_scales(sc[kv2], s0, s1);
-      v8h* const to = (v8h*)((kv2 ? v_pool : a.wide) + out + (int64_t)it * 32);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) to[h] = e2m1x8_to_f16((uint32_t)code[kv2][h], s0);
+      *(v8h*)((kv2 ? v_pool : a.wide) + out + (int64_t)it * 16) = e2m1x8_to_f16(code[kv2], s0);
     }
   }
 }
@@ -1257,7 +1255,9 @@ int launch_attn(const AttnArgs& codes, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   AttnArgs a = codes;
   if (a.wide) {
-    const dim3 grid((unsigned)(a.b.requests * a.wide_pages)), block(256);
+    const int64_t lanes = ((int64_t)a.c.kv_heads << a.c.page_shift) * a.dim / 8;
+    const int64_t ways = lanes / 1024 < 1 ? 1 : lanes / 1024 > 64 ? 64 : lanes / 1024;
+    const dim3 grid((unsigned)(a.b.requests * a.wide_pages), (unsigned)ways), block(256);
     if (a.dim == 64) hipLaunchKernelGGL((k_widen<64>), grid, block, 0, st, codes);
     else if (a.dim == 128) hipLaunchKernelGGL((k_widen<128>), grid, block, 0, st, codes);
     else hipLaunchKernelGGL((k_widen<256>), grid, block, 0, st, codes);

@@ -362,10 +362,12 @@ void run(const RopeArgs& a, hipStream_t st) {
   }
 }
 
-// The values of a pool of codes: a lane makes 16 of one row, of k, then of v.
+// The values of a pool of codes: a lane makes 8 of one row, of k, then of v, so that
+// a wave's stores lie side by side (32,000 tokens of 8 heads of 128: 36.8 us; 16 a lane
+// 44.9, with non-temporal stores 61).  Bound by HBM's writes.
 template <bool NVFP4>
 __global__ __launch_bounds__(256) void k_values(ValuesArgs a, int64_t first) {
-  const int lanes = a.dim / 16;
+  const int lanes = a.dim / 8;
   const int64_t it = first + (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = it / lanes;
   if (row >= a.rows) return;
@@ -377,39 +379,30 @@ __global__ __launch_bounds__(256) void k_values(ValuesArgs a, int64_t first) {
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
     const uint8_t* const pool = (kv ? a.c.v : a.c.k) + at;
-    float y[16];
+    float y[8];
     if constexpr (NVFP4) {
-      const v2u c = *(const v2u*)(pool + 8 * i);
-      const uint32_t sc = ((const uint8_t*)(kv ? a.c.v_scale : a.c.k_scale))[s_at + i];
+      const uint32_t sc = ((const uint8_t*)(kv ? a.c.v_scale : a.c.k_scale))[s_at + i / 2];
       const float unit = kv ? a.c.v_unit : a.c.k_unit;
       v2h s0, s1;
       e4m3x2_scales(sc, s0, s1);
+      const v8h v = e2m1x8_to_f16(*(const uint32_t*)(pool + 4 * i), s0);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v8h v = e2m1x8_to_f16(c[h], s0);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[8 * h + j] = (float)v[j] * unit;
-      }
+      for (int j = 0; j < 8; ++j) y[j] = (float)v[j] * unit;
     } else {
-      const v4i c = *(const v4i*)(pool + 16 * i);
+      const v2u c = *(const v2u*)(pool + 8 * i);
       const float s = (kv ? a.c.v_scale : a.c.k_scale)[s_at];
+      const v8h v = e4m3x8_to_f16(c[0], c[1]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const v8h v = e4m3x8_to_f16((uint32_t)c[2 * h], (uint32_t)c[2 * h + 1]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[8 * h + j] = (float)v[j] * s;
-      }
+      for (int j = 0; j < 8; ++j) y[j] = (float)v[j] * s;
     }
-    uint16_t* const to = (kv ? a.v : a.k) + row * a.dim + 16 * i;
-    store8(to, y);
-    store8(to + 8, y + 8);
+    store8((kv ? a.v : a.k) + row * a.dim + 8 * i, y);
   }
 }
 
 }  // namespace
 
 int launch_values(const ValuesArgs& a, void* stream) {
-  const int64_t items = a.rows * (a.dim / 16);
+  const int64_t items = a.rows * (a.dim / 8);
   for (int64_t first = 0; first < items; first += kLanesAtOnce) {
     const int64_t left = items - first, now = left < kLanesAtOnce ? left : kLanesAtOnce;
     const dim3 grid((unsigned)((now + 255) / 256)), block(256);
