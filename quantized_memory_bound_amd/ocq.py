@@ -815,6 +815,15 @@ def cache_values(cache, k=None, v=None, stream=None):
 
 # ---------------------------------------------------------------- between two verify steps
 
+def _vector(t, name, dtype, index, size):
+    """The address of t, a contiguous tensor of this type and size on device `index`."""
+    if hasattr(t, "get_device") and t.dtype is dtype and t.get_device() == index and t.shape == (size,) and \
+            t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, _torch.device("cuda", index), (size,))
+    return t.data_ptr()
+
+
 def _row_matrix(t, name, index, rows, cols):
     """(pointer, row stride, is bf16) of a float32 or bf16 matrix with `rows` rows or more, its last axis contiguous."""
     if t is None or not hasattr(t, "get_device") or t.get_device() != index or t.dim() != 2 or \
@@ -854,23 +863,18 @@ def verify_drafts(target, tokens, batch, u_accept, u_next, draft_probs=None, tem
         d_rows = draft_probs.shape[0]
         if d_rows == 0:
             d = t                                   # no drafts: not read, but not a missing q either
-    _need(tokens, "tokens", _torch.int32, dev, (rows,))
-    _need(u_accept, "u_accept", _torch.float32, dev, (rows,))
-    _need(u_next, "u_next", _torch.float32, dev, (requests,))
-    temps, temp = None, 1.0
+    int32, f32 = _torch.int32, _torch.float32
+    ids, ua = _vector(tokens, "tokens", int32, i, rows), _vector(u_accept, "u_accept", f32, i, rows)
+    un, temps, temp = _vector(u_next, "u_next", f32, i, requests), None, 1.0
     if hasattr(temperature, "data_ptr"):
-        _need(temperature, "temperature", _torch.float32, dev, (requests,))
-        temps = temperature.data_ptr()
+        temps = _vector(temperature, "temperature", f32, i, requests)
     else:
         temp = float(temperature)
     if accepted is None:
-        accepted = _empty(requests, _torch.int32, i, stream)
-    else:
-        _need(accepted, "accepted", _torch.int32, dev, (requests,))
+        accepted = _empty(requests, int32, i, stream)
     if out is None:
-        out = _empty(rows, _torch.int32, i, stream)
-    else:
-        _need(out, "out", _torch.int32, dev, (rows,))
+        out = _empty(rows, int32, i, stream)
+    acc, to = _vector(accepted, "accepted", int32, i, requests), _vector(out, "out", int32, i, rows)
     if handle != batch.stream:
         batch.move_to(handle)
     if workspace is None:
@@ -879,8 +883,8 @@ def verify_drafts(target, tokens, batch, u_accept, u_next, draft_probs=None, tem
     else:
         _need(workspace, "workspace", _torch.uint8, dev)
     _check(L.ocq_verify_drafts(t, t_stride, t_bf16, int(bool(probabilities)), d or None, d_stride, d_rows, d_bf16,
-                               tokens.data_ptr(), u_accept.data_ptr(), u_next.data_ptr(), temps, temp, vocab, ref,
-                               accepted.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.numel(), handle))
+                               ids, ua, un, temps, temp, vocab, ref, acc, to, workspace.data_ptr(), workspace.numel(),
+                               handle))
     return accepted, out
 
 
@@ -945,17 +949,20 @@ def step_tables(tables, news, tokens, accepted=None, out=None, slots=None, posit
     tokens = _int32(tokens, "tokens")
     if tokens < 0:
         raise OcqError(ERR_INVALID_ARG, "tokens is %d" % tokens)
-    _need(news, "news", _torch.int32, dev, (n,))
+    int32, acc = _torch.int32, None
+    new = _vector(news, "news", int32, i, n)
     if accepted is not None:
-        _need(accepted, "accepted", _torch.int32, dev, (n,))
-    given = []
-    for t, name, dtype, size in ((slots, "slots", _torch.int64, tokens), (positions, "positions", _torch.int32, tokens),
-                                 (requests, "requests", _torch.int32, tokens), (missing, "missing", _torch.int32, 1)):
-        if t is None:
-            t = _empty(size, dtype, i, stream)
-        else:
-            _need(t, name, dtype, dev, (size,))
-        given.append(t)
+        acc = _vector(accepted, "accepted", int32, i, n)
+    if slots is None:
+        slots = _empty(tokens, _torch.int64, i, stream)
+    if positions is None:
+        positions = _empty(tokens, int32, i, stream)
+    if requests is None:
+        requests = _empty(tokens, int32, i, stream)
+    if missing is None:
+        missing = _empty(1, int32, i, stream)
+    to = (_vector(slots, "slots", _torch.int64, i, tokens), _vector(positions, "positions", int32, i, tokens),
+          _vector(requests, "requests", int32, i, tokens), _vector(missing, "missing", int32, i, 1))
     L = lib()
     if workspace is None:
         need = L.ocq_step_tables_workspace_bytes(tables.ref, tokens)
@@ -964,11 +971,9 @@ def step_tables(tables, news, tokens, accepted=None, out=None, slots=None, posit
     else:
         _need(workspace, "workspace", _torch.uint8, dev)
         need = workspace.numel()
-    _check(L.ocq_step_tables(tables.ref, after.ref, news.data_ptr(), None if accepted is None else accepted.data_ptr(),
-                             tokens, given[0].data_ptr(), given[1].data_ptr(), given[2].data_ptr(),
-                             given[3].data_ptr(), None if workspace is None else workspace.data_ptr(), need,
-                             _stream_of(stream, i)))
-    return tuple(given)
+    _check(L.ocq_step_tables(tables.ref, after.ref, new, acc, tokens, *to,
+                             None if workspace is None else workspace.data_ptr(), need, _stream_of(stream, i)))
+    return slots, positions, requests, missing
 
 
 # ---------------------------------------------------------------- measurement helpers
