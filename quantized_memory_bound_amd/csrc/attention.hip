@@ -134,6 +134,11 @@ struct Geo {
   static constexpr int JOIN = WK > 1 ? WK * ROWS * (SO * 4 + 8) + 4 : 0;
   static constexpr int LDS = RING + NW * VTAB > JOIN ? RING + NW * VTAB : JOIN;
   static constexpr bool EVEN = WK > 1;                                  // may be cut into pieces (layer_index.h)
+  // Tiles of the smallest piece.  A stage of 4-bit keys takes a wave alone as long as
+  // its loads (2.3 us): two tiles (4 requests, one token over 1100 / 2200 / 4400 / 8800
+  // keys 14.2, 14.6, 19.9, 24.3 us; four tiles 16.4, 16.6, 18.7, 26.2).  For more rows
+  // four as well (16 x 13 over 1000 keys 22.7; two tiles 26.9).
+  static constexpr int MIN_TILES = KV4 && MT == 16 ? 2 : kMinTiles;
   static constexpr int PER_CU = 160 * 1024 / (LDS + 1024) < 4 * MINW / NW ? 160 * 1024 / (LDS + 1024) : 4 * MINW / NW;
   static constexpr int RESIDENT = 256 * (PER_CU > 0 ? PER_CU : 1);      // workgroups at once, 256 CUs
   static_assert(PART % 1024 == 0 && (PART % (1024 * WR) == 0 || KV4) && TK % 32 == 0 && LDS <= 160 * 1024, "");
@@ -275,7 +280,7 @@ struct Found {
 
 // Every wave cuts the batch into pieces by itself, in registers: lane l holds
 // request base + l.
-__device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int piece) {
+__device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int min_tiles, int piece) {
   const int lane = threadIdx.x & 63, kvh = a.c.kv_heads;
   auto load = [&](int base, int& t0, int& n, int& kv) {
     const int r = base + lane;
@@ -336,7 +341,7 @@ __device__ __forceinline__ Found find_piece(const AttnArgs& a, int TT, int piece
       if (fits) per = __shfl(mine, __builtin_ctzll(fits));
     }
   }
-  per = fmaxf(per, (float)kMinTiles);
+  per = fmaxf(per, (float)min_tiles);
   const float inv = 1.0f / per;
   Found f{-1, 0, 0, 0, 0, 0, 0};
   int carry = 0;
@@ -1034,7 +1039,7 @@ __global__ __launch_bounds__(G::THREADS, G::MINW) void k_attn(AttnArgs a) {
   Piece pc;
   if constexpr (G::EVEN) {
     if (a.even) {
-      const Found f = find_piece(a, G::TT, blockIdx.x);
+      const Found f = find_piece(a, G::TT, G::MIN_TILES, blockIdx.x);
       if (f.req < 0) return;
       const int in = blockIdx.x - f.first, i = in % f.pieces;
       pc.req = f.req;
@@ -1230,7 +1235,7 @@ AttnPlan attn_plan(int tokens, int requests, int max_new, int max_kv, int heads,
     const int64_t pairs = (int64_t)requests * kv_heads, tiles = (rows + G::ROWS - 1) / G::ROWS;
     p.lanes = (double)pairs * (double)tiles * G::THREADS;
     const int64_t key_tiles = (keys + G::TT - 1) / G::TT;
-    if (key_tiles <= kMinTiles) return p;
+    if (key_tiles <= G::MIN_TILES) return p;
     if (G::EVEN && requests <= kEvenRequests && pairs < 4 * G::RESIDENT && pairs <= OCQ_ATTENTION_COUNTERS &&
         pairs * (cap / G::TT + 1) < (1 << 30)) {
       p.even = 1;
