@@ -363,6 +363,9 @@ __global__ __launch_bounds__(kThreads) void k_stats(DraftArgs a) {
   };
   const int j0 = from + threadIdx.x * kVec;
   load(j0);
+  if (blockIdx.x == 0)                                  // requests without rows
+    for (int r = threadIdx.x; r < a.requests; r += kThreads)
+      if (token_span(a.q_start, r, a.tokens).n <= 0) a.accepted[r] = 0;
   const int cut = end - end % kVec + threadIdx.x;
   const float rest = (int)threadIdx.x < end % kVec ? load1(row + cut) : -__builtin_inff();
   const int r = request_of(a, t);
@@ -634,10 +637,7 @@ __global__ __launch_bounds__(kThreads) void k_next(DraftArgs a) {
       for (int t = (behind < 0 ? 0 : behind) + threadIdx.x; t < a.tokens; t += kThreads) a.out[t] = -1;
     }
   } else {
-    if (sp.n <= 0) {                                    // (A has no row of it)
-      if (g == 0 && threadIdx.x == 0) a.accepted[r] = 0;
-      return;
-    }
+    if (sp.n <= 0) return;
     c = a.choices[r];
   }
   if (!c.draw) return;
@@ -694,7 +694,8 @@ void run(const DraftArgs& a, hipStream_t st) {
     return;
   }
   hipLaunchKernelGGL((k_stats<T, Q>), dim3((unsigned)(a.tokens * a.splits)), block, 0, st, a);
-  hipLaunchKernelGGL((k_next<T, Q, false>), next, block, 0, st, a);
+  // (greedy for all: A has found the next tokens; 4 us)
+  if (a.temps || a.temp != 0.0f) hipLaunchKernelGGL((k_next<T, Q, false>), next, block, 0, st, a);
 }
 
 }  // namespace

@@ -258,6 +258,17 @@ def test_drafts_scalar_temperature_outputs_and_streams():
         assert a is acc and b is out and torch.equal(a, want[0]) and torch.equal(b, want[1])
 
 
+@pytest.mark.parametrize("news", [[5, 0, 3, 1, 0], [0, 2], [20]])
+def test_drafts_greedy_for_all(news):
+    """One temperature of 0 for all requests: as a tensor of zeros."""
+    for dtype in (torch.bfloat16, torch.float32):
+        s = make_drafts(news, 3001, 2, dtype, temps=0.0)
+        want = check_drafts(s)
+        got = ocq.verify_drafts(s["target"], s["ids"], s["batch"], s["u_accept"], s["u_next"], draft_probs=s["draft"],
+                                temperature=0.0, accepted=torch.full((len(news),), 9, dtype=torch.int32, device=DEV))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_drafts_rows_behind_the_last_request():
     """A padded batch: the rows that no request has are -1."""
     s = make_drafts([3, 4], 500, 10)
