@@ -476,15 +476,21 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   operand q[G::QS];
   const uint16_t* qp = a.q + (t0 + tok) * a.q_token + head * a.q_head;
   float c = a.scale * kLog2e;
-  if constexpr (G::F16) {
-    // Codes times their scales are exact in fp16, not all in bf16 with one
-    // instruction less; q goes to fp16 after a power of two that brings the row's
-    // largest value to 2^14 .. 2^15, which is exact down to 2^-28 of it (and off by
-    // at most 2^-40 of it below).
+  v4i q_bits[G::QS];
+#pragma unroll
+  for (int s = 0; s < G::QS; ++s) {
+    q_bits[s] = live ? *(const v4i*)(qp + q_dim<G>(s, g)) : v4i{0, 0, 0, 0};
+    if constexpr (!G::F16) q[s] = __builtin_bit_cast(operand, q_bits[s]);
+  }
+  // Codes times their scales are exact in fp16, not all in bf16 with one
+  // instruction less; q goes to fp16 after a power of two that brings the row's
+  // largest value to 2^14 .. 2^15, which is exact down to 2^-28 of it (and off by
+  // at most 2^-40 of it below).  (Called while the first page ids are on their way.)
+  auto q_to_f16 = [&](auto& to) {
     float f[G::QS][8], top = 0.0f;
 #pragma unroll
     for (int s = 0; s < G::QS; ++s) {
-      unpack8_bf16(live ? *(const v4i*)(qp + q_dim<G>(s, g)) : v4i{0, 0, 0, 0}, f[s]);
+      unpack8_bf16(q_bits[s], f[s]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[s][j]));
     }
@@ -494,15 +500,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
 #pragma unroll
     for (int s = 0; s < G::QS; ++s)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[s][j] = (_Float16)__builtin_ldexpf(f[s][j], up);
+      for (int j = 0; j < 8; ++j) to[s][j] = (_Float16)__builtin_ldexpf(f[s][j], up);
     c = __builtin_ldexpf(c * a.c.k_unit, -up);
-  } else {
-#pragma unroll
-    for (int s = 0; s < G::QS; ++s) {
-      const v4i u = live ? *(const v4i*)(qp + q_dim<G>(s, g)) : v4i{0, 0, 0, 0};
-      q[s] = __builtin_bit_cast(v8bf, u);
-    }
-  }
+  };
 
   // ---- loads: rows of this wave's part of its key group's stage.  V of a stage
   // goes after K of it, with the same offsets.
@@ -861,6 +861,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
     for (int st = 0; st < G::NST; ++st)
 #pragma unroll
       for (int i = 0; i < G::QI + G::SI; ++i) first_ids[st][i] = *entry(st < ns ? st : 0, q_row(i));
+    if constexpr (G::F16) q_to_f16(q);
 #pragma unroll
     for (int st = 0; st < G::NST; ++st)
       if (st < ns) {
