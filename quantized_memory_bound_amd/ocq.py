@@ -862,7 +862,7 @@ def verify_drafts(target, tokens, batch, u_accept, u_next, draft_probs=None, tem
         d, d_stride, d_bf16 = _row_matrix(draft_probs, "draft_probs", i, max(0, rows - requests), vocab)
         d_rows = draft_probs.shape[0]
         if d_rows == 0:
-            d = t                                   # no drafts: not read, but not a missing q either
+            d = batch.q_start.data_ptr()            # no drafts: not read, but not a missing q either
     int32, f32 = _torch.int32, _torch.float32
     ids, ua = _vector(tokens, "tokens", int32, i, rows), _vector(u_accept, "u_accept", f32, i, rows)
     un, temps, temp = _vector(u_next, "u_next", f32, i, requests), None, 1.0

@@ -269,6 +269,16 @@ def test_drafts_greedy_for_all(news):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_drafts_without_any():
+    """Requests of one token each, with an empty matrix of draft probabilities and with none."""
+    s = make_drafts([1, 1, 1], 5001, 3, torch.bfloat16, shift=1)
+    assert s["draft"].shape[0] == 0
+    want = check_drafts(s)
+    s["draft"] = None
+    got = check_drafts(s)
+    assert torch.equal(want[1], got[1]) and got[0].tolist() == [0, 0, 0]
+
+
 def test_drafts_rows_behind_the_last_request():
     """A padded batch: the rows that no request has are -1."""
     s = make_drafts([3, 4], 500, 10)

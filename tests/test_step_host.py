@@ -1,12 +1,17 @@
 """What stands between two verify steps, what runs without a GPU: argument checks of the C ABI."""
 
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
 
 from quantized_memory_bound_amd import ocq
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 P = 4096   # an aligned address that no refused call reads
 
 
@@ -128,3 +133,19 @@ def test_binding_refuses_tensors_that_are_not_on_the_gpu():
         with pytest.raises(ocq.OcqError) as e:
             call()
         assert e.value.status == ocq.ERR_INVALID_ARG
+
+
+def test_c_abi_refusals_under_sanitizers(tmp_path):
+    gxx = shutil.which("g++")
+    if gxx is None or not os.path.exists(os.path.join(ROCM, "include", "hip", "hip_runtime.h")):
+        pytest.skip("g++ or the HIP headers are missing")
+    csrc, exe = os.path.join(ROOT, "quantized_memory_bound_amd", "csrc"), str(tmp_path / "driver")
+    cmd = [gxx, "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+           "-I" + os.path.join(ROOT, "include"), "-I" + csrc, "-I" + os.path.join(ROCM, "include"), "-D__HIP_PLATFORM_AMD__",
+           os.path.join(csrc, "step_api.cpp"), os.path.join(ROOT, "tests", "sanitize", "step_host_driver.cpp"), "-o", exe,
+           "-L" + os.path.join(ROCM, "lib"), "-lamdhip64", "-Wl,-rpath," + os.path.join(ROCM, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-4000:]
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=600)
+    out = r.stdout + r.stderr
+    assert r.returncode == 0 and "OK (0 failed checks)" in out and "runtime error" not in out, out[-4000:]
