@@ -702,14 +702,16 @@ void run(const DraftArgs& a, hipStream_t st) {
 
 // A: about 768 workgroups, none below 4096 elements (208 rows of 131072 in bf16:
 // 18.4 us; 2048 workgroups 22.1); a drawn row in chunks of 2048, one load a lane, 64
-// at most.
+// at most, and 32 where the requests fill the chip with them (B over 131072 elements,
+// us with 64 and 32: 16 requests 13.2 and 15.8, 64 28.5 and 28, 128 55 and 47-50).
 DraftPlan draft_plan(int tokens, int requests, int vocab, int probs) {
   DraftPlan p{1, 1, 0, 0, 0, 0};
   const int64_t want = tokens > 0 ? (768 + tokens - 1) / tokens : 1, fit = (vocab + 4095) / 4096;
   p.splits = (int)(want < fit ? want : fit);
   p.splits = p.splits < 1 ? 1 : p.splits > 64 ? 64 : p.splits;
   p.chunks = (vocab + 2047) / 2048;
-  p.chunks = p.chunks > 64 ? 64 : p.chunks;
+  const int most = requests > 64 ? 32 : 64;
+  p.chunks = p.chunks > most ? most : p.chunks;
   p.drafts_at = probs ? 0 : (size_t)tokens * p.splits * sizeof(RowStat);
   p.choices_at = p.drafts_at + (probs ? 0 : (size_t)tokens * sizeof(RowDraft));
   p.parts_at = p.choices_at + (probs ? 0 : (size_t)requests * sizeof(Choice));

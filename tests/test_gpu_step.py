@@ -237,6 +237,13 @@ def test_drafts_many_requests():
     check_drafts(make_drafts(news, 333, 7, temps=[float(x) for x in rng.choice([0.0, 0.5, 1.0], 4096)]))
 
 
+@pytest.mark.parametrize("requests", [64, 65, 130])
+@pytest.mark.parametrize("draft", [True, False])
+def test_drafts_of_batches_that_fill_the_chip(requests, draft):
+    """Long rows of 64 requests and fewer are drawn from in 64 chunks, those of more in 32."""
+    check_drafts(make_drafts([2] * requests, 70001, requests, torch.bfloat16, draft=draft, near=0.05))
+
+
 def test_drafts_scalar_temperature_outputs_and_streams():
     s = make_drafts([5, 2, 7], 9001, 9)
     want = check_drafts(s)
