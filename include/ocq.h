@@ -510,7 +510,8 @@ ocq_status ocq_cache_values(const ocq_kv_cache* cache, void* k_out_dev, void* v_
  * = max(p - q, 0) (p where that is 0 throughout), after the last one from w = p: the
  * lowest j with sum_{i <= j} w_i > u_next[r] sum_i w_i.  Sums and exponentials of
  * that row are 64-bit; the normalization of an acceptance's p is within 2^-20.
- *   accepted[r]            drafts that stay (0 for a request without tokens)
+ *   accepted[r]            drafts that stay (0 for a request without tokens beside
+ *                          others that have some)
  *   out[t0 .. t0 + n - 1]  those drafts, the next token, then -1; -1 too in rows
  *                          behind the last request
  * A next token of -1 says that the row has none: no weight above 0, or values that
@@ -522,7 +523,8 @@ ocq_status ocq_cache_values(const ocq_kv_cache* cache, void* k_out_dev, void* v_
  * [tokens] and u_next_dev float [requests], numbers in [0, 1); temperature_dev float
  * [requests], or NULL: temperature for all (neither is read with probabilities 1).
  * accepted_dev int32 [requests], out_dev int32 [tokens]: not overlapping the inputs;
- * a batch without requests writes neither.  Of the batch q_start,
+ * a batch without requests or without tokens has nothing to verify: OCQ_OK, nothing
+ * is launched or written, accepted stays as the caller left it.  Of the batch q_start,
  * requests (up to OCQ_ATTENTION_COUNTERS), tokens (up to 2^20) and the counters are
  * used, the counters as attention uses them.
  * workspace_dev: ocq_verify_drafts_workspace_bytes(...) bytes, contents need not be

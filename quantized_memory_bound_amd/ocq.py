@@ -6,6 +6,7 @@ fallback: if the library is missing, every call raises.  PyTorch is used only
 for device memory and streams.
 """
 
+import contextlib
 import ctypes
 import os
 
@@ -473,9 +474,16 @@ def _empty(shape, dtype, index, stream):
     """A new tensor for a call on `stream`: allocated on it, so that its memory is not reused before the call."""
     if stream is None:
         return _torch.empty(shape, dtype=dtype, device=index)
-    cuda = _torch.cuda
-    with cuda.stream(stream if hasattr(stream, "cuda_stream") else cuda.ExternalStream(stream, index)):
+    with _in_order_of(stream, index):
         return _torch.empty(shape, dtype=dtype, device=index)
+
+
+def _in_order_of(stream, index):
+    """A context in which torch's own calls are queued on the stream of a call."""
+    if stream is None:
+        return contextlib.nullcontext()
+    cuda = _torch.cuda
+    return cuda.stream(stream if hasattr(stream, "cuda_stream") else cuda.ExternalStream(stream, index))
 
 
 def _empty_as(t, shape, dtype, index, stream):
@@ -845,7 +853,7 @@ def verify_drafts(target, tokens, batch, u_accept, u_next, draft_probs=None, tem
     u_next float32 [requests]: random numbers in [0, 1).  draft_probs: float32 or bf16 [drafts, vocab], what each draft
     was drawn from, in the order of the requests (tokens - requests rows where each has one); None where drafts were
     not drawn.  temperature: a number or float32 [requests], 0 for greedy requests.  A next token of -1: the row has
-    no token to draw.
+    no token to draw.  A request without tokens (or a step without any) accepts 0.
     """
     i = _gpu(target, "target")
     if target.dim() != 2:
@@ -885,6 +893,10 @@ def verify_drafts(target, tokens, batch, u_accept, u_next, draft_probs=None, tem
     _check(L.ocq_verify_drafts(t, t_stride, t_bf16, int(bool(probabilities)), d or None, d_stride, d_rows, d_bf16,
                                ids, ua, un, temps, temp, vocab, ref, acc, to, workspace.data_ptr(), workspace.numel(),
                                handle))
+    if rows == 0 or requests == 0:                  # the library has nothing to verify and writes nothing
+        with _in_order_of(stream, i):
+            accepted.zero_()
+            out.fill_(-1)
     return accepted, out
 
 
