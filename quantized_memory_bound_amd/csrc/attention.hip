@@ -485,7 +485,12 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   // Codes times their scales are exact in fp16, not all in bf16 with one
   // instruction less; q goes to fp16 after a power of two that brings the row's
   // largest value to 2^14 .. 2^15, which is exact down to 2^-28 of it (and off by
-  // at most 2^-40 of it below).  (Called while the first page ids are on their way.)
+  // at most 2^-39 of it below).  The factor c takes the power back, and k's unit, in
+  // one step: c times the unit alone may be past 32 bits where the product is not.
+  // It stays a normal number: a masked score is -inf, and 0 times it is none, nor is
+  // inf times a score of 0.  (Scores are below 2^36 here: a c of less than 2^-126
+  // makes them all 0 beside any other one, 2^-126 too.)  (Called while the first
+  // page ids are on their way.)
   auto q_to_f16 = [&](auto& to) {
     float f[G::QS][8], top = 0.0f;
 #pragma unroll
@@ -501,7 +506,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
     for (int s = 0; s < G::QS; ++s)
 #pragma unroll
       for (int j = 0; j < 8; ++j) to[s][j] = (_Float16)__builtin_ldexpf(f[s][j], up);
-    c = __builtin_ldexpf(c * a.c.k_unit, -up);
+    c = __builtin_ldexpf(c, __builtin_amdgcn_frexp_expf(a.c.k_unit) - 1 - up);
+    c = __builtin_amdgcn_fmed3f(c, 0x1p-126f, 0x1.fffffep127f);
   };
 
   // ---- loads: rows of this wave's part of its key group's stage.  V of a stage
