@@ -402,8 +402,8 @@ typedef struct {
  * max_new, max_kv: host bounds of the new tokens and of kv_lens of any
  * request.  Tokens past max_new of a request are not attended, nor are tokens
  * of no request: what out and lse hold for them is not defined.  max_kv only
- * shapes the split of the work (but see ocq_paged_attention for NVFP4 calls of many
- * rows).
+ * shapes the split of the work, but for NVFP4 calls of many rows (see
+ * ocq_paged_attention), which see no key past it.
  * counters_dev: uint32 [OCQ_ATTENTION_COUNTERS] for ocq_paged_attention and
  * ocq_verify_drafts (not read by the others): zeroed by the caller before the first call in that
  * call's order, zero again after every call; calls that share it must
@@ -471,7 +471,10 @@ ocq_status ocq_rope_append(const void* q_dev, int64_t q_token_stride, int64_t q_
  * window).  Over NVFP4 caches both products are of fp16 operands: q after a power of
  * two of each row, the probabilities rounded to fp16; but where max_new x heads /
  * kv_heads is 1024 or more the pages are widened to fp16 in the workspace first, if
- * those of max_kv tokens a request fit 1 GiB (keys past max_kv are then not read).
+ * those of max_kv tokens a request fit 1 GiB.  Of a request whose kv_lens is past
+ * max_kv, a bound that does not hold, such a call widens the first max_kv keys only:
+ * its tokens keep their places (what kv_lens says) and see of those keys what the
+ * mask leaves, out 0 and lse -inf where that is nothing.
  * Requests x kv heads x row tiles (of 16 to 128 of the max_new *
  * heads / kv_heads rows) are one launch of fewer than 2^32 lanes, 64 to 256 a
  * tile; beyond that: OCQ_ERR_UNSUPPORTED.  Scores, softmax statistics and sums are fp32; probabilities are

@@ -110,7 +110,8 @@ struct Geo {
   static constexpr int MINW = MINW_, NST = 2;
   static constexpr int D = D_, MT = MT_, WR = WR_, WK = WK_, TK = TK_;
   static constexpr bool KV8 = FMT_ == OCQ_CACHE_E4M3, KV4 = FMT_ == OCQ_CACHE_NVFP4;
-  static constexpr bool F16 = KV4 || FMT_ == kWidened;                  // operands of the products: fp16, or bf16
+  static constexpr bool WIDE = FMT_ == kWidened;                        // only keys below wide_keys are there
+  static constexpr bool F16 = KV4 || WIDE;                              // operands of the products: fp16, or bf16
   static constexpr int NW = WR * WK, THREADS = 64 * NW, ROWS = MT * WR;
   static constexpr int RB = KV4 ? D / 2 : KV8 ? D : 2 * D, CH = RB / 16;   // bytes and chunks of a row
   static constexpr int PART = TK * RB;                                  // K (or V) bytes of a key group's stage
@@ -456,6 +457,12 @@ __device__ __forceinline__ void put_part(const AttnArgs& a, size_t row, int d, i
   if (d == 0) __hip_atomic_store(a.part_lse + row, lse2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// The last key that rows up to place p_hi can see.
+template <class G>
+__device__ __forceinline__ int last_key(const AttnArgs& a, int p_hi) {
+  return G::WIDE && p_hi >= a.wide_keys ? a.wide_keys - 1 : p_hi;
+}
+
 template <class G>
 __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8_t* lds) {
   typedef typename Acc<G::MT>::T acc_t;
@@ -541,7 +548,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
   for (int i = 0; i < G::SI; ++i)
     s_part[i] = (q_row(G::QI + i) & page_mask) * a.c.s_token * SE + (G::KV4 ? lane % (G::SB / 4) * 4 : 0);
   const uint64_t zero = (uint64_t)g_zero;
-  const KeyRange range = key_range(p_lo, p_hi, a.window, a.sinks);
+  const KeyRange range = key_range(p_lo, last_key<G>(a, p_hi), a.window, a.sinks);
   uint64_t src[G::QI], s_src[G::SI + 1];   // rows of the last K stage issued
   bool there[G::QI], s_there[G::SI + 1];
   // Page ids come with the K stage AHEAD before the one that they are for: a
@@ -700,14 +707,15 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Piece& pc, uint8
           for (int i = 0; i < 4; ++i) s[kt][4 * i4 + i] *= ks[i];
         }
     }
-    if (key0 + G::TK - 1 > p_lo || (a.window > 0 && key0 <= p_hi - a.window)) {
+    if (key0 + G::TK - 1 > p_lo || (a.window > 0 && key0 <= p_hi - a.window) || (G::WIDE && key0 + G::TK > a.wide_keys)) {
       asm volatile("");   // a branch, not selects in every stage
 #pragma unroll
       for (int kt = 0; kt < G::NKT; ++kt)
 #pragma unroll
         for (int i = 0; i < AN; ++i) {
           const int j = key0 + kt * G::MT + 8 * (i >> 2) + 4 * g + (i & 3);
-          s[kt][i] = key_seen(j, place, a.window, a.sinks) ? s[kt][i] : -__builtin_inff();
+          const bool seen = key_seen(j, place, a.window, a.sinks) && (!G::WIDE || j < a.wide_keys);
+          s[kt][i] = seen ? s[kt][i] : -__builtin_inff();
         }
     }
   };
@@ -1090,7 +1098,8 @@ __global__ __launch_bounds__(G::THREADS, G::MINW) void k_attn(AttnArgs a) {
   const int last_row = (pc.row0 + G::ROWS < pc.n * a.group ? pc.row0 + G::ROWS : pc.n * a.group) - 1;
   pc.p_lo = pc.base + pc.row0 / a.group;
   pc.p_hi = pc.base + last_row / a.group;
-  pc.tiles = key_tiles(pc.p_lo, pc.p_hi, a.window, a.sinks, G::TT);
+  if constexpr (G::WIDE) pc.kv = pc.kv < a.wide_keys ? pc.kv : a.wide_keys;   // (rows keep their places)
+  pc.tiles = key_tiles(pc.p_lo, last_key<G>(a, pc.p_hi), a.window, a.sinks, G::TT);
   const int per = (pc.tiles.total + a.splits - 1) / a.splits;
   pc.s0 = split * per < pc.tiles.total ? split * per : pc.tiles.total;
   pc.s1 = pc.s0 + per < pc.tiles.total ? pc.s0 + per : pc.tiles.total;
@@ -1142,7 +1151,7 @@ __global__ __launch_bounds__(256) void k_widen(AttnArgs a) {
   const int req = blockIdx.x / a.wide_pages, j = blockIdx.x % a.wide_pages;
   if (threadIdx.x == 0 && blockIdx.y == 0) a.wide_table[blockIdx.x] = blockIdx.x;
   const Span span = token_span(a.b.q_start, req, a.b.tokens);
-  const int kv = kv_bound(a.b.kv_lens[req], a.wide_pages, a.c.page_shift);
+  const int kv = kv_bound(a.b.kv_lens[req], a.b.max_pages, a.c.page_shift);
   const int page_size = 1 << a.c.page_shift, first = j << a.c.page_shift;
   if (span.n <= 0 || first >= kv) return;
   const KeyRange range = key_range(kv - span.n, kv - 1, a.window, a.sinks);
@@ -1281,7 +1290,7 @@ int launch_attn(const AttnArgs& codes, void* stream) {
                     (uint32_t)page, (uint32_t)row, 0, 0, a.b.requests * a.wide_pages, codes.c.page_shift, codes.c.kv_heads,
                     codes.c.k_unit, codes.c.v_unit};
     a.b.table = codes.wide_table;
-    a.b.table_stride = a.b.max_pages = a.wide_pages;
+    a.b.table_stride = a.wide_pages;
   }
   return (int)visit(a.dim, a.format, (int64_t)a.max_new * a.group,
                     [&](auto geo) { return run<decltype(geo)>(a, st); });

@@ -79,6 +79,7 @@ struct AttnArgs {
   uint8_t* wide;
   int32_t* wide_table;
   int wide_pages;
+  int wide_keys;             // keys of a request that these pages hold, max_kv at most
 };
 
 // The values that an E4M3 or NVFP4 cache stands for, [pages][kv_heads][page_size][dim] bf16.

@@ -176,6 +176,8 @@ ocq_status ocq_paged_attention(const void* q_dev, int64_t q_token_stride, int64_
   if (call.wide) {
     a.wide = (uint8_t*)workspace_dev;
     a.wide_pages = call.wide;
+    const int64_t held = (int64_t)call.wide * cache->page_size;
+    a.wide_keys = held < batch->max_kv ? (int)held : batch->max_kv;
     a.wide_table = (int32_t*)(a.wide + wide_bytes(batch->requests, call.wide, cache->page_size, cache->kv_heads,
                                                   cache->head_dim) - (int64_t)4 * batch->requests * call.wide);
   }

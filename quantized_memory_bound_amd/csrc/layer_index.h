@@ -30,22 +30,24 @@ OCQ_HD int kv_bound(int kv, int max_pages, int page_shift) {
 }
 
 // Tiles of TT keys that rows at places p_lo .. p_hi can see: those of the
-// first `sinks` tokens, then from the first row's window to the last row's
-// place.  Tile t of the `total` starts at key tile_of(t) * TT.
+// first `sinks` tokens, then from the first row's window to p_hi (the last row's
+// place, or the last key that is there).  Tile t of the `total` starts at key
+// tile_of(t) * TT.
 struct KeyTiles {
   int lo_tile, sink_tiles, total;
 };
 OCQ_HD KeyTiles key_tiles(int p_lo, int p_hi, int window, int sinks, int TT) {
   KeyTiles k{0, 0, 0};
   if (p_hi < 0) return k;
+  const int end = p_hi / TT + 1;
   if (window > 0 && p_lo >= window) {
     const int lo = p_lo - window + 1;
-    k.lo_tile = lo / TT;
+    k.lo_tile = lo / TT < end ? lo / TT : end;
     const int s = sinks < lo ? sinks : lo;
     k.sink_tiles = s / TT + (s % TT != 0);
     if (k.sink_tiles > k.lo_tile) k.sink_tiles = k.lo_tile;
   }
-  k.total = k.sink_tiles + p_hi / TT + 1 - k.lo_tile;
+  k.total = k.sink_tiles + end - k.lo_tile;
   return k;
 }
 OCQ_HD int tile_of(const KeyTiles& k, int t) { return t < k.sink_tiles ? t : t - k.sink_tiles + k.lo_tile; }

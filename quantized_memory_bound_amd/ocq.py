@@ -624,7 +624,9 @@ class TokenBatch:
 
     q_start int32 [requests + 1], kv_lens int32 [requests], page_table int32 [requests, max_pages] (its rows max_pages
     entries or more apart): CUDA tensors whose contents may change between calls.  tokens (the rows of q), max_new and
-    max_kv are host numbers: bounds of the new tokens and of kv_lens of any request.
+    max_kv are host numbers: bounds of the new tokens and of kv_lens of any request.  (Attention over an NVFP4 cache with
+    1024 rows a kv head or more sees no key past max_kv: a batch that is kept while its contexts grow needs a max_kv for
+    the longest of them.)
 
     Attention calls over one batch (and verify_drafts) count their finished work in memory of the batch, 0 between calls, apart for every
     stream that they run on.  A captured call counts where calls on the stream that the batch was made on do: its replays
