@@ -512,7 +512,7 @@ ocq_status ocq_cache_values(const ocq_kv_cache* cache, void* k_out_dev, void* v_
  * and all before it do.  At the first that does not, the next token is drawn from w
  * = max(p - q, 0) (p where that is 0 throughout), after the last one from w = p: the
  * lowest j with sum_{i <= j} w_i > u_next[r] sum_i w_i.  Sums and exponentials of
- * that row are 64-bit; the normalization of an acceptance's p is within 2^-20.
+ * that row are 64-bit; the normalization of an acceptance's p is within 2^-19.
  *   accepted[r]            drafts that stay (0 for a request without tokens beside
  *                          others that have some)
  *   out[t0 .. t0 + n - 1]  those drafts, the next token, then -1; -1 too in rows

@@ -1,4 +1,10 @@
-"""Draft verification and step tables at their ends: steps without tokens."""
+"""Draft verification and step tables at their ends: steps without tokens, acceptances next to their border.
+
+An acceptance compares u q(x) with p(x) = e_x / Z in 64 bits but for Z, whose exponentials are 32-bit: the kernel's bound of
+its error is 2^-19 (subtraction, product with log2(e) / T and that factor's own rounding, 2^-24 each of an exponent whose
+weighted mean over a lane's n <= 2^16 elements is below 8.1, Lambert's W of n / e; 2^-23 of the exponential, 3 2^-24 of a sum
+of eight: 30 2^-24).  Decisions further than that from the border are certain: they are asked for at 1.05 2^-19.
+"""
 
 import numpy as np
 import pytest
@@ -61,3 +67,47 @@ def test_drafts_of_rows_without_requests():
         a, out = ocq.verify_drafts(torch.zeros((3, 50), device=DEV), _ints([1, 2, 3]), _batch([]), torch.rand(3, device=DEV),
                                    empty, **kw)
         assert a.shape == (0,) and out.tolist() == [-1, -1, -1]
+
+
+def _rows(kind, vocab, rows, gen):
+    if kind == "tail":      # a maximum for each of 256 lanes, all else below half a last place of what is summed
+        x = torch.full((rows, vocab), -18.75, device=DEV)
+        x[:, :2048:8] = 0.0
+        return x
+    if kind == "rising":    # every lane's maximum moves with every vector
+        return torch.linspace(-30.0, 0.0, vocab, device=DEV).expand(rows, -1) + torch.arange(rows, device=DEV)[:, None] * 0.37
+    if kind == "flat":      # the weighted mean of the exponent is large: many unlikely ones beside one likely one
+        x = torch.randn((rows, vocab), device=DEV, generator=gen) * 0.5
+        x[:, vocab // 3] = 8.0
+        return x
+    return torch.randn((rows, vocab), device=DEV, generator=gen) * 3
+
+
+@pytest.mark.parametrize("kind", ["tail", "rising", "flat", "random"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab,requests", [(131072, 400), (131072, 8), (50001, 400)])
+def test_acceptances_next_to_their_border(kind, dtype, vocab, requests):
+    """Two rows a request; u just below and just above the draft's probability, from one workgroup a row to many."""
+    gen = torch.Generator(DEV).manual_seed(len(kind))
+    some = min(8, requests)
+    for temp in (1.0, 0.7):
+        logits = _rows(kind, vocab, some, gen).to(dtype)
+        p = torch.softmax(logits.double() * (1.0 / float(np.float32(temp))), -1)
+        top = p.topk(40, -1).indices
+        x = top[torch.arange(some, device=DEV), torch.randint(0, 40, (some,), device=DEV, generator=gen)]
+        if kind == "tail":
+            x = torch.arange(some, device=DEV) * 8
+        px = p[torch.arange(some, device=DEV), x].cpu().numpy()
+        assert (px < 0.999).all()
+        of = torch.arange(requests, device=DEV) % some
+        below = np.arange(requests) // some % 2 == 0
+        u = px[of.cpu().numpy()] * np.where(below, 1 - 1.05 * 2.0 ** -19, 1 + 1.05 * 2.0 ** -19)
+        ids = torch.zeros((requests, 2), dtype=torch.int32, device=DEV)
+        ids[:, 1] = x[of].to(torch.int32)
+        ua = torch.zeros((requests, 2), device=DEV)
+        ua[:, 0] = torch.from_numpy(u.astype(np.float32)).to(DEV)
+        target = logits[of].repeat_interleave(2, 0)
+        a, out = ocq.verify_drafts(target, ids.flatten(), _batch([2] * requests), ua.flatten(),
+                                   torch.rand(requests, device=DEV, generator=gen), temperature=temp)
+        assert a.tolist() == below.astype(int).tolist()
+        assert (out.view(-1, 2)[:, 0][torch.from_numpy(below).to(DEV)] == ids[:, 1][torch.from_numpy(below).to(DEV)]).all()
