@@ -576,7 +576,8 @@ typedef struct {
  * without a page), positions int32 (its place in the request), requests int32; each
  * and missing nullable.
  * before and after may be the same; they share the page table and the ring, which
- * are changed in place.  No output may overlap news or accepted. */
+ * are changed in place.  No output may overlap news or accepted. Tables without
+ * requests: OCQ_OK, nothing is launched or written. */
 size_t ocq_step_tables_workspace_bytes(const ocq_page_tables* tables, int tokens);
 ocq_status ocq_step_tables(const ocq_page_tables* before, const ocq_page_tables* after, const void* news_dev,
                            const void* accepted_dev, int tokens, void* slots_dev, void* positions_dev,

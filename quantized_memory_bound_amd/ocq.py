@@ -977,6 +977,17 @@ def step_tables(tables, news, tokens, accepted=None, out=None, slots=None, posit
         missing = _empty(1, int32, i, stream)
     to = (_vector(slots, "slots", _torch.int64, i, tokens), _vector(positions, "positions", int32, i, tokens),
           _vector(requests, "requests", int32, i, tokens), _vector(missing, "missing", int32, i, 1))
+    if n == 0:                                      # the library has nothing to step and writes nothing
+        if after.requests or after.ring.data_ptr() != tables.ring.data_ptr() or after.ring.shape != tables.ring.shape:
+            raise OcqError(ERR_INVALID_ARG, "tables and out share one page table and one ring, and their sizes")
+        with _in_order_of(stream, i):
+            for t in (slots, positions, requests):
+                t.fill_(-1)
+            missing.zero_()
+            after.q_start.zero_()
+            if after is not tables:
+                after.counts.copy_(tables.counts)
+        return slots, positions, requests, missing
     L = lib()
     if workspace is None:
         need = L.ocq_step_tables_workspace_bytes(tables.ref, tokens)

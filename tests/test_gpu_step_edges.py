@@ -1,4 +1,5 @@
-"""Draft verification and step tables at their ends: steps without tokens, acceptances next to their border.
+"""Draft verification and step tables at their ends: steps without tokens, acceptances next to their border, tables without
+requests.
 
 An acceptance compares u q(x) with p(x) = e_x / Z in 64 bits but for Z, whose exponentials are 32-bit: the kernel's bound of
 its error is 2^-19 (subtraction, product with log2(e) / T and that factor's own rounding, 2^-24 each of an exponent whose
@@ -111,3 +112,33 @@ def test_acceptances_next_to_their_border(kind, dtype, vocab, requests):
                                    torch.rand(requests, device=DEV, generator=gen), temperature=temp)
         assert a.tolist() == below.astype(int).tolist()
         assert (out.view(-1, 2)[:, 0][torch.from_numpy(below).to(DEV)] == ids[:, 1][torch.from_numpy(below).to(DEV)]).all()
+
+
+# ---------------------------------------------------------------- tables
+
+@pytest.mark.parametrize("tokens", [0, 5, 40000])
+@pytest.mark.parametrize("apart", [False, True])
+def test_tables_without_requests(tokens, apart):
+    """All rows are behind the last request; nothing lacks; the ring's counts go on."""
+    def tables(counts):
+        none = torch.zeros(0, dtype=torch.int32, device=DEV)
+        return ocq.PageTables(_ints([7]), none, none, torch.tensor(counts, device=DEV), table, ring, 16)
+    table, ring = torch.zeros((0, 4), dtype=torch.int32, device=DEV), _ints([0, 1, 2])
+    before = tables([4, 6])
+    after = tables([0, 0]) if apart else None
+    outs = (torch.full((tokens,), 8, dtype=torch.int64, device=DEV), torch.full((tokens,), 8, dtype=torch.int32, device=DEV),
+            torch.full((tokens,), 8, dtype=torch.int32, device=DEV), _ints([8]))
+    got = ocq.step_tables(before, _ints([]), tokens, out=after, slots=outs[0], positions=outs[1], requests=outs[2],
+                          missing=outs[3])
+    assert all(a is b for a, b in zip(got, outs)) and all((t == -1).all() for t in got[:3]) and got[3].tolist() == [0]
+    after = after or before
+    assert after.q_start.tolist() == [0] and after.counts.tolist() == [4, 6] and ring.tolist() == [0, 1, 2]
+
+
+def test_tables_without_requests_and_others_do_not_go_together():
+    none, three = ocq.PageTables.allocate(0, 4, 12, 16, device=DEV), ocq.PageTables.allocate(3, 4, 12, 16, device=DEV)
+    for before, after, news in ((none, three, _ints([])), (none, ocq.PageTables.allocate(0, 4, 12, 16, device=DEV), _ints([])),
+                                (three, none, _ints([1, 1, 1]))):
+        with pytest.raises(ocq.OcqError) as e:
+            ocq.step_tables(before, news, 3, out=after)
+        assert e.value.status == ocq.ERR_INVALID_ARG
