@@ -569,8 +569,9 @@ typedef struct {
  *     order of the requests, what it no longer needs goes back there (and can be
  *     taken in the next call; its entries stay in the table, unused)
  * Where the ring has too few pages, or max_pages is too small, missing[0] counts
- * those that lack, their entries in the table are -1 and held' counts the others:
- * appended tokens without a page are dropped, and the next call tries again.
+ * those that lack (at most 2^31 - 1), their entries in the table are -1 and held'
+ * counts the others: appended tokens without a page are dropped, and the next call
+ * tries again.
  * Per new token, in the order of the token axis (tokens rows, at least the sum of
  * news; -1 in rows behind it): slots int64 (page * page_size + row in the page, -1
  * without a page), positions int32 (its place in the request), requests int32; each

@@ -94,6 +94,7 @@ __device__ __forceinline__ int last_le(const int* s, int n, int v) {
 template <bool SMALL>
 __global__ __launch_bounds__(kWide) void k_sums(TableArgs a) {
   __shared__ int s_sum[3][16], s_prev;
+  __shared__ unsigned long long s_over;
   __shared__ int s_start[SMALL ? kWide : 1], s_take[SMALL ? kWide : 1], s_give[SMALL ? kWide : 1];
   __shared__ Rec s_rec[SMALL ? kWide : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -101,7 +102,9 @@ __global__ __launch_bounds__(kWide) void k_sums(TableArgs a) {
   const uint64_t span = given - taken, size = (uint64_t)a.ring_size;
   const int from = (int)(taken % size), to = (int)(given % size);   // where entries come from and go to
   const int free = (int64_t)span < 0 ? 0 : span > (uint64_t)a.ring_size ? a.ring_size : (int)span;
-  int c_new = 0, c_want = 0, c_back = 0, over = 0;
+  int c_new = 0, c_want = 0, c_back = 0;
+  int64_t over = 0;
+  if (threadIdx.x == 0) s_over = 0;
   for (int base = 0; base < a.requests; base += kWide) {
     const int r = base + threadIdx.x;
     const bool in = r < a.requests;
@@ -129,7 +132,7 @@ __global__ __launch_bounds__(kWide) void k_sums(TableArgs a) {
     const int need = pages < a.max_pages ? (int)pages : a.max_pages;
     const int want = need > held ? need - held : 0, back = held > need ? held - need : 0;
     int v[3] = {in ? fresh : 0, in ? want : 0, in ? back : 0}, sum[3];
-    if (in) over += (int)(pages - need);
+    if (in) over += pages - need;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       sum[k] = wave_scan(v[k]);
@@ -165,14 +168,13 @@ __global__ __launch_bounds__(kWide) void k_sums(TableArgs a) {
     c_back += all[2];
     __syncthreads();
   }
-  // pages beyond the table's rows are missing as well
-  over = wave_scan(over);
-  if (lane == 63) s_sum[0][wave] = over;
+  // pages beyond the table's rows are missing as well (few requests have any; all of
+  // them may be more than an int holds)
+  if (over) atomicAdd(&s_over, (unsigned long long)over);
   __syncthreads();
   if (threadIdx.x == 0) {
-    int64_t missing = c_want > free ? c_want - free : 0;
-    for (int w = 0; w < 16; ++w) missing += s_sum[0][w];
-    if (a.missing) a.missing[0] = (int)missing;
+    const int64_t missing = (int64_t)s_over + (c_want > free ? c_want - free : 0);
+    if (a.missing) a.missing[0] = missing < 0x7FFFFFFF ? (int)missing : 0x7FFFFFFF;
     a.counts_out[0] = (int64_t)(taken + (uint64_t)(c_want < free ? c_want : free));
     a.counts_out[1] = (int64_t)(given + (uint64_t)c_back);
     if constexpr (!SMALL) {

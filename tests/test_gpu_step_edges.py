@@ -1,5 +1,5 @@
 """Draft verification and step tables at their ends: steps without tokens, acceptances next to their border, tables without
-requests.
+requests or with far too few pages.
 
 An acceptance compares u q(x) with p(x) = e_x / Z in 64 bits but for Z, whose exponentials are 32-bit: the kernel's bound of
 its error is 2^-19 (subtraction, product with log2(e) / T and that factor's own rounding, 2^-24 each of an exponent whose
@@ -142,3 +142,17 @@ def test_tables_without_requests_and_others_do_not_go_together():
         with pytest.raises(ocq.OcqError) as e:
             ocq.step_tables(before, news, 3, out=after)
         assert e.value.status == ocq.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("requests", [3, 1500])
+def test_tables_that_lack_more_pages_than_a_number_holds(requests):
+    """Lengths of nearly 2^31 in rows of four pages: what is missing stops at the largest int32."""
+    t = ocq.PageTables.allocate(requests, 4, 12, 1, device=DEV)
+    t.kv_lens.fill_(2 ** 31 - 1)
+    missing = ocq.step_tables(t, torch.zeros(requests, dtype=torch.int32, device=DEV), 8)[3]
+    assert missing.tolist() == [2 ** 31 - 1]
+    assert t.kv_lens.tolist() == [2 ** 31 - 1] * requests and t.counts.tolist() == [12, 12]
+    assert t.page_table[:3].tolist() == [[0, 1, 2, 3], [4, 5, 6, 7], [8, 9, 10, 11]]
+    one = ocq.PageTables.allocate(1, 4, 12, 1, device=DEV)
+    one.kv_lens.fill_(2 ** 31 - 1)
+    assert ocq.step_tables(one, _ints([0]), 8)[3].tolist() == [2 ** 31 - 1 - 4]
