@@ -548,7 +548,8 @@ ocq_status ocq_verify_drafts(const void* target_dev, int64_t target_stride, int 
  * int32 [ring_size]: page ids, free ones at places counts[0] .. counts[1] - 1 modulo
  * ring_size; counts_dev int64 [2]: entries ever taken out and put in.  ring_size is
  * at least the number of pages in all.  page_size a power of two up to 1024,
- * max_pages * page_size below 2^31, up to 65536 requests. */
+ * max_pages up to 2^30, max_pages * page_size and requests * max_pages below 2^31, up
+ * to 65536 requests. */
 typedef struct {
   void* q_start_dev;
   void* kv_lens_dev;
@@ -573,7 +574,7 @@ typedef struct {
  * counts the others: appended tokens without a page are dropped, and the next call
  * tries again.
  * Per new token, in the order of the token axis (tokens rows, at least the sum of
- * news; -1 in rows behind it): slots int64 (page * page_size + row in the page, -1
+ * news, up to 2^30; -1 in rows behind it): slots int64 (page * page_size + row in the page, -1
  * without a page), positions int32 (its place in the request), requests int32; each
  * and missing nullable.
  * before and after may be the same; they share the page table and the ring, which

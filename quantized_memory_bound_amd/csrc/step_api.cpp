@@ -29,6 +29,10 @@ ocq_status check_tables(const ocq_page_tables* t) {
     return unsupported("page_size must be a power of two in [1, 1024]");
   if (t->max_pages < 1 || (int64_t)t->max_pages * t->page_size >= (int64_t)1 << 31)
     return unsupported("max_pages * page_size must be in [1, 2^31)");
+  // (a lane's next page is up to 2^14 places on, in 32 bits; so are the sums over the
+  // requests of the pages that they take and give: past that two would get one page)
+  if (t->max_pages > 1 << 30) return unsupported("at most 2^30 pages a request");
+  if ((int64_t)t->requests * t->max_pages >= (int64_t)1 << 31) return unsupported("requests * max_pages must be below 2^31");
   if (t->ring_size < 1) return invalid("ring_size must be positive");
   if (!stride_ok(t->table_stride, 1) || t->table_stride < t->max_pages)
     return invalid("table_stride must be at least max_pages");
@@ -128,7 +132,7 @@ ocq_status ocq_verify_drafts(const void* target_dev, int64_t target_stride, int 
 
 size_t ocq_step_tables_workspace_bytes(const ocq_page_tables* tables, int tokens) {
   set_error(OCQ_OK, "");
-  if (check_tables(tables) != OCQ_OK || tokens < 0) return 0;
+  if (check_tables(tables) != OCQ_OK || tokens < 0 || tokens > 1 << 30) return 0;
   return table_workspace(tables->requests, tokens, tables->max_pages);
 }
 
@@ -147,6 +151,8 @@ ocq_status ocq_step_tables(const ocq_page_tables* before, const ocq_page_tables*
       before->page_size != after->page_size)
     return invalid("before and after share one page table and one ring, and their sizes");
   if (tokens < 0) return invalid("tokens must not be negative");
+  // (a lane's next token is up to 2^16 places on, in 32 bits)
+  if (tokens > 1 << 30) return unsupported("at most 2^30 tokens");
   if (before->requests == 0) return OCQ_OK;
   if (!news_dev) return invalid("null device pointer");
   const void* ptrs[] = {news_dev, accepted_dev, positions_dev, requests_dev, missing_dev};
