@@ -59,13 +59,15 @@ class VerifyLoop:
     layer: a VerifyLayer; embed: bf16 [vocab, hidden]; head: bf16 [hidden, vocab]; tables: ocq.PageTables of empty
     requests over the layer's cache; drafts: drafted tokens a request and step; max_kv: a host bound of any request's
     tokens in the cache.  The draft model is the embedding and the head without the layer: each draft is drawn from
-    softmax(embed[token before] head / temperature).
+    softmax(embed[token before] head / temperature), or is its largest logit where temperature, a number, is 0.
     """
 
     def __init__(self, layer, embed, head, tables, drafts, max_kv, temperature=1.0, seed=0):
         import torch
         self.layer, self.embed, self.head, self.tables = layer, embed, head, tables
-        self.drafts, self.max_kv, self.temperature = drafts, max_kv, temperature
+        self.drafts, self.max_kv, self.temperature = drafts, max_kv, float(temperature)
+        if not 0 <= self.temperature < float("inf"):
+            raise ocq.OcqError(ocq.ERR_INVALID_ARG, "temperature must be finite and not negative, got %g" % self.temperature)
         dev, requests = tables.device, tables.requests
         self.gen = torch.Generator(dev).manual_seed(seed)
         self.batch = ocq.TokenBatch(tables.q_start, tables.kv_lens, tables.page_table, 1 + drafts, max_kv,
@@ -98,6 +100,9 @@ class VerifyLoop:
         ids, probs = [self.last], []
         for _ in range(self.drafts):
             logits = (self.embed[ids[-1]] @ self.head).float()
+            if self.temperature == 0:             # not drawn: no probabilities to compare with
+                ids.append(logits.argmax(-1).to(torch.int32))
+                continue
             probs.append(torch.softmax(logits / self.temperature, -1))
             ids.append((probs[-1] / -torch.log(rand(requests, vocab).clamp(min=1e-30))).argmax(-1).to(torch.int32))
         ids = torch.stack(ids, 1).flatten()
