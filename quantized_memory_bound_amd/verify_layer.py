@@ -60,6 +60,9 @@ class VerifyLoop:
     requests over the layer's cache; drafts: drafted tokens a request and step; max_kv: a host bound of any request's
     tokens in the cache.  The draft model is the embedding and the head without the layer: each draft is drawn from
     softmax(embed[token before] head / temperature), or is its largest logit where temperature, a number, is 0.
+
+    missing: int64 [1], the pages that steps lacked, summed over them (tokens without a page are lost to the steps that
+    follow; the host looks at it when it likes).
     """
 
     def __init__(self, layer, embed, head, tables, drafts, max_kv, temperature=1.0, seed=0):
@@ -76,17 +79,23 @@ class VerifyLoop:
         self.first = torch.arange(requests, device=dev) * (1 + drafts)
         self.accepted = None          # all of the prompt's tokens stay
         self.last = None
+        self.missing = torch.zeros(1, dtype=torch.int64, device=dev)
 
     def prefill(self, prompts, chunk=512):
-        """prompts: int [requests, length]; all but their last tokens go into the cache."""
+        """prompts: int [requests, length]; all but their last tokens go into the cache.  Raises where it has not enough
+        pages for them (this waits for the GPU; the loop's cache then holds a part of the prompts)."""
         import torch
         requests, length = prompts.shape
+        lacking = torch.zeros_like(self.missing)
         for at in range(0, length - 1, chunk):
             ids = prompts[:, at: min(at + chunk, length - 1)]
             n = ids.shape[1]
-            ocq.step_tables(self.tables, torch.full_like(self.news, n), requests * n)
+            lacking += ocq.step_tables(self.tables, torch.full_like(self.news, n), requests * n)[3]
             batch = ocq.TokenBatch(self.tables.q_start, self.tables.kv_lens, self.tables.page_table, n, at + n)
             self.layer(self.embed[ids.flatten()], None, batch)
+        if int(lacking):
+            raise ocq.OcqError(ocq.ERR_BUFFER_TOO_SMALL, "prompts of %d tokens: the cache has too few pages for them, or "
+                               "max_pages is too small" % length)
         self.last, self.accepted = prompts[:, -1].to(torch.int32), None
 
     def step(self):
@@ -106,7 +115,7 @@ class VerifyLoop:
             probs.append(torch.softmax(logits / self.temperature, -1))
             ids.append((probs[-1] / -torch.log(rand(requests, vocab).clamp(min=1e-30))).argmax(-1).to(torch.int32))
         ids = torch.stack(ids, 1).flatten()
-        _, _, _, self.missing = ocq.step_tables(self.tables, self.news, len(ids), accepted=self.accepted)
+        self.missing += ocq.step_tables(self.tables, self.news, len(ids), accepted=self.accepted)[3]
         x, pending = self.layer(self.embed[ids], None, self.batch)
         self.accepted, out = ocq.verify_drafts((x + pending) @ self.head, ids, self.batch, rand(len(ids)), rand(requests),
                                                draft_probs=torch.stack(probs, 1).flatten(0, 1) if probs else None,

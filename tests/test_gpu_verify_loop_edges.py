@@ -1,4 +1,4 @@
-"""Whole verify steps at their ends: temperature 0."""
+"""Whole verify steps at their ends: temperature 0, prompts and steps that do not fit."""
 
 import pytest
 import torch
@@ -51,3 +51,23 @@ def test_temperatures_that_are_none(temperature):
     with pytest.raises(ocq.OcqError) as e:
         _loop(1, 1, 4, temperature=temperature)
     assert e.value.status == ocq.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("per,pages,length", [(4, 8, 66), (4, 7, 64), (2, 99, 100)])
+def test_prompts_that_do_not_fit_are_refused(per, pages, length):
+    """Too few entries in the table, too few pages in the ring."""
+    loop, gen = _loop(2, 2, per, pages=pages)
+    with pytest.raises(ocq.OcqError) as e:
+        loop.prefill(_prompts(2, length, gen), chunk=17)
+    assert e.value.status == ocq.ERR_BUFFER_TOO_SMALL
+
+
+def test_steps_that_lack_pages_are_counted():
+    loop, gen = _loop(1, 3, 2)
+    loop.prefill(_prompts(1, 30, gen))
+    for _ in range(4):
+        loop.step()
+    lacking = int(loop.missing)
+    assert lacking > 0
+    loop.step()
+    assert int(loop.missing) > lacking
