@@ -82,21 +82,23 @@ class VerifyLoop:
         self.missing = torch.zeros(1, dtype=torch.int64, device=dev)
 
     def prefill(self, prompts, chunk=512):
-        """prompts: int [requests, length]; all but their last tokens go into the cache.  Raises where it has not enough
-        pages for them (this waits for the GPU; the loop's cache then holds a part of the prompts)."""
+        """prompts: int [requests, length]; all but their last tokens go into the cache, behind what steps before have
+        left there (the token that such a step ended with, `last`, is not in it yet).  Raises where the cache has not
+        enough pages for them (this waits for the GPU; it then holds a part of the prompts)."""
         import torch
         requests, length = prompts.shape
         lacking = torch.zeros_like(self.missing)
         for at in range(0, length - 1, chunk):
             ids = prompts[:, at: min(at + chunk, length - 1)]
             n = ids.shape[1]
-            lacking += ocq.step_tables(self.tables, torch.full_like(self.news, n), requests * n)[3]
+            lacking += ocq.step_tables(self.tables, torch.full_like(self.news, n), requests * n, accepted=self.accepted)[3]
+            self.accepted = None
             batch = ocq.TokenBatch(self.tables.q_start, self.tables.kv_lens, self.tables.page_table, n, at + n)
             self.layer(self.embed[ids.flatten()], None, batch)
         if int(lacking):
             raise ocq.OcqError(ocq.ERR_BUFFER_TOO_SMALL, "prompts of %d tokens: the cache has too few pages for them, or "
                                "max_pages is too small" % length)
-        self.last, self.accepted = prompts[:, -1].to(torch.int32), None
+        self.last = prompts[:, -1].to(torch.int32)
 
     def step(self):
         """One verify step: (accepted int32 [requests], out int32 [requests, 1 + drafts], each request's accepted

@@ -1,4 +1,5 @@
-"""Whole verify steps at their ends: temperature 0, prompts and steps that do not fit."""
+"""Whole verify steps at their ends: temperature 0, prompts and steps that do not fit, prompts after
+steps."""
 
 import pytest
 import torch
@@ -71,3 +72,38 @@ def test_steps_that_lack_pages_are_counted():
     assert lacking > 0
     loop.step()
     assert int(loop.missing) > lacking
+
+
+def test_prompts_after_steps():
+    """A prompt that begins with the loop's last tokens goes behind what was accepted: the cache is that of a loop which was
+    given all of these tokens at once."""
+    loop, gen = _loop(2, 4, 12)
+    prompts = _prompts(2, 20, gen)
+    loop.prefill(prompts)
+    text = [p.tolist() for p in prompts]
+    for _ in range(3):
+        _, out = loop.step()
+        for r in range(2):
+            text[r] += [t for t in out[r].tolist() if t >= 0]
+    more = _prompts(2, 9, gen)
+    lens = [len(t) for t in text]
+    loop.prefill(torch.cat([loop.last[:, None], more], 1))
+    assert loop.tables.kv_lens.tolist() == [n + 8 for n in lens]
+    assert loop.last.tolist() == more[:, -1].tolist()
+    for r in range(2):
+        other, _ = _loop(1, 4, 12)
+        whole = torch.tensor([text[r]], device=DEV)
+        other.prefill(torch.cat([whole, more[r:r + 1]], 1))
+        for mine, its in ((loop.layer.cache.k, other.layer.cache.k), (loop.layer.cache.v, other.layer.cache.v)):
+            j = torch.arange(lens[r] + 8, device=DEV)
+            a = mine[loop.tables.page_table[r][j // 16].long(), :, j % 16].float()
+            b = its[other.tables.page_table[0][j // 16].long(), :, j % 16].float()
+            # (products of another number of rows may sum in another order: off by a rounding or two, other tokens by
+            # values of order one)
+            assert (a - b).abs().max() <= 2.0 ** -6 * b.abs().max()
+    loop.step()
+    # a prompt of one token changes nothing but the next step's token
+    kv, last = loop.tables.kv_lens.tolist(), loop.accepted.tolist()
+    loop.prefill(loop.last[:, None])
+    loop.step()
+    assert loop.tables.kv_lens.tolist() == [k - 5 + 1 + a + 5 for k, a in zip(kv, last)]
