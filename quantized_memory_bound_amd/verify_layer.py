@@ -102,13 +102,15 @@ class VerifyLoop:
 
     def step(self):
         """One verify step: (accepted int32 [requests], out int32 [requests, 1 + drafts], each request's accepted
-        drafts, the next token and -1)."""
+        drafts, the next token and -1).  A request whose next token was -1 (its logits are not numbers) has ended: it
+        takes part with token 0, of which nothing stays in the cache, and its row is -1, until the next prefill."""
         import torch
         requests, vocab = self.tables.requests, self.head.shape[1]
 
         def rand(*shape):
             return torch.rand(shape, device=self.last.device, generator=self.gen)
-        ids, probs = [self.last], []
+        ended = self.last < 0
+        ids, probs = [self.last.clamp(min=0)], []
         for _ in range(self.drafts):
             logits = (self.embed[ids[-1]] @ self.head).float()
             if self.temperature == 0:             # not drawn: no probabilities to compare with
@@ -119,11 +121,14 @@ class VerifyLoop:
         ids = torch.stack(ids, 1).flatten()
         self.missing += ocq.step_tables(self.tables, self.news, len(ids), accepted=self.accepted)[3]
         x, pending = self.layer(self.embed[ids], None, self.batch)
-        self.accepted, out = ocq.verify_drafts((x + pending) @ self.head, ids, self.batch, rand(len(ids)), rand(requests),
-                                               draft_probs=torch.stack(probs, 1).flatten(0, 1) if probs else None,
-                                               temperature=self.temperature)
-        self.last = out[self.first + self.accepted]
-        return self.accepted, out.view(requests, -1)
+        accepted, out = ocq.verify_drafts((x + pending) @ self.head, ids, self.batch, rand(len(ids)), rand(requests),
+                                          draft_probs=torch.stack(probs, 1).flatten(0, 1) if probs else None,
+                                          temperature=self.temperature)
+        out.view(requests, -1).masked_fill_(ended[:, None], -1)
+        accepted.masked_fill_(ended, 0)
+        self.last = out[self.first + accepted]
+        self.accepted = accepted - ended.to(torch.int32)     # -1: not even the first token stays
+        return accepted, out.view(requests, -1)
 
 
 def random_layer(hidden, inter, heads, kv_heads, head_dim, pages, page_size, e4m3=False, seed=0, device="cuda",

@@ -1,5 +1,5 @@
 """Whole verify steps at their ends: temperature 0, prompts and steps that do not fit, prompts after
-steps."""
+steps, rows without a next token."""
 
 import pytest
 import torch
@@ -107,3 +107,36 @@ def test_prompts_after_steps():
     loop.prefill(loop.last[:, None])
     loop.step()
     assert loop.tables.kv_lens.tolist() == [k - 5 + 1 + a + 5 for k, a in zip(kv, last)]
+
+
+@pytest.mark.parametrize("why", ["a NaN", "-1"])
+def test_requests_without_a_next_token_say_nothing_more(why):
+    """Their rows are -1 from then on, no more of them stays in the cache, and the other requests go on as if nothing had
+    happened; a new prompt takes them up again."""
+    runs = []
+    for bad in (False, True):
+        loop, gen = _loop(3, 4, 12)
+        prompts = _prompts(3, 20, gen).clamp(max=VOCAB - 2)
+        if bad and why == "a NaN":
+            loop.embed[VOCAB - 1] = float("nan")
+            prompts[1, -1] = VOCAB - 1
+        loop.prefill(prompts)
+        steps = []
+        for step in range(5):
+            accepted, out = loop.step()
+            if step == 0 and bad and why == "-1":
+                loop.last[1] = -1
+            steps.append((accepted.tolist(), out.tolist(), loop.tables.kv_lens.tolist()))
+        runs.append(steps)
+    for step, (a, b) in enumerate(zip(*runs)):
+        for r in (0, 2):
+            assert [x[r] for x in a] == [x[r] for x in b]
+        if step > 0 or why == "a NaN":
+            assert b[0][1] == 0 and b[1][1] == [-1] * 5
+    first = runs[1][0]
+    # (19 tokens of the prompt, its last one and what the first step accepted; 5 rows more during each step)
+    assert [s[2][1] for s in runs[1]] == [24] + [20 + first[0][1] + 5] * 4
+    loop.prefill(prompts.clamp(max=VOCAB - 2))
+    assert (loop.last >= 0).all() and loop.tables.kv_lens.tolist()[1] == 20 + first[0][1] + 19
+    if why == "-1":
+        assert (loop.step()[1][:, 0] >= 0).all()
