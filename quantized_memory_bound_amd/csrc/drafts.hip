@@ -650,6 +650,11 @@ __global__ __launch_bounds__(kThreads) void k_next(DraftArgs a) {
   } else {
     if (sp.n <= 0) return;
     c = a.choices[r];
+    // No workgroup of A has left it where q_start falls or changes, or counters were
+    // not 0: what is used as a place stays inside the request all the same.
+    c.t0 = sp.t0;
+    c.count = c.count < 0 ? 0 : c.count >= sp.n ? sp.n - 1 : c.count;
+    c.q_row = a.draft && c.q_row < a.draft_rows ? c.q_row : -1;
   }
   if (!c.draw) return;
   const float u = a.u_next[r];

@@ -114,6 +114,27 @@ def test_acceptances_next_to_their_border(kind, dtype, vocab, requests):
         assert (out.view(-1, 2)[:, 0][torch.from_numpy(below).to(DEV)] == ids[:, 1][torch.from_numpy(below).to(DEV)]).all()
 
 
+@pytest.mark.parametrize("start", [[0, 5, 3, 8], [0, 9, 2, 2], [-4, 90, 1, 7], [2 ** 31 - 1, -2 ** 31, 0, 8]])
+@pytest.mark.parametrize("draft", [False, True])
+def test_offsets_that_fall_write_nothing_elsewhere(start, draft):
+    """q_start that no step gives: the outputs are any, the memory beside them stays, whatever the workspace holds; so it
+    does where counters were left wrong by such a call."""
+    gen = torch.Generator(DEV).manual_seed(3)
+    target, ids = torch.randn((8, 3000), device=DEV, generator=gen), torch.randint(0, 3000, (8,), device=DEV, generator=gen)
+    q = torch.softmax(torch.randn((8, 3000), device=DEV, generator=gen), -1) if draft else None
+    one = torch.ones(3, dtype=torch.int32, device=DEV)
+    batch = ocq.TokenBatch(_ints(start), one, one[:, None], 8, 1)
+    for fill in (0x7F, 0x80, 0xFF, 0x01):
+        accepted, out = _ints([99] * 5), _ints([99] * 10)
+        workspace = torch.full((1 << 16,), fill, dtype=torch.uint8, device=DEV)
+        ocq.verify_drafts(target, ids.to(torch.int32), batch, torch.rand(8, device=DEV, generator=gen),
+                          torch.rand(3, device=DEV, generator=gen), draft_probs=q, accepted=accepted[1:-1], out=out[1:-1],
+                          workspace=workspace)
+        torch.cuda.synchronize()
+        assert accepted[[0, -1]].tolist() == [99, 99] and out[[0, -1]].tolist() == [99, 99]
+        assert (workspace[-(1 << 14):] == fill).all()
+
+
 # ---------------------------------------------------------------- tables
 
 @pytest.mark.parametrize("tokens", [0, 5, 40000])
