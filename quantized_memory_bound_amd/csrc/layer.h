@@ -102,7 +102,7 @@ struct AttnPlan {
 // convert for themselves keep the vector unit busy; widened once they cost a pass
 // through memory.  32 heads of 128 on 8 kv heads, two requests over up to 10007 keys,
 // us with and without: 512 rows a kv head 82 (67), 1024 113 (113), 2048 181 (187),
-// 8192 471-490 (573); 16 requests, 2048 rows over 700 keys 117 (113).
+// 8192 469-498 (573); 16 requests, 2048 rows over 700 keys 117 (113).
 constexpr int kWidened = 3;               // format of such a call's second launch
 constexpr int kWideRows = 1024;
 constexpr int64_t kWideBytes = (int64_t)1 << 30;
